@@ -121,15 +121,18 @@ SHARD = [w for w in WORKLOADS if w.endswith("_shard8")]
 
 HEADLINE = "fp32_8192"
 
-# Sources the GEMM kernels and their launch parameters are built from (the
-# probes and the allocation-free entry point's wrapper do not change them).
-_NOT_KERNEL_SOURCES = {"gemm_probe.hip", "gemm_noalloc.hip", "gemm_plan.hpp"}
+# Sources the dense GEMM kernels and their launch parameters are built from
+# (the probes, the allocation-free entry point's wrapper and the grouped and
+# adapter operators do not change them).
+_NOT_KERNEL_SOURCES = {"gemm_probe.hip", "gemm_noalloc.hip", "gemm_plan.hpp", "gemm_checks.hpp"}
+_NOT_KERNEL_PREFIXES = ("gemm_ragged", "gemm_lora", "gemm_skinny")
 
 
 def kernel_source_hash():
     h = hashlib.sha256()
     for p in sorted(glob.glob(os.path.join(ROOT, "dense_gemm_engineering_run_amd", "csrc", "*"))):
-        if os.path.basename(p) in _NOT_KERNEL_SOURCES:
+        name = os.path.basename(p)
+        if name in _NOT_KERNEL_SOURCES or name.startswith(_NOT_KERNEL_PREFIXES):
             continue
         with open(p, "rb") as f:
             h.update(os.path.basename(p).encode())

@@ -70,6 +70,11 @@ _lib.gemm_workspace_size.argtypes = [_i64, _i64, _i64, _chr, _chr, _chr, _int, _
 _lib.gemm_workspace_size.restype = _int
 _lib.gemm_run_config.argtypes = _RUN_ARGS + [_int]
 _lib.gemm_run_config.restype = _int
+_GROUPED_ARGS = _RUN_ARGS[:-1] + [_i64, _i64, _vp]
+_lib.gemm_run_grouped.argtypes = _GROUPED_ARGS + [_vp]
+_lib.gemm_run_grouped.restype = _int
+_lib.gemm_run_grouped_k.argtypes = _GROUPED_ARGS + [_int, _vp]
+_lib.gemm_run_grouped_k.restype = _int
 _lib.gemm_status_str.argtypes = [_int]
 _lib.gemm_status_str.restype = ctypes.c_char_p
 _lib.gemm_num_configs.argtypes = [_int]
@@ -162,6 +167,21 @@ def gemm_run_ex(M, N, K, a_major, b_major, c_major, dtype, A, B, C, lda, ldb, ld
     epi = ctypes.byref(epilogue) if epilogue is not None else None
     return _lib.gemm_run_ex(M, N, K, _c(a_major), _c(b_major), _c(c_major), dtype, A, B, C,
                             lda, ldb, ldc, epi, workspace, workspace_bytes, stream, config_id)
+
+
+def gemm_run_grouped(M, N, K, a_major, b_major, c_major, dtype, A, B, C, lda, ldb, ldc, groups,
+                     stride_b, ends, stream=0):
+    """C ABI gemm_run_grouped (rows of A and C by group). Returns the status."""
+    return _lib.gemm_run_grouped(M, N, K, _c(a_major), _c(b_major), _c(c_major), dtype, A, B, C,
+                                 lda, ldb, ldc, groups, stride_b, ends, stream)
+
+
+def gemm_run_grouped_k(M, N, K, a_major, b_major, c_major, dtype, A, B, C, lda, ldb, ldc, groups,
+                       stride_c, ends, accumulate=0, stream=0):
+    """C ABI gemm_run_grouped_k (k by group, one C per group). Returns the status."""
+    return _lib.gemm_run_grouped_k(M, N, K, _c(a_major), _c(b_major), _c(c_major), dtype, A, B, C,
+                                   lda, ldb, ldc, groups, stride_c, ends, int(bool(accumulate)),
+                                   stream)
 
 
 def gemm_workspace_size(M, N, K, a_major, b_major, c_major, dtype, config_id=-1):
@@ -261,6 +281,104 @@ def gemm(a, b, c, stream=None, config=None):
     st = gemm_run(*args) if config is None else gemm_run_config(*args, config)
     if st != GEMM_OK:
         raise GemmError(st)
+    return c
+
+
+def _ld(shape, stride, outer, inner):
+    """Leading dimension of a matrix whose dim `inner` is the contiguous one
+    (None when it is not).  With at most one row the stride says nothing: any
+    leading dimension will do, so one that keeps 16-byte loads."""
+    if shape[inner] > 1 and stride[inner] != 1:
+        return None
+    if shape[outer] <= 1:
+        return max(16, -(-shape[inner] // 16) * 16)
+    return stride[outer] if stride[outer] >= max(1, shape[inner]) else None
+
+
+def _on_stream(device, stream):
+    """The raw stream to launch on: torch's current one on `device` by default."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    return getattr(stream, "cuda_stream", stream)
+
+
+def _same_device(*tensors):
+    device = tensors[0].device
+    if device.type != "cuda" or any(t.device != device for t in tensors):
+        raise ValueError("tensors must be on one GPU: " + ", ".join(str(t.device) for t in tensors))
+    return device
+
+
+def _int32_vector(t, n, what):
+    import torch
+    if t.dtype != torch.int32 or t.dim() != 1 or (n is not None and t.shape[0] != n) or \
+            (t.shape[0] > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous int32 vector" + ("" if n is None else f" of {n}"))
+
+
+def _launch(fn, device, *args):
+    """Call a C ABI function with `device` current; raise on a bad status."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st != GEMM_OK:
+        raise GemmError(st)
+
+
+def grouped_gemm(a, b, ends, c, stream=None):
+    """C[m] = A[m] * B_g^T for the rows m of each group g (gemm_run_grouped): a
+    is (M, K) and c (M, N), both row-major; b is (G, N, K) with N or K
+    contiguous; ends is an int32 GPU vector of G ascending ends of the groups'
+    rows.  Rows of c past the last end keep their values.  The output of a
+    mixture's experts is grouped_gemm(x, w, ends, y); the gradient of x is
+    grouped_gemm(dy, w.transpose(1, 2), ends, dx)."""
+    device = _same_device(a, b, ends, c)
+    if a.dim() != 2 or b.dim() != 3 or c.dim() != 2 or b.shape[2] != a.shape[1] or \
+            tuple(c.shape) != (a.shape[0], b.shape[1]):
+        raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, c {tuple(c.shape)}")
+    if b.dtype != a.dtype:
+        raise ValueError("a and b must have the same dtype")
+    _int32_vector(ends, b.shape[0], "ends")
+    lda, ldc = _ld(a.shape, a.stride(), 0, 1), _ld(c.shape, c.stride(), 0, 1)
+    bm, ldb = "k", _ld(b.shape[1:], b.stride()[1:], 0, 1)
+    if ldb is None:
+        bm, ldb = "n", _ld(b.shape[1:], b.stride()[1:], 1, 0)
+    if lda is None or ldb is None or ldc is None:
+        raise ValueError(f"a {a.stride()} and c {c.stride()} must be row-major, b {b.stride()} have one "
+                         "contiguous dimension")
+    _launch(_lib.gemm_run_grouped, device, a.shape[0], b.shape[1], a.shape[1], b"k", _c(bm), b"n",
+            dtype_code(a.dtype, c.dtype), a.data_ptr(), b.data_ptr(), c.data_ptr(), lda, ldb, ldc,
+            b.shape[0], b.stride(0), ends.data_ptr(), _on_stream(device, stream))
+    return c
+
+
+def grouped_gemm_k(a, b, ends, c, accumulate=False, stream=None):
+    """C_g = sum over the k of group g of A[:, k] * B[:, k]^T (gemm_run_grouped_k):
+    a is (M, K) and b (N, K), views of row-major token matrices (K x M and
+    K x N), c is (G, M, N) with M or N contiguous, ends the G ascending ends of
+    the groups' k.  Groups without any k get zeros; accumulate adds to c.  The
+    gradient of a mixture's weights is grouped_gemm_k(dy.t(), x.t(), ends, dw)."""
+    device = _same_device(a, b, ends, c)
+    if a.dim() != 2 or b.dim() != 2 or c.dim() != 3 or b.shape[1] != a.shape[1] or \
+            tuple(c.shape[1:]) != (a.shape[0], b.shape[0]):
+        raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, c {tuple(c.shape)}")
+    if b.dtype != a.dtype:
+        raise ValueError("a and b must have the same dtype")
+    _int32_vector(ends, c.shape[0], "ends")
+    lda, ldb = _ld(a.shape, a.stride(), 1, 0), _ld(b.shape, b.stride(), 1, 0)
+    cm, ldc = "n", _ld(c.shape[1:], c.stride()[1:], 0, 1)
+    if ldc is None:
+        cm, ldc = "m", _ld(c.shape[1:], c.stride()[1:], 1, 0)
+    if lda is None or ldb is None or ldc is None:
+        raise ValueError(f"a {a.stride()} and b {b.stride()} must be transposed views of row-major matrices, "
+                         f"c {c.stride()} have one contiguous dimension")
+    _launch(_lib.gemm_run_grouped_k, device, a.shape[0], b.shape[0], a.shape[1], b"m", b"n", _c(cm),
+            dtype_code(a.dtype, c.dtype), a.data_ptr(), b.data_ptr(), c.data_ptr(), lda, ldb, ldc,
+            c.shape[0], c.stride(0), ends.data_ptr(), int(bool(accumulate)), _on_stream(device, stream))
     return c
 
 

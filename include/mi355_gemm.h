@@ -266,6 +266,49 @@ int gemm_run_config(int64_t M, int64_t N, int64_t K, char a_major, char b_major,
                     int dtype, const void* A, const void* B, void* C,
                     int64_t lda, int64_t ldb, int64_t ldc, void* stream, int config_id);
 
+/*
+ * Grouped products (the experts of a mixture of experts, and their
+ * gradients).  `ends` is a device array of one int32 per group: consecutive
+ * groups, group g covering [ends[g-1], ends[g]) (from 0 for the first) of the
+ * rows (gemm_run_grouped) or of k (gemm_run_grouped_k).  The host does not
+ * read it: nothing synchronises, and a captured call takes the ends that the
+ * array holds at each replay.  A group may be empty.  Ends that do not ascend
+ * or lie outside [0, rows] are taken as the running maximum of the ends
+ * clamped to that range, so no content of the array reaches outside A, B or C.
+ *
+ * gemm_run_grouped:  C[m][n] = sum_k A[m][k] * B_g[n][k] for the rows m of
+ * group g, B_g = B + g*stride_b (elements; 0: one B for all).  A is k-major
+ * and C n-major (the index that is grouped must not be the contiguous one,
+ * else GEMM_ERR_BAD_MAJOR); B k- or n-major: with weights N x K, k-major, this
+ * is the layer's output, and the same weights read n-major (N and K
+ * exchanged) give the gradient of its input.  Rows of C past the last end
+ * are left as they were; rows of A past it are not read.  K == 0 writes zeros.
+ *
+ * gemm_run_grouped_k:  C_g[m][n] = sum over the k of group g of
+ * A[m][k] * B[n][k], C_g = C + g*stride_c: the gradient of the weights, with A
+ * the gradient of the outputs and B the inputs, both stored row by row of
+ * tokens, i.e. a_major 'm' and b_major 'n' (else GEMM_ERR_BAD_MAJOR); c_major
+ * 'n' or 'm'.  A group without any k gets zeros.  accumulate != 0 adds to C
+ * instead, in fp32 before the rounding to C's type (a group without any k is
+ * then left as it was).  C_g must not overlap (GEMM_ERR_BAD_LD).
+ *
+ * Sizes, alignment (operands that are not 16-byte aligned run element by
+ * element; C's own alignment only decides the width of its stores), the
+ * checks and their order, asynchrony and errors are those of gemm_run; ends
+ * must be 4-byte aligned and not overlap C.  groups <= 65535; groups == 0
+ * launches nothing.  No workspace; results are deterministic.  The tile
+ * config is the library's choice (gemm_last_config does not record it).
+ */
+int gemm_run_grouped(int64_t M, int64_t N, int64_t K, char a_major, char b_major, char c_major,
+                     int dtype, const void* A, const void* B, void* C,
+                     int64_t lda, int64_t ldb, int64_t ldc,
+                     int64_t groups, int64_t stride_b, const int32_t* ends, void* stream);
+int gemm_run_grouped_k(int64_t M, int64_t N, int64_t K, char a_major, char b_major, char c_major,
+                       int dtype, const void* A, const void* B, void* C,
+                       int64_t lda, int64_t ldb, int64_t ldc,
+                       int64_t groups, int64_t stride_c, const int32_t* ends, int accumulate,
+                       void* stream);
+
 /* Static description of a status code; never NULL. */
 const char* gemm_status_str(int status);
 

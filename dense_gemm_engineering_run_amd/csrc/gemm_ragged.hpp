@@ -121,18 +121,24 @@ __device__ __forceinline__ int64_t row_tail(int inner)
     return VEC ? ((int64_t)inner * ES + 15) / 16 * 16 : (int64_t)inner * ES;
 }
 
+// Which index of the canonical product C = A * B^T the groups divide.
+//  Rows: the rows of A and C; each group has a matrix of its own in B.
+//  K:    the summed index; each group has a C of its own.
+enum class By : int { Rows = 0, K = 1 };
+
 // Point p at the workgroup's group; false: no tile for this workgroup.
-// ROWS (by rows): p.M is the group's rows, A and C start at its first row, B
-// at its matrix.  Otherwise p.K is the group's k-range, A and B (both with k
-// as the outer index) start at its first k, C at the group's matrix; a group
-// without any k writes zeros, or nothing where C is added to.
+// By rows p.M becomes the group's rows, A and C start at its first row, B at
+// its matrix.  By k p.K is the
+// group's k-range, A and B (both with k as the outer index) start at its first
+// k, C at the group's matrix; a group without any k writes zeros, or nothing
+// where C is added to.
 // tm, tn: the tile within the group.
-template <In TI, Out TO, int BM, int BN, bool ROWS, bool VEC>
+template <In TI, Out TO, int BM, int BN, By BY, bool VEC>
 __device__ __forceinline__ bool select_group(Params& p, const Ragged& r, int lane, int& tm, int& tn)
 {
     constexpr int ES = TI == In::F32 ? 4 : 2, EO = TO == Out::F32 ? 4 : 2;
     int g, start, len;
-    if constexpr (ROWS) {
+    if constexpr (BY == By::Rows) {
         int L;
         p.tiles_n = (p.N + BN - 1) / BN;
         if (!find_row_group(r, BM, p.tiles_n, lane, g, start, len, L)) return false;
@@ -156,12 +162,16 @@ __device__ __forceinline__ bool select_group(Params& p, const Ragged& r, int lan
         p.a_bytes = rows_extent(len, p.lda * ES, row_tail<ES, VEC>(p.M));
         p.b_bytes = rows_extent(len, p.ldb * ES, row_tail<ES, VEC>(p.N));
     }
+    // Wave-uniform, but divisions run on the vector unit: back into scalar
+    // registers, which the main loop's addresses are made of.
+    tm = __builtin_amdgcn_readfirstlane(tm);
+    tn = __builtin_amdgcn_readfirstlane(tn);
     return true;
 }
 
 // The grouped product on the register-staged tile of gemm_kernel.hpp: right
 // for every type, layout and alignment (VEC = false: element-aligned operands).
-template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, int MI, bool AK, bool BKM, bool ROWS, bool EPI, bool VEC>
+template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, int MI, bool AK, bool BKM, By BY, bool EPI, bool VEC>
 __global__ void __launch_bounds__(WM * WN * 64)
 gemm_ragged_kernel(Params p, Ragged r)
 {
@@ -176,7 +186,7 @@ gemm_ragged_kernel(Params p, Ragged r)
     t.frow = lane % MI;
     t.fq = lane / MI;
     int tm, tn;
-    if (!select_group<TI, TO, BM, BN, ROWS, VEC>(p, r, lane, tm, tn)) return;
+    if (!select_group<TI, TO, BM, BN, BY, VEC>(p, r, lane, tm, tn)) return;
     const int m0 = tm * BM, n0 = tn * BN;
     t.la.init(t.tid, p.lda);
     t.lb.init(t.tid, p.ldb);
@@ -237,7 +247,239 @@ gemm_ragged_kernel(Params p, Ragged r)
     }
 }
 
-// What the host asks of a dtype's launchers (gemm_grouped_<dtype>.hip).
+// ------------------------------------------------------- direct-to-LDS kernels
+
+// Store a tile held by a Dma16 engine: through the elementwise epilogue (EPI),
+// as whole rows through LDS, or element by element.
+template <class KT, bool EPI>
+__device__ __forceinline__ void store_tile(const Params& p, char* smem, int m0, int n0, const typename KT::Acc& acc,
+                                           int tid, int lane, int wave)
+{
+    if constexpr (EPI) {
+        KT::store_staged(p, smem, m0, n0, acc, tid, lane, wave);
+    } else {
+        if (KT::ROWS_OK && p.c_vec) {
+            bare_barrier();   // every wave's loads have landed and its ring reads are done
+            if constexpr (KT::ROWS_OK) KT::store_rows(p, smem, m0, n0, acc, lane, wave);
+        } else {
+            KT::store_direct(p, m0, n0, acc, lane, wave);
+        }
+    }
+}
+
+// 16-bit inputs on the direct-to-LDS ring of gemm_dma.hpp.
+template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, int MI, int STAGES, bool AK, bool BKM, By BY, bool EPI>
+__global__ void __launch_bounds__(WM * WN * 64)
+gemm_ragged_dma_kernel(Params p, Ragged r)
+{
+    using KT = Dma16<TI, TO, BM, BN, BK, WM, WN, MI, STAGES, AK, BKM>;
+    __shared__ __attribute__((aligned(1024))) char smem[KT::SMEM];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tm, tn;
+    if (!select_group<TI, TO, BM, BN, BY, true>(p, r, lane, tm, tn)) return;
+    const int m0 = tm * BM, n0 = tn * BN;
+    typename KT::OA oa;
+    typename KT::OB ob;
+    oa.init(wave, lane, p.lda);
+    ob.init(wave, lane, p.ldb);
+    typename KT::Acc acc;
+    KT::zero(acc);
+    KT::mainloop(p, smem, oa, ob, m0, n0, 0, (p.K + BK - 1) / BK, acc, tid, lane, wave);
+    store_tile<KT, EPI>(p, smem, m0, n0, acc, tid, lane, wave);
+}
+
+// The ping-pong schedule of gemm_pp_kernel (gemm_dma.hpp, which explains it)
+// over all of p.K, adding to acc: two groups of four waves, one multiplying a
+// k-tile out of registers while the other issues its loads and reads the next
+// fragments.  All loads have landed on return.
+template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, int MI, bool AK, bool BKM>
+struct PingPong {
+    using KT = Dma16<TI, TO, BM, BN, BK, WM, WN, MI, 3, AK, BKM, 2>;
+    using LA = DmaOperand<BM, BK, 4, AK, MI>;     // loaded by group 1
+    using LB = DmaOperand<BN, BK, 4, BKM, MI>;    // loaded by group 0
+    static constexpr int NG = KT::NG, KG = KT::KG, TM = KT::TM, TN = KT::TN, NT = KT::NT;
+    static constexpr int WTM = KT::WTM, WTN = KT::WTN, IA = LA::IPW, IB = LB::IPW;
+    static_assert(WM * WN == 8, "two groups of four waves");
+    static_assert(IA == IB, "one offset set for either operand");
+
+    __device__ static __forceinline__ void mainloop(const Params& p, char* smem, int m0, int n0, typename KT::Acc& acc,
+                                                    int tid, int lane, int wave)
+    {
+        const int grp = wave >> 2, gw = wave & 3, wm = wave / WN, wn = wave % WN;
+        // The loop runs the whole k-tiles.  (A k-contiguous operand's partial
+        // last tile needs zeros past K, written in LDS: inside the loop that
+        // code's registers spill, and each reload waits for every load in
+        // flight -- measured 1.7x on the gradient of the tokens.  An
+        // m-contiguous operand reads zeros there, so if both are it is a tile
+        // like the others.)
+        constexpr bool TAIL = AK || BKM;
+        const int nkt = TAIL ? p.K / BK : (p.K + BK - 1) / BK;
+        // A wave loads one operand only; its per-lane offsets pass through an
+        // empty asm so that each takes one register (the 64-bit product they
+        // come from would keep two, and a spilled offset's reload waits for
+        // every load in flight).
+        int voff[IA];
+        if (grp) {
+            LA o;
+            o.init(gw, lane, p.lda);
+#pragma unroll
+            for (int j = 0; j < IA; ++j) voff[j] = o.voff[j];
+        } else {
+            LB o;
+            o.init(gw, lane, p.ldb);
+#pragma unroll
+            for (int j = 0; j < IB; ++j) voff[j] = o.voff[j];
+        }
+#pragma unroll
+        for (int j = 0; j < IA; ++j) asm volatile("" : "+v"(voff[j]));
+        auto issue_a = [&](int t, int stage, uint64_t bytes) {
+            LA o;
+#pragma unroll
+            for (int j = 0; j < IA; ++j) o.voff[j] = voff[j];
+            o.issue(p.A, bytes, p.lda, m0, t * BK, KT::a_stage(smem, stage), gw);
+        };
+        auto issue_b = [&](int t, int stage, uint64_t bytes) {
+            LB o;
+#pragma unroll
+            for (int j = 0; j < IB; ++j) o.voff[j] = voff[j];
+            o.issue(p.B, bytes, p.ldb, n0, t * BK, KT::b_stage(smem, stage), gw);
+        };
+        // Loads past the last tile get an empty extent: zeros into a free slot.
+        auto next_a = [&](int t) { issue_a(t, t, t < nkt ? p.a_bytes : 0); };
+        auto next_b = [&](int t) { issue_b(t, t, t < nkt ? p.b_bytes : 0); };
+        i32x4 fa[NG][TM], fb[NG][TN];
+        auto read_all = [&](int s) {
+            const char* sa = KT::a_stage(smem, s);
+            const char* sb = KT::b_stage(smem, s);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i) fa[g][i] = LA::template frag<MI>(sa, wm * WTM + i * MI, g * KG, lane);
+#pragma unroll
+                for (int j = 0; j < TN; ++j) fb[g][j] = LB::template frag<MI>(sb, wn * WTN + j * MI, g * KG, lane);
+            }
+        };
+        auto mfma_all = [&]() {
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) mfma_step<TI, MI>(fa[g][i], fb[g][j], acc[i][j]);
+        };
+        if (grp) {
+            next_a(0);
+            next_a(1);
+            wait_vmcnt<IA>();
+        } else {
+            next_b(0);
+            next_b(1);
+            wait_vmcnt<IB>();
+        }
+        bare_barrier();
+        if (!grp) {
+            read_all(0);
+            __builtin_amdgcn_s_waitcnt(0xc07f);
+            for (int t = 0; t < nkt; ++t) {
+                __builtin_amdgcn_sched_barrier(0);
+                mfma_all();                       // phase A: tile t
+                __builtin_amdgcn_sched_barrier(0);
+                wait_vmcnt<0>();                  // B of tile t + 1
+                bare_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+                next_b(t + 2);                   // phase B: into tile t's B slot
+                if (t + 1 < nkt) read_all(t + 1);
+                __builtin_amdgcn_s_waitcnt(0xc07f);
+                __builtin_amdgcn_sched_barrier(0);
+                bare_barrier();
+            }
+        } else {
+            for (int t = 0; t < nkt; ++t) {
+                __builtin_amdgcn_sched_barrier(0);
+                next_a(t + 2);                   // phase A: into tile t-1's A slot
+                read_all(t);
+                __builtin_amdgcn_s_waitcnt(0xc07f);
+                wait_vmcnt<IA>();                 // A of tile t + 1
+                __builtin_amdgcn_sched_barrier(0);
+                bare_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+                mfma_all();                       // phase B: tile t
+                __builtin_amdgcn_sched_barrier(0);
+                bare_barrier();
+            }
+        }
+        wait_vmcnt<0>();
+        if constexpr (TAIL) {
+            const int left = p.K - nkt * BK;
+            if (left == 0) return;
+            bare_barrier();                       // no empty load into the ring is still to land
+            if (grp) issue_a(nkt, 0, p.a_bytes);
+            else issue_b(nkt, 0, p.b_bytes);
+            wait_vmcnt<0>();
+            bare_barrier();
+            LA::template zero_tail<NT>(KT::a_stage(smem, 0), left, tid);
+            LB::template zero_tail<NT>(KT::b_stage(smem, 0), left, tid);
+            __syncthreads();
+#pragma unroll 1
+            for (int g = 0; g * KG < left; ++g) {    // rolled: the accumulators stay where they are
+                i32x4 ta[TM], tb[TN];
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+                    ta[i] = LA::template frag<MI>(KT::a_stage(smem, 0), wm * WTM + i * MI, g * KG, lane);
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    tb[j] = LB::template frag<MI>(KT::b_stage(smem, 0), wn * WTN + j * MI, g * KG, lane);
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) mfma_step<TI, MI>(ta[i], tb[j], acc[i][j]);
+            }
+        }
+    }
+};
+
+template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, int MI, bool AK, bool BKM, By BY, bool EPI>
+__global__ void __launch_bounds__(WM * WN * 64)
+gemm_ragged_pp_kernel(Params p, Ragged r)
+{
+    using PP = PingPong<TI, TO, BM, BN, BK, WM, WN, MI, AK, BKM>;
+    using KT = typename PP::KT;
+    __shared__ __attribute__((aligned(1024))) char smem[KT::SMEM];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tm, tn;
+    if (!select_group<TI, TO, BM, BN, BY, true>(p, r, lane, tm, tn)) return;
+    const int m0 = tm * BM, n0 = tn * BN;
+    typename KT::Acc acc;
+    KT::zero(acc);
+    PP::mainloop(p, smem, m0, n0, acc, tid, lane, wave);
+    store_tile<KT, EPI>(p, smem, m0, n0, acc, tid, lane, wave);
+}
+
+// fp32 on the direct-to-LDS engine of gemm_f32dma.hpp (VEC = false: 4-byte
+// loads of element-aligned operands).
+template <int BM, int BN, int BK, int WM, int WN, int STAGES, bool AK, bool BKM, By BY, bool EPI, bool VEC>
+__global__ void __launch_bounds__(WM * WN * 64)
+gemm_ragged_f32_kernel(Params p, Ragged r)
+{
+    using KT = F32Dma<Out::F32, BM, BN, BK, WM, WN, STAGES, AK, BKM, VEC>;
+    __shared__ __attribute__((aligned(1024))) char smem[KT::SMEM];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tm, tn;
+    if (!select_group<In::F32, Out::F32, BM, BN, BY, VEC>(p, r, lane, tm, tn)) return;
+    const int m0 = tm * BM, n0 = tn * BN;
+    typename KT::OA oa;
+    typename KT::OB ob;
+    oa.init(wave, lane, p.lda);
+    ob.init(wave, lane, p.ldb);
+    typename KT::Acc acc;
+    KT::zero(acc);
+    KT::mainloop(p, smem, oa, ob, m0, n0, 0, (p.K + BK - 1) / BK, acc, tid, lane, wave);
+    KT::template store<false, EPI>(p, m0, n0, acc, lane, wave, smem);
+}
+
+// ------------------------------------------------------------------ launchers
+
+// What the host asks of a dtype's launchers (gemm_ragged_<dtype>.hip).
 struct RaggedCall {
     Params p;             // p.epi: add to C (by k only)
     Ragged r;
@@ -246,9 +488,9 @@ struct RaggedCall {
     bool vec;             // operands allow 16-byte loads
 };
 
-// Tiles of the grid's upper bound: by rows, ceil(len_g / BM) summed over the
-// groups is at most (rows + groups * (BM - 1)) / BM.
-template <class Kernel>
+// The grid's upper bound: by rows, ceil(len_g / BM) tiles of BM rows summed
+// over the groups are at most (rows + groups * (BM - 1)) / BM.
+template <By BY, class Kernel>
 hipError_t launch_ragged(Kernel kernel, const RaggedCall& c, int BM, int BN, int threads, hipStream_t s)
 {
     Params p = c.p;
@@ -257,12 +499,12 @@ hipError_t launch_ragged(Kernel kernel, const RaggedCall& c, int BM, int BN, int
     p.tiles_n = (p.N + BN - 1) / BN;
     p.group_m = p.tiles_m < 8 ? p.tiles_m : 8;
     dim3 grid;
-    if (c.by_rows) {
-        int64_t tm = ((int64_t)r.rows + (int64_t)r.groups * (BM - 1)) / BM;
-        if (tm > r.rows) tm = r.rows;
-        grid = dim3((unsigned)(tm * p.tiles_n));
-    } else {
+    if (BY == By::K) {
         grid = dim3((unsigned)(p.tiles_m * p.tiles_n), (unsigned)r.groups);
+    } else {
+        int64_t t = ((int64_t)r.rows + (int64_t)r.groups * (BM - 1)) / BM;
+        if (t > r.rows) t = r.rows;
+        grid = dim3((unsigned)(t * p.tiles_n));
     }
     void* args[] = {&p, &r};
     return hipLaunchKernel((const void*)kernel, grid, dim3(threads), args, 0, s);
@@ -270,20 +512,85 @@ hipError_t launch_ragged(Kernel kernel, const RaggedCall& c, int BM, int BN, int
 
 template <In TI, Out TO>
 struct RaggedInst {
-    static constexpr int BK = TI == In::F32 ? 32 : 64;
-    template <bool AK, bool BKM, bool ROWS, bool EPI, bool VEC>
-    static hipError_t generic(const RaggedCall& c, hipStream_t s)
+    // Element-by-element loads: any alignment, any type but fp32.
+    template <bool BKM>
+    static hipError_t scalar_rows(const RaggedCall& c, hipStream_t s)
     {
-        return launch_ragged(&gemm_ragged_kernel<TI, TO, 64, 64, BK, 2, 2, 16, AK, BKM, ROWS, EPI, VEC>, c, 64, 64, 256, s);
+        return launch_ragged<By::Rows>(&gemm_ragged_kernel<TI, TO, 64, 64, 64, 2, 2, 16, true, BKM, By::Rows, false, false>, c, 64, 64, 256, s);
     }
-    template <bool VEC>
-    static hipError_t any(const RaggedCall& c, hipStream_t s)
+    template <bool EPI>
+    static hipError_t scalar_k(const RaggedCall& c, hipStream_t s)
     {
-        if (c.by_rows)
-            return c.b_kmajor ? generic<true, true, true, false, VEC>(c, s) : generic<true, false, true, false, VEC>(c, s);
-        return c.p.epi ? generic<false, false, false, true, VEC>(c, s) : generic<false, false, false, false, VEC>(c, s);
+        return launch_ragged<By::K>(&gemm_ragged_kernel<TI, TO, 64, 64, 64, 2, 2, 16, false, false, By::K, EPI, false>, c, 64, 64, 256, s);
     }
-    static hipError_t launch(const RaggedCall& c, hipStream_t s) { return c.vec ? any<true>(c, s) : any<false>(c, s); }
+    template <int BM, int BN, int BK, int WM, int WN, int MI, int ST, bool AK, bool BKM, By BY, bool EPI>
+    static hipError_t dma(const RaggedCall& c, hipStream_t s)
+    {
+        return launch_ragged<BY>(&gemm_ragged_dma_kernel<TI, TO, BM, BN, BK, WM, WN, MI, ST, AK, BKM, BY, EPI>, c, BM, BN, WM * WN * 64, s);
+    }
+    template <bool AK, bool BKM, By BY, bool EPI>
+    static hipError_t pp(const RaggedCall& c, hipStream_t s)
+    {
+        return launch_ragged<BY>(&gemm_ragged_pp_kernel<TI, TO, 256, 256, 64, 4, 2, 16, AK, BKM, BY, EPI>, c, 256, 256, 512, s);
+    }
+    // By rows: the tile height follows the rows a group has on average (the
+    // host knows no more), then how many tiles that makes.  Measured in bf16,
+    // B k-major (n-major in brackets where it differs), us:
+    //   rows/group  groups  N x K       16-row 32     64     128x128 128x256 256x256
+    //       1         8     4096 x 4096   39.7  38.6 [44.9] 42.0 [36.7] 41.6  61.7  75
+    //      16         8     4096 x 4096   55.9  53.2 [62.8] 61.8 [47.5] 62.5  74.1  75
+    //      16        64     2048 x 1024   60.3  56.9   51.5   61.1   59.0   85
+    //      64         8     4096 x 4096  100    77.4   67.3   90.4   78.7   88.9
+    //     128         8     4096 x 4096  168   118     95.6   89.0   81.5   89.2
+    //     128        32     2048 x 4096                155    143    154    194
+    //     256         8     4096 x 4096               132    121    131     90.9
+    //     256         8     2048 x 1024                21.1   25.7   20.8   23.5
+    //    1024         8     4096 x 2048               206    190    175    140
+    //    4096         8     4096 x 4096                      1270   1150    847
+    // 128x128 in two stages, two workgroups a CU: 18.5 us at 256 rows in 8
+    // groups of 2048 x 1024 (64 tiles of 256x256), 33.4 at 512 (128 tiles;
+    // 256x256: 25.7).
+    template <bool BKM>
+    static hipError_t rows(const RaggedCall& c, hipStream_t s)
+    {
+        const int64_t groups = c.r.groups, avg = (c.r.rows + groups - 1) / groups;
+        const int64_t cols256 = (c.p.N + 255) / 256;
+        if (avg <= 24) {
+            if constexpr (BKM) return dma<32, 64, 128, 1, 4, 16, 3, true, BKM, By::Rows, false>(c, s);
+            else return dma<64, 128, 64, 2, 2, 16, 3, true, BKM, By::Rows, false>(c, s);
+        }
+        if (avg <= 80) return dma<64, 128, 64, 2, 2, 16, 3, true, BKM, By::Rows, false>(c, s);
+        if (avg < 192) {
+            if (groups * ((avg + 127) / 128) * cols256 >= 100)
+                return dma<128, 256, 64, 2, 2, 32, 3, true, BKM, By::Rows, false>(c, s);
+            return dma<128, 128, 64, 2, 2, 16, 4, true, BKM, By::Rows, false>(c, s);
+        }
+        if (groups * ((avg + 255) / 256) * cols256 >= 100) return pp<true, BKM, By::Rows, false>(c, s);
+        return dma<128, 128, 64, 2, 2, 32, 2, true, BKM, By::Rows, false>(c, s);
+    }
+    // By k: 256x256 tiles from half a CU's share of them up (bf16 -> fp32, 8
+    // groups: 4096 x 2048 of 8192 k 161 us against 197 on 128x128; 64 groups of
+    // 512 x 512, 256 tiles, 22.3 against 23.6), then 128x128 in two stages (8
+    // groups of 1024 x 1024, 128 tiles of 256x256: 36.4 against 48.3), and
+    // 64x64 where even those leave CUs idle (8 groups of 512 x 512 of 8192 k:
+    // 19.8 against 27.6).
+    template <bool EPI>
+    static hipError_t by_k(const RaggedCall& c, hipStream_t s)
+    {
+        auto tiles = [&](int t) { return ((int64_t)c.p.M + t - 1) / t * ((c.p.N + t - 1) / t) * c.r.groups; };
+        if (tiles(256) >= 192) return pp<false, false, By::K, EPI>(c, s);
+        if (tiles(128) >= 192) return dma<128, 128, 64, 2, 2, 32, 2, false, false, By::K, EPI>(c, s);
+        return dma<64, 64, 64, 2, 2, 32, 4, false, false, By::K, EPI>(c, s);
+    }
+    static hipError_t launch(const RaggedCall& c, hipStream_t s)
+    {
+        if (c.by_rows) {
+            if (c.vec) return c.b_kmajor ? rows<true>(c, s) : rows<false>(c, s);
+            return c.b_kmajor ? scalar_rows<true>(c, s) : scalar_rows<false>(c, s);
+        }
+        if (c.vec) return c.p.epi ? by_k<true>(c, s) : by_k<false>(c, s);
+        return c.p.epi ? scalar_k<true>(c, s) : scalar_k<false>(c, s);
+    }
 };
 
 hipError_t ragged_f32(const RaggedCall& c, hipStream_t s);

@@ -227,6 +227,20 @@ def test_large_tiles(dtype, lens):
     run_k(lens, 1024, 1024, dtype, "n", kind="int5", accumulate=True)
 
 
+@pytest.mark.parametrize("dtype", ["bf16_bf16", "f16_f32", "f16_f16", "f32"])
+@pytest.mark.parametrize("K", [40, 64, 72, 192, 328])
+def test_wide_outputs(dtype, K):
+    """Enough columns for the largest tile whatever the groups' lengths, with
+    every kind of last k-tile."""
+    for b_major in "kn":
+        run_rows([700, 0, 1, 900, 511], 5400, K, dtype, b_major, left=3)      # 256x256
+        run_rows([150, 0, 97, 128, 129] * 4, 2100, K, dtype, b_major, left=3)  # 128x256
+        run_rows([40] * 48, 1100, K, dtype, b_major, left=3)                   # 64x128
+        run_rows([600, 0, 300], 520, K, dtype, b_major, left=3)                # 128x128
+    run_k([K, 0, 3, 2 * K, 65], 1100, 2104, dtype, "n", left=3)
+    run_k([K, 0, 3, 2 * K, 65], 1100, 2104, dtype, "m", left=3, accumulate=True)
+
+
 @pytest.mark.parametrize("ends", [[50, 20, 90], [-5, 30, 30], [1000, 40, 99], [100, 100, 100], [-1, -1, -1],
                                   [2 ** 31 - 1, -2 ** 31, 5]])
 def test_ends_that_do_not_ascend_stay_in_bounds(ends):

@@ -53,6 +53,15 @@ class Epilogue(ctypes.Structure):
                 ("bias", ctypes.c_void_p), ("activation", ctypes.c_int)]
 
 
+class Lora(ctypes.Structure):
+    """gemm_lora_t: the slots of low-rank adapters and each row's slot."""
+    _fields_ = [("adapters", ctypes.c_int64), ("rank", ctypes.c_int64),
+                ("down", ctypes.c_void_p), ("up", ctypes.c_void_p),
+                ("ld_down", ctypes.c_int64), ("ld_up", ctypes.c_int64),
+                ("stride_down", ctypes.c_int64), ("stride_up", ctypes.c_int64),
+                ("ids", ctypes.c_void_p), ("ranks", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
 _RUN_ARGS = [_i64, _i64, _i64, _chr, _chr, _chr, _int, _vp, _vp, _vp, _i64, _i64, _i64, _vp]
 _lib.gemm_run.argtypes = _RUN_ARGS
 _lib.gemm_run.restype = _int
@@ -75,6 +84,10 @@ _lib.gemm_run_grouped.argtypes = _GROUPED_ARGS + [_vp]
 _lib.gemm_run_grouped.restype = _int
 _lib.gemm_run_grouped_k.argtypes = _GROUPED_ARGS + [_int, _vp]
 _lib.gemm_run_grouped_k.restype = _int
+_lib.gemm_run_lora.argtypes = _RUN_ARGS[:-1] + [ctypes.POINTER(Lora), _vp, ctypes.c_size_t, _vp]
+_lib.gemm_run_lora.restype = _int
+_lib.gemm_lora_workspace_size.argtypes = [_i64, _i64, _i64, _int, _i64, ctypes.POINTER(ctypes.c_size_t)]
+_lib.gemm_lora_workspace_size.restype = _int
 _lib.gemm_status_str.argtypes = [_int]
 _lib.gemm_status_str.restype = ctypes.c_char_p
 _lib.gemm_num_configs.argtypes = [_int]
@@ -182,6 +195,23 @@ def gemm_run_grouped_k(M, N, K, a_major, b_major, c_major, dtype, A, B, C, lda, 
     return _lib.gemm_run_grouped_k(M, N, K, _c(a_major), _c(b_major), _c(c_major), dtype, A, B, C,
                                    lda, ldb, ldc, groups, stride_c, ends, int(bool(accumulate)),
                                    stream)
+
+
+def gemm_run_lora(M, N, K, a_major, b_major, c_major, dtype, A, B, C, lda, ldb, ldc, lora=None,
+                  workspace=0, workspace_bytes=0, stream=0):
+    """C ABI gemm_run_lora; `lora` is a Lora or None. Returns the status."""
+    return _lib.gemm_run_lora(M, N, K, _c(a_major), _c(b_major), _c(c_major), dtype, A, B, C, lda, ldb, ldc,
+                              ctypes.byref(lora) if lora is not None else None, workspace, workspace_bytes,
+                              stream)
+
+
+def gemm_lora_workspace_size(M, N, K, dtype, rank):
+    """Workspace bytes for gemm_run_lora / gemm_lora; raises GemmError on invalid arguments."""
+    n = ctypes.c_size_t(0)
+    st = _lib.gemm_lora_workspace_size(M, N, K, dtype, rank, ctypes.byref(n))
+    if st != GEMM_OK:
+        raise GemmError(st)
+    return n.value
 
 
 def gemm_workspace_size(M, N, K, a_major, b_major, c_major, dtype, config_id=-1):
@@ -379,6 +409,49 @@ def grouped_gemm_k(a, b, ends, c, accumulate=False, stream=None):
     _launch(_lib.gemm_run_grouped_k, device, a.shape[0], b.shape[0], a.shape[1], b"m", b"n", _c(cm),
             dtype_code(a.dtype, c.dtype), a.data_ptr(), b.data_ptr(), c.data_ptr(), lda, ldb, ldc,
             c.shape[0], c.stride(0), ends.data_ptr(), int(bool(accumulate)), _on_stream(device, stream))
+    return c
+
+
+def gemm_lora(a, b, c, down, up, ids, workspace, ranks=None, scales=None, stream=None):
+    """C = A * B^T plus each row's low-rank adapter (gemm_run_lora): a is (M, K)
+    and c (M, N), row-major, b is (N, K) with N or K contiguous; down is
+    (L, R, K) and up (L, N, R), each slot row-major; ids (M,), ranks (L,) are
+    int32 and scales (L,) float32 GPU vectors; a row whose id is outside
+    [0, L) has no adapter.  workspace is a contiguous GPU tensor of at least
+    gemm_lora_workspace_size(M, N, K, dtype_code(a.dtype, c.dtype), R) bytes,
+    kept by the caller and not shared by calls that may run at once."""
+    import torch
+    device = _same_device(a, b, c, down, up, ids, workspace, *(t for t in (ranks, scales) if t is not None))
+    M, K = a.shape if a.dim() == 2 else (-1, -1)
+    N = b.shape[0]
+    if b.dim() != 2 or c.dim() != 2 or down.dim() != 3 or up.dim() != 3 or b.shape[1] != K or \
+            tuple(c.shape) != (M, N) or down.shape[2] != K or tuple(up.shape) != (down.shape[0], N, down.shape[1]):
+        raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, c {tuple(c.shape)}, "
+                         f"down {tuple(down.shape)}, up {tuple(up.shape)}")
+    if not (a.dtype == b.dtype == down.dtype == up.dtype):
+        raise ValueError("a, b, down and up must have the same dtype")
+    L, R = down.shape[:2]
+    _int32_vector(ids, M, "ids")
+    if ranks is not None:
+        _int32_vector(ranks, L, "ranks")
+    if scales is not None and (scales.dtype != torch.float32 or tuple(scales.shape) != (L,) or
+                               (L > 1 and scales.stride(0) != 1)):
+        raise ValueError(f"scales must be a contiguous float32 vector of {L}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    lda, ldc = _ld(a.shape, a.stride(), 0, 1), _ld(c.shape, c.stride(), 0, 1)
+    bm, ldb = "k", _ld(b.shape, b.stride(), 0, 1)
+    if ldb is None:
+        bm, ldb = "n", _ld(b.shape, b.stride(), 1, 0)
+    ld_down, ld_up = (_ld(t.shape[1:], t.stride()[1:], 0, 1) for t in (down, up))
+    if None in (lda, ldb, ldc, ld_down, ld_up):
+        raise ValueError(f"a {a.stride()}, c {c.stride()} and the slots of down {down.stride()} and up {up.stride()} "
+                         f"must be row-major, b {b.stride()} have one contiguous dimension")
+    lora = Lora(L, R, down.data_ptr(), up.data_ptr(), ld_down, ld_up, down.stride(0), up.stride(0), ids.data_ptr(),
+                None if ranks is None else ranks.data_ptr(), None if scales is None else scales.data_ptr())
+    _launch(_lib.gemm_run_lora, device, M, N, K, b"k", _c(bm), b"n", dtype_code(a.dtype, c.dtype), a.data_ptr(),
+            b.data_ptr(), c.data_ptr(), lda, ldb, ldc, ctypes.byref(lora), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _on_stream(device, stream))
     return c
 
 

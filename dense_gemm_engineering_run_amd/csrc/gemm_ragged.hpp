@@ -169,6 +169,41 @@ __device__ __forceinline__ bool select_group(Params& p, const Ragged& r, int lan
     return true;
 }
 
+// Main loop of the register-staged tile over all of p.K, adding to t.acc:
+// k-tile kt is multiplied out of LDS while kt + 1 goes from registers to the
+// other LDS stage and kt + 2 from memory to registers.
+template <class T, int BK>
+__device__ __forceinline__ void staged_mainloop(T& t, char* smem, const Params& p, int m0, int n0)
+{
+    const int nkt = (p.K + BK - 1) / BK;
+    if (nkt == 0) return;
+    const bool ragged = p.K % BK != 0;
+    auto load = [&](int kt) {
+        t.la.load(p.A, p.a_bytes, p.lda, m0, kt * BK, t.tid);
+        t.lb.load(p.B, p.b_bytes, p.ldb, n0, kt * BK, t.tid);
+    };
+    auto mask = [&](int kt) {
+        if (!ragged || kt != nkt - 1) return;
+        t.la.mask(kt * BK, p.K, t.tid);
+        t.lb.mask(kt * BK, p.K, t.tid);
+    };
+    load(0);
+    mask(0);
+    t.la.store(smem, t.tid);
+    t.lb.store(smem + T::A_BYTES, t.tid);
+    if (nkt > 1) load(1);
+    __syncthreads();
+    t.read_frags(smem, 0, 0);
+    int kt = 0;
+    for (; kt + 2 < nkt; ++kt) t.template tile<true, true, true>(smem, kt & 1, p, m0, n0, (kt + 2) * BK);
+    if (kt + 1 < nkt) {
+        mask(kt + 1);
+        t.template tile<true, false, true>(smem, kt & 1, p, m0, n0, 0);
+        ++kt;
+    }
+    t.template tile<false, false, false>(smem, kt & 1, p, m0, n0, 0);
+}
+
 // The grouped product on the register-staged tile of gemm_kernel.hpp: right
 // for every type, layout and alignment (VEC = false: element-aligned operands).
 template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, int MI, bool AK, bool BKM, By BY, bool EPI, bool VEC>
@@ -195,36 +230,7 @@ gemm_ragged_kernel(Params p, Ragged r)
 #pragma unroll
         for (int j = 0; j < T::TN; ++j) t.acc[i][j] = typename T::Acc{};
 
-    // k-tile kt is multiplied out of LDS while kt + 1 goes from registers to
-    // the other LDS stage and kt + 2 from memory to registers.
-    const int nkt = (p.K + BK - 1) / BK;
-    const bool ragged = p.K % BK != 0;
-    auto load = [&](int kt) {
-        t.la.load(p.A, p.a_bytes, p.lda, m0, kt * BK, t.tid);
-        t.lb.load(p.B, p.b_bytes, p.ldb, n0, kt * BK, t.tid);
-    };
-    auto mask = [&](int kt) {
-        if (!ragged || kt != nkt - 1) return;
-        t.la.mask(kt * BK, p.K, t.tid);
-        t.lb.mask(kt * BK, p.K, t.tid);
-    };
-    if (nkt > 0) {
-        load(0);
-        mask(0);
-        t.la.store(smem, t.tid);
-        t.lb.store(smem + T::A_BYTES, t.tid);
-        if (nkt > 1) load(1);
-        __syncthreads();
-        t.read_frags(smem, 0, 0);
-        int kt = 0;
-        for (; kt + 2 < nkt; ++kt) t.template tile<true, true, true>(smem, kt & 1, p, m0, n0, (kt + 2) * BK);
-        if (kt + 1 < nkt) {
-            mask(kt + 1);
-            t.template tile<true, false, true>(smem, kt & 1, p, m0, n0, 0);
-            ++kt;
-        }
-        t.template tile<false, false, false>(smem, kt & 1, p, m0, n0, 0);
-    }
+    staged_mainloop<T, BK>(t, smem, p, m0, n0);
     if constexpr (EPI) {
         store_tile_via_lds<TO, BM, BN, T::NT, T::TM * T::TN * 4, 2 * T::STAGE>(
             p, smem, m0, n0, t.tid, [&](int v) { return t.acc[v / (T::TN * 4)][(v / 4) % T::TN][v % 4]; },

@@ -309,6 +309,63 @@ int gemm_run_grouped_k(int64_t M, int64_t N, int64_t K, char a_major, char b_maj
                        int64_t groups, int64_t stride_c, const int32_t* ends, int accumulate,
                        void* stream);
 
+/*
+ * A shared projection beside the low-rank adapters of many requests:
+ *
+ *     C[m][n] = sum_k A[m][k] B[n][k] + scales[i] * sum_r v[m][r] up_i[n][r]
+ *     v[m][r] = sum_k A[m][k] down_i[r][k]          r < ranks[i], i = ids[m]
+ *
+ * Every row m of A (a token) names its adapter; rows of different adapters may
+ * stand in any order, and a row whose id is outside [0, adapters) has none.
+ * One call serves packed prompts and single tokens alike.  Adapters live in
+ * slots of equal size: slot i holds down_i (rank x K) at down +
+ * i*stride_down, element (r, k) at r*ld_down + k, and up_i (N x rank) at up +
+ * i*stride_up, element (n, r) at n*ld_up + r, both in the input type.  A slot
+ * may use fewer columns than `rank`: what it holds past ranks[i] (clamped to
+ * [0, rank]) is not used.
+ */
+typedef struct {
+    int64_t adapters;          /* slots (at most 2^20); 0: no adapters              */
+    int64_t rank;              /* largest rank (at most 4096); 0: no adapters       */
+    const void* down;
+    const void* up;
+    int64_t ld_down, ld_up;    /* elements */
+    int64_t stride_down, stride_up;   /* elements; may be 0 (one adapter in every slot) */
+    const int32_t* ids;        /* device array, M: the slot of each row             */
+    const int32_t* ranks;      /* device array, adapters: the slot's rank; NULL: rank */
+    const float* scales;       /* device array, adapters: the slot's factor; NULL: 1 */
+} gemm_lora_t;
+
+/*
+ * The product above, rounded once.  a_major 'k', c_major 'n' (else
+ * GEMM_ERR_BAD_MAJOR), b_major 'k' or 'n'.  v and all sums are fp32; v enters
+ * the second product as two terms of the input type (22 bits for fp16, 16 for
+ * bf16).  Infinities and NaN in one slot reach only the rows that use it.
+ * lora NULL, adapters 0, rank 0 or K 0 is the plain product.
+ *
+ * workspace: at least gemm_lora_workspace_size() bytes of device memory,
+ * 16-byte aligned, that hold v between the two kernels of the call; no
+ * initialisation.  Too small: GEMM_ERR_WORKSPACE.  Calls that may run at the
+ * same time (streams, captured graphs) need different workspaces.  The host
+ * reads none of ids, ranks and scales: nothing synchronises, and a captured
+ * call takes what the arrays hold at each replay.  The workspace, the adapters
+ * and the three arrays must not overlap C, nor the workspace any input
+ * (GEMM_ERR_ALIAS).  Sizes, alignment (any operand that is not 16-byte
+ * aligned: all run element by element), the checks and their order, asynchrony
+ * and errors are otherwise those of gemm_run_ws; results are deterministic.
+ */
+int gemm_run_lora(int64_t M, int64_t N, int64_t K, char a_major, char b_major, char c_major,
+                  int dtype, const void* A, const void* B, void* C,
+                  int64_t lda, int64_t ldb, int64_t ldc, const gemm_lora_t* lora,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of workspace for gemm_run_lora with up to M rows and that N, K, type
+ * and largest rank, written to *bytes.  Host only.  Returns GEMM_OK,
+ * GEMM_ERR_NULL_PTR (bytes NULL), GEMM_ERR_BAD_SHAPE or GEMM_ERR_BAD_DTYPE.
+ */
+int gemm_lora_workspace_size(int64_t M, int64_t N, int64_t K, int dtype, int64_t rank, size_t* bytes);
+
 /* Static description of a status code; never NULL. */
 const char* gemm_status_str(int status);
 

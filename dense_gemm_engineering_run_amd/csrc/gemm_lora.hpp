@@ -108,12 +108,14 @@ lora_shrink_kernel(Params p, Lora q)
             auto body = [&](auto NJ) {
                 constexpr int n = decltype(NJ)::value;
                 constexpr int UN = 4;                  // steps in flight
-                for (int s = s0 + wave; s < s1; s += 4 * UN) {
+                // A wave's steps are neighbours: a row's 64 bytes per step share
+                // cache lines with the next step's.
+                for (int s = s0 + wave * UN; s < s1; s += 4 * UN) {
                     i32x4 fa[UN], fd[UN][n];
 #pragma unroll
                     for (int t = 0; t < UN; ++t) {
-                        const int k = (s + 4 * t) * KS + (lane / 16) * CE;
-                        const bool in = s + 4 * t < s1 && k < p.K;
+                        const int k = (s + t) * KS + (lane / 16) * CE;
+                        const bool in = s + t < s1 && k < p.K;
                         fa[t] = load_chunk<ES, VEC>(ra, in ? aoff + k * ES : -16);       // past the extent: zeros
 #pragma unroll
                         for (int j = 0; j < n; ++j)
@@ -121,7 +123,7 @@ lora_shrink_kernel(Params p, Lora q)
                     }
 #pragma unroll
                     for (int t = 0; t < UN; ++t) {
-                        const int k = (s + 4 * t) * KS + (lane / 16) * CE;
+                        const int k = (s + t) * KS + (lane / 16) * CE;
                         if (k + CE > p.K) {            // the chunk that holds K: zeros from K on
                             fa[t] = mask_k<TI>(fa[t], k, p.K);
 #pragma unroll
@@ -147,6 +149,58 @@ lora_shrink_kernel(Params p, Lora q)
                 const float sum = ((part[0][m][r] + part[1][m][r]) + part[2][m][r]) + part[3][m][r];
                 out[(int64_t)m * q.pitch + r0 + r] = r < left ? sum : 0.f;
             }
+        }
+    }
+}
+
+// The same for many rows: 64 rows and 64 columns of v per workgroup on the
+// direct-to-LDS ring, so that each cache line of A and of the adapter is asked
+// for whole and once per workgroup (the fragments straight from memory above
+// ask for 64 bytes of 16 rows at a time: 41 us at 4096 rows, K = 4096, rank
+// 64, where this form takes SHRINK_US).
+template <In TI>
+using ShrinkTile = Dma16<TI, Out::F32, 64, 64, 64, 2, 2, 16, 4, true, true>;
+
+template <In TI>
+__global__ void __launch_bounds__(256)
+lora_shrink_dma_kernel(Params p, Lora q)
+{
+    using KT = ShrinkTile<TI>;
+    __shared__ __attribute__((aligned(1024))) char smem[KT::SMEM];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int m0 = blockIdx.x * 64, split = blockIdx.y;
+    const int nkt = (p.K + 63) / 64;
+    const int kt0 = (int)((int64_t)nkt * split / q.splits), kt1 = (int)((int64_t)nkt * (split + 1) / q.splits);
+    Distinct d(q, m0 + lane, m0 + lane < p.M);
+    typename KT::OA oa;
+    typename KT::OB ob;
+    oa.init(wave, lane, p.lda);
+    ob.init(wave, lane, q.ld_down);
+    p.ldb = q.ld_down;
+    float* const out = q.v + ((int64_t)split * p.M + m0) * q.pitch;
+    for (int u = 0;; ++u) {
+        uint64_t rows;
+        const int a = d.next(rows);
+        if (a < 0) break;
+        if (u % q.z != (int)blockIdx.z) continue;
+        const int rank = lora_rank(q, a);
+        for (int r0 = 0; r0 < q.pitch; r0 += 64) {
+            const int left = max(0, min(rank - r0, 64));
+            p.B = q.down + a * q.s_down + (int64_t)r0 * q.ld_down * 2;
+            p.b_bytes = rows_extent(left, q.ld_down * 2, row_tail<2, true>(p.K));
+            typename KT::Acc acc;
+            KT::zero(acc);
+            bare_barrier();               // no wave reads the ring any more
+            if (left) KT::mainloop(p, smem, oa, ob, m0, 0, kt0, kt1, acc, tid, lane, wave);
+#pragma unroll
+            for (int i = 0; i < KT::TM; ++i)
+#pragma unroll
+                for (int j = 0; j < KT::TN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int m = KT::row(wave / 2, i, e, lane), r = KT::col(wave % 2, j, lane);
+                        if ((rows >> m & 1) && r0 + r < q.pitch) out[(int64_t)m * q.pitch + r0 + r] = r < left ? acc[i][j][e] : 0.f;
+                    }
         }
     }
 }
@@ -433,26 +487,37 @@ struct LoraCall {
     Lora q;
     bool b_kmajor;
     bool vec;             // A, B and the adapters allow 16-byte loads
+    int shrink_rows;      // ShrinkPlan::rows
 };
 
-// Ranges of k that v is computed in, and workgroups per row tile: enough
-// workgroups for the chip where the rows alone are too few, with at least 256
-// k to a range.
+// How v is computed: rows per workgroup, ranges of k (their partial sums add
+// up where v is used) and workgroups sharing a row tile's adapters.  From 128
+// rows up the 64-row tile; below, the 16-row one, with a workgroup per adapter
+// and enough ranges of k, at least 256 long, to fill the chip.
 struct ShrinkPlan {
-    int splits, z;
+    int rows, splits, z;
 };
-inline ShrinkPlan shrink_plan(int64_t M, int64_t K)
+inline ShrinkPlan shrink_plan(int64_t M, int64_t K, bool tiled)
 {
-    const int64_t tiles = (M + kShrinkRows - 1) / kShrinkRows;
     ShrinkPlan s;
-    const int64_t rows = M < kShrinkRows ? M : kShrinkRows;
-    s.z = (int)(tiles >= 64 ? 1 : rows);
-    int64_t n = 512 / (tiles * s.z);
+    tiled = tiled && M >= 128;
+    s.rows = tiled ? 64 : kShrinkRows;
+    const int64_t tiles = (M + s.rows - 1) / s.rows;
+    int64_t n;
+    if (tiled) {
+        s.z = 2;
+        n = 256 / tiles;
+    } else {
+        s.z = (int)(tiles >= 64 ? 1 : M < kShrinkRows ? M : kShrinkRows);
+        n = 512 / (tiles * s.z);
+    }
     if (n > 8) n = 8;
     if (n > K / 256) n = K / 256;
     s.splits = (int)(n < 1 ? 1 : n);
     return s;
 }
+// The 64-row tile is for 16-bit operands that allow 16-byte loads.
+inline bool shrink_tiled(int in_bytes, bool vec) { return in_bytes == 2 && vec; }
 
 template <class Kernel>
 hipError_t launch_lora(Kernel kernel, const LoraCall& c, int BM, int BN, int threads, hipStream_t s)
@@ -472,7 +537,10 @@ hipError_t launch_shrink(const LoraCall& c, hipStream_t s)
     Params p = c.p;
     Lora q = c.q;
     void* args[] = {&p, &q};
-    const dim3 grid((unsigned)((p.M + kShrinkRows - 1) / kShrinkRows), (unsigned)q.splits, (unsigned)q.z);
+    const int rows = c.shrink_rows;
+    const dim3 grid((unsigned)((p.M + rows - 1) / rows), (unsigned)q.splits, (unsigned)q.z);
+    if constexpr (TI != In::F32)
+        if (rows == 64) return hipLaunchKernel((const void*)&lora_shrink_dma_kernel<TI>, grid, dim3(256), args, 0, s);
     const void* kernel = c.vec ? (const void*)&lora_shrink_kernel<TI, true> : (const void*)&lora_shrink_kernel<TI, false>;
     return hipLaunchKernel(kernel, grid, dim3(256), args, 0, s);
 }

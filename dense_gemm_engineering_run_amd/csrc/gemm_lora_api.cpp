@@ -28,19 +28,23 @@ bool bad_shape(int64_t M, int64_t N, int64_t K, int64_t rank)
     return M < 0 || N < 0 || K < 0 || rank < 0 || M > mg::kMaxDim || N > mg::kMaxDim || K > mg::kMaxDim || rank > kMaxRank;
 }
 
-uint64_t workspace(int64_t M, int64_t N, int64_t K, int64_t rank)
+uint64_t workspace(int64_t M, int64_t N, int64_t K, int64_t rank, bool tiled)
 {
     if (M == 0 || N == 0 || K == 0 || rank == 0) return 0;
-    return (uint64_t)mg::shrink_plan(M, K).splits * M * pitch(rank) * 4;
+    return (uint64_t)mg::shrink_plan(M, K, tiled).splits * M * pitch(rank) * 4;
 }
 
-// The most that any call of at most M rows needs: the ranges of k grow fewer
-// as the tiles of rows grow more, so fewer rows can need more.
-uint64_t workspace_up_to(int64_t M, int64_t N, int64_t K, int64_t rank)
+// The most that any call of at most M rows needs, whatever its alignment: the
+// ranges of k grow fewer as the tiles of rows grow more, so fewer rows can
+// need more.
+uint64_t workspace_up_to(int64_t M, int64_t N, int64_t K, int dtype, int64_t rank)
 {
-    uint64_t most = workspace(M, N, K, rank);
-    for (int64_t m = mg::kShrinkRows; m < std::min<int64_t>(M, 513 * mg::kShrinkRows); m += mg::kShrinkRows)
-        most = std::max(most, workspace(m, N, K, rank));
+    uint64_t most = 0;
+    for (int tiled = 0; tiled <= (mg::in_bytes(dtype) == 2); ++tiled) {
+        most = std::max(most, workspace(M, N, K, rank, tiled));
+        for (int64_t m = mg::kShrinkRows; m < std::min<int64_t>(M, 1 << 14); m += mg::kShrinkRows)
+            most = std::max(most, std::max(workspace(m - 1, N, K, rank, tiled), workspace(m, N, K, rank, tiled)));
+    }
     return most;
 }
 
@@ -76,7 +80,7 @@ int run(int64_t M, int64_t N, int64_t K, char a, char b, char c, int dtype, cons
                  (((uintptr_t)l.ids | (uintptr_t)l.ranks | (uintptr_t)l.scales) & 3)))
         return GEMM_ERR_MISALIGNED;
     const bool vec = !reads || (oa.aligned(16) && ob.aligned(16) && (!with || (od.aligned(16) && ou.aligned(16))));
-    const uint64_t cn = oc.bytes(false), need = with ? workspace(M, N, K, l.rank) : 0;
+    const uint64_t cn = oc.bytes(false), need = with ? workspace(M, N, K, l.rank, mg::shrink_tiled(es, vec)) : 0;
     // What is read, against what is written: C and the part of the workspace in use.
     const struct { const void* p; uint64_t n; } in[] = {
         {A, reads ? oa.bytes(vec) : 0}, {B, reads ? ob.bytes(vec) : 0},
@@ -103,7 +107,8 @@ int run(int64_t M, int64_t N, int64_t K, char a, char b, char c, int dtype, cons
     p.b_bytes = reads ? ob.bytes(vec) : 0;
     p.c_vec = oc.aligned(16);
     if (with) {
-        const mg::ShrinkPlan s = mg::shrink_plan(M, K);
+        const mg::ShrinkPlan s = mg::shrink_plan(M, K, mg::shrink_tiled(es, vec));
+        q.shrink_rows = s.rows;
         q.q = mg::Lora{(const char*)l.down, (const char*)l.up, l.ids, l.ranks, l.scales, (float*)ws,
                        l.stride_down * es, l.stride_up * es, l.ld_down, l.ld_up,
                        (int)l.adapters, (int)l.rank, (int)pitch(l.rank), s.splits, s.z};
@@ -138,7 +143,7 @@ int gemm_lora_workspace_size(int64_t M, int64_t N, int64_t K, int dtype, int64_t
     *bytes = 0;
     if (bad_shape(M, N, K, rank)) return GEMM_ERR_BAD_SHAPE;
     if (dtype < 0 || dtype >= GEMM_NUM_DTYPES) return GEMM_ERR_BAD_DTYPE;
-    *bytes = (size_t)workspace_up_to(M, N, K, rank);
+    *bytes = (size_t)workspace_up_to(M, N, K, dtype, rank);
     return GEMM_OK;
 }
 

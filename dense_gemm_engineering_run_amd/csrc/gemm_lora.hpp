@@ -18,6 +18,8 @@
 // read.
 #pragma once
 
+#include <cstdlib>
+
 #include "gemm_ragged.hpp"
 
 namespace mg {
@@ -41,29 +43,38 @@ constexpr int kRankStep = 32;
 // Rows of v one workgroup computes.
 constexpr int kShrinkRows = 16;
 
-__device__ __forceinline__ int lora_rank(const Lora& q, int a)
-{
-    return q.ranks ? min(max(q.ranks[a], 0), q.R) : q.R;
-}
-
-// The distinct adapters of up to 64 rows, one lane each: `next` gives an
-// adapter and the rows (bits) that have it.
+// The distinct adapters of up to 64 rows, one lane each.  A lane fetches its
+// own row's rank and scale, so that the walk over the adapters waits for no
+// memory.
+struct Adapter {
+    int id;               // -1: none
+    int rank;
+    float scale;
+    uint64_t rows;        // the rows that have it
+};
 struct Distinct {
-    int id;               // this lane's row's adapter, or -1
+    int id, rank;         // of this lane's row; id -1: none
+    float scale;
     uint64_t left;
 
     __device__ __forceinline__ Distinct(const Lora& q, int row, bool valid)
     {
         id = valid ? q.ids[row] : -1;
         if (id >= q.slots) id = -1;
+        rank = id >= 0 && q.ranks ? min(max(q.ranks[id], 0), q.R) : q.R;
+        scale = id >= 0 && q.scales ? q.scales[id] : 1.f;
         left = __builtin_amdgcn_ballot_w64(id >= 0);
     }
-    __device__ __forceinline__ int next(uint64_t& rows)
+    __device__ __forceinline__ Adapter next()
     {
-        if (!left) { rows = 0; return -1; }
-        const int a = __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(left));
-        rows = __builtin_amdgcn_ballot_w64(id == a);
-        left &= ~rows;
+        if (!left) return {-1, 0, 0.f, 0};
+        const int l = (int)__builtin_ctzll(left);
+        Adapter a;
+        a.id = __builtin_amdgcn_readlane(id, l);
+        a.rank = __builtin_amdgcn_readlane(rank, l);
+        a.scale = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale), l));
+        a.rows = __builtin_amdgcn_ballot_w64(id == a.id);
+        left &= ~a.rows;
         return a;
     }
 };
@@ -91,17 +102,15 @@ lora_shrink_kernel(Params p, Lora q)
     const int aoff = (int)((lane % 16) * p.lda * ES);
     float* const out = q.v + ((int64_t)split * p.M + m0) * q.pitch;
     for (int u = 0;; ++u) {
-        uint64_t rows;
-        const int a = d.next(rows);
-        if (a < 0) break;
+        const Adapter a = d.next();
+        if (a.id < 0) break;
         if (u % q.z != (int)blockIdx.z) continue;
-        const int rank = lora_rank(q, a);
         for (int r0 = 0; r0 < q.pitch; r0 += RJ * 16) {
             f32x4 acc[RJ];
 #pragma unroll
             for (int j = 0; j < RJ; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-            const int left = max(0, min(rank - r0, RJ * 16));
-            const __amdgpu_buffer_rsrc_t rd = make_rsrc(q.down + a * q.s_down + (int64_t)r0 * q.ld_down * ES,
+            const int left = max(0, min(a.rank - r0, RJ * 16));
+            const __amdgpu_buffer_rsrc_t rd = make_rsrc(q.down + a.id * q.s_down + (int64_t)r0 * q.ld_down * ES,
                                                         rows_extent(left, q.ld_down * ES, row_tail<ES, VEC>(p.K)));
             const int doff = (int)((lane % 16) * q.ld_down * ES);
             const int nj = (left + 15) / 16;
@@ -145,7 +154,7 @@ lora_shrink_kernel(Params p, Lora q)
             __syncthreads();
             for (int x = tid; x < kShrinkRows * RJ * 16; x += 256) {
                 const int m = x / (RJ * 16), r = x % (RJ * 16);
-                if (!(rows >> m & 1) || r0 + r >= q.pitch) continue;
+                if (!(a.rows >> m & 1) || r0 + r >= q.pitch) continue;
                 const float sum = ((part[0][m][r] + part[1][m][r]) + part[2][m][r]) + part[3][m][r];
                 out[(int64_t)m * q.pitch + r0 + r] = r < left ? sum : 0.f;
             }
@@ -179,14 +188,12 @@ lora_shrink_dma_kernel(Params p, Lora q)
     p.ldb = q.ld_down;
     float* const out = q.v + ((int64_t)split * p.M + m0) * q.pitch;
     for (int u = 0;; ++u) {
-        uint64_t rows;
-        const int a = d.next(rows);
-        if (a < 0) break;
+        const Adapter a = d.next();
+        if (a.id < 0) break;
         if (u % q.z != (int)blockIdx.z) continue;
-        const int rank = lora_rank(q, a);
         for (int r0 = 0; r0 < q.pitch; r0 += 64) {
-            const int left = max(0, min(rank - r0, 64));
-            p.B = q.down + a * q.s_down + (int64_t)r0 * q.ld_down * 2;
+            const int left = max(0, min(a.rank - r0, 64));
+            p.B = q.down + a.id * q.s_down + (int64_t)r0 * q.ld_down * 2;
             p.b_bytes = rows_extent(left, q.ld_down * 2, row_tail<2, true>(p.K));
             typename KT::Acc acc;
             KT::zero(acc);
@@ -199,7 +206,7 @@ lora_shrink_dma_kernel(Params p, Lora q)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int m = KT::row(wave / 2, i, e, lane), r = KT::col(wave % 2, j, lane);
-                        if ((rows >> m & 1) && r0 + r < q.pitch) out[(int64_t)m * q.pitch + r0 + r] = r < left ? acc[i][j][e] : 0.f;
+                        if ((a.rows >> m & 1) && r0 + r < q.pitch) out[(int64_t)m * q.pitch + r0 + r] = r < left ? acc[i][j][e] : 0.f;
                     }
         }
     }
@@ -251,10 +258,11 @@ struct VFrag {
 // Add scale_i v up_i^T to the accumulators of one wave.  Its rows are m0 ..
 // m0 + TM * MI - 1 (at most 64), its columns start at n0; MFMA tile (i, j)
 // holds rows i * MI and columns j * MI on.  NB: adapters whose loads are
-// in flight together.
+// in flight together.  Of the rows' distinct adapters, those with an index of
+// `share` modulo `shares` are added (all: 0 of 1).
 template <In TI, bool VEC, int NB, int MI, int TM, int TN, class AccT>
 __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&acc)[TM][TN], int m0, int n0, int lane,
-                                         float* tab = nullptr)
+                                         float* tab, int share = 0, int shares = 1)
 {
     constexpr int ES = TI == In::F32 ? 4 : 2, CE = 16 / ES, KS = 64 / MI * CE, R4 = MI == 32 ? 16 : 4;
     constexpr bool BIG = TM * TN * R4 >= 128;          // accumulators that leave few registers
@@ -262,19 +270,16 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
     constexpr int NK = CH / KS;
     static_assert(TM * MI <= 64, "one lane per row");
     if (q.slots == 0 || q.R == 0) return;
-    Distinct d(q, m0 + lane, lane < TM * MI && m0 + lane < p.M);
-    if (!d.left) return;
-    const uint64_t all = d.left;
     const int fr = lane % MI, fk = lane / MI * CE;     // fragment row, first k
     const int up_row = (int)(q.ld_up * ES);            // (256 rows fit 32 bits)
     const int64_t vsplit = (int64_t)p.M * q.pitch * 4;
+    const uint64_t vbytes = (uint64_t)max(0, min(p.M - m0, TM * MI)) * q.pitch * 4;
     auto load_v = [&](int i, int r, float (&v)[CE]) {
 #pragma unroll
         for (int e = 0; e < CE; ++e) v[e] = 0.f;
         const int off = r + fk < q.pitch ? ((i * MI + fr) * q.pitch + r + fk) * 4 : -16;
         for (int s = 0; s < q.splits; ++s) {
-            const __amdgpu_buffer_rsrc_t rs = make_rsrc((const char*)(q.v + (int64_t)m0 * q.pitch) + s * vsplit,
-                                                        (uint64_t)min(p.M - m0, TM * MI) * q.pitch * 4);
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc((const char*)(q.v + (int64_t)m0 * q.pitch) + s * vsplit, vbytes);
 #pragma unroll
             for (int e = 0; e < CE; e += 4) {
                 const i32x4 t = buf_load16(rs, off + e * 4);
@@ -283,6 +288,9 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
             }
         }
     };
+    Distinct d(q, m0 + lane, lane < TM * MI && m0 + lane < p.M);
+    if (!d.left) return;
+    const uint64_t all = d.left;
     // fp16: v is scaled by a power of two per row that brings its largest
     // finite value to 2^13 .. 2^14, so that neither part leaves fp16's range.
     // The factors stand in LDS (tab: 128 floats of this wave's own): 2^-e of
@@ -330,18 +338,23 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
                 fv[i][k].set(v);
             }
         d.left = all;
+        int turn = 0;                                  // distinct adapters so far, modulo shares
+        auto mine = [&]() {
+            for (;;) {
+                const Adapter a = d.next();
+                const bool take = turn == share;
+                turn = turn + 1 == shares ? 0 : turn + 1;
+                if (a.id < 0 || take) return a;
+            }
+        };
         while (d.left) {
-            uint64_t rows[NB];
-            int rank[NB];
-            float scale[NB];
+            Adapter a[NB];
             __amdgpu_buffer_rsrc_t ru[NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const int a = d.next(rows[b]);
-                rank[b] = a < 0 ? 0 : lora_rank(q, a);
-                scale[b] = a < 0 ? 0.f : q.scales ? q.scales[a] : 1.f;
-                ru[b] = make_rsrc(q.up + max(a, 0) * q.s_up + (int64_t)n0 * q.ld_up * ES,
-                                  a < 0 || n0 >= p.N ? 0 : rows_extent(min(p.N - n0, TN * MI), q.ld_up * ES, row_tail<ES, VEC>(q.R)));
+                a[b] = mine();
+                ru[b] = make_rsrc(q.up + max(a[b].id, 0) * q.s_up + (int64_t)n0 * q.ld_up * ES,
+                                  a[b].id < 0 || n0 >= p.N ? 0 : rows_extent(min(p.N - n0, TN * MI), q.ld_up * ES, row_tail<ES, VEC>(q.R)));
             }
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
@@ -352,29 +365,29 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
 #pragma unroll
                     for (int k = 0; k < NK; ++k) {
                         const int r = r0 + k * KS + fk;
-                        fu[b][k] = load_chunk<ES, VEC>(ru[b], r < rank[b] ? fr * up_row + r * ES + j * MI * up_row : -16);
+                        fu[b][k] = load_chunk<ES, VEC>(ru[b], r < a[b].rank ? fr * up_row + r * ES + j * MI * up_row : -16);
                     }
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    if (r0 >= rank[b]) continue;
+                    if (r0 >= a[b].rank) continue;
 #pragma unroll
                     for (int k = 0; k < NK; ++k) {
                         const int r = r0 + k * KS + fk;
-                        if (r + CE > rank[b]) fu[b][k] = mask_k<TI>(fu[b][k], r, rank[b]);
+                        if (r + CE > a[b].rank) fu[b][k] = mask_k<TI>(fu[b][k], r, a[b].rank);
                     }
 #pragma unroll
                     for (int i = 0; i < TM; ++i) {
                         AccT t = {};
 #pragma unroll
                         for (int k = 0; k < NK; ++k) {
-                            if (r0 + k * KS >= rank[b]) continue;
+                            if (r0 + k * KS >= a[b].rank) continue;
 #pragma unroll
                             for (int h = 0; h < VFrag<TI>::N; ++h) mfma_step<TI, MI>(fv[i][k].f[h], fu[b][k], t);
                         }
 #pragma unroll
                         for (int x4 = 0; x4 < R4; x4 += 4) {
                             const int row4 = i * MI + (MI == 32 ? x4 / 4 * 8 + (lane / 32) * 4 : (lane / 16) * 4);
-                            f32x4 f = {scale[b], scale[b], scale[b], scale[b]};
+                            f32x4 f = {a[b].scale, a[b].scale, a[b].scale, a[b].scale};
                             if constexpr (TI == In::F16) {
                                 const f32x4 down = *(const f32x4*)(tab + row4);
 #pragma unroll
@@ -383,7 +396,7 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
                                 const float y = __builtin_fmaf(f[x], t[x4 + x], acc[i][j][x4 + x]);
-                                acc[i][j][x4 + x] = rows[b] >> (row4 + x) & 1 ? y : acc[i][j][x4 + x];
+                                acc[i][j][x4 + x] = a[b].rows >> (row4 + x) & 1 ? y : acc[i][j][x4 + x];
                             }
                         }
                     }
@@ -392,6 +405,303 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
         }
     }
 }
+
+// The same for a whole workgroup on 16-bit inputs, through LDS (the ring, free
+// after the main loop): v of the tile's rows, scaled and split, is put there
+// once for all waves, and each adapter's rows for the tile's columns come in
+// by direct loads, one adapter ahead of the one that is multiplied.  The MFMAs
+// add straight into the accumulators (temporaries beside the 256x256 tile's
+// accumulators spilled); rows of other adapters enter them as zeros.  That
+// keeps rows apart only while the adapter is finite, so infinities and NaN in
+// it are replaced by zeros in LDS and reported: `repair` then adds their terms
+// to the stored C, for the adapter's own rows.  Measured at 4096 rows, N = K =
+// 4096, rank 64 in bf16: the product with its adapters 121 us by lora_add,
+// whose every adapter waits for its own loads, SHARED_US here (plain 97).
+template <class KT, In TI>
+struct SharedLora {
+    static constexpr int BM = KT::TILE_M, BN = KT::TILE_N, NW = KT::NW, NT = KT::NT, MI = 16;
+    static constexpr int TM = KT::TM, TN = KT::TN, WTM = KT::WTM, WTN = KT::WTN, WN = BN / WTN;
+    static constexpr int CH = 64, NG = 2;              // columns of v at a time, in MFMA steps
+    using OV = DmaOperand<BM, CH, NW, true, MI>;       // for its fragments
+    using OU = DmaOperand<BN, CH, NW, true, MI>;
+    static constexpr int V_BYTES = BM * CH * 2, U_BYTES = OU::BYTES;
+    static constexpr int TAB = 2 * V_BYTES + 2 * U_BYTES, PROP = TAB + BM * 8, BAD = PROP + 2 * NW * 8;
+    static_assert(BAD + 16 <= KT::SMEM, "fits the ring");
+    static_assert(WTM <= 64, "one lane per row");
+
+    // True: an adapter held infinities or NaN (repair has work).
+    __device__ static __forceinline__ bool add(const Params& p, const Lora& q, char* smem, typename KT::Acc& acc, int m0,
+                                               int n0, int tid, int lane, int wave)
+    {
+        if (q.slots == 0 || q.R == 0) return false;
+        const int wm = wave / WN, wn = wave % WN;
+        char* const vh = smem;
+        char* const vl = smem + V_BYTES;
+        float* const tab = (float*)(smem + TAB);       // fp16: 2^e of each row, then 2^-e
+        int* const prop = (int*)(smem + PROP);
+        int* const bad = (int*)(smem + BAD);
+        const int row = m0 + wm * WTM + lane;
+        const bool valid = lane < WTM && row < p.M;
+        Distinct d(q, row, valid);
+        const uint64_t all = d.left;
+        // The workgroup's next adapter: the first wave that has one left names it.
+        int parity = 0;
+        auto select = [&](int& rank) {
+            int* const at = prop + parity * 2 * NW;
+            parity ^= 1;
+            if (lane == 0) {
+                const int l = d.left ? (int)__builtin_ctzll(d.left) : 0;
+                const int id = __builtin_amdgcn_readlane(d.id, l), rk = __builtin_amdgcn_readlane(d.rank, l);
+                at[2 * wave] = d.left ? id : -1;
+                at[2 * wave + 1] = rk;
+            }
+            __syncthreads();
+            int a = -1;
+            rank = 0;
+#pragma unroll
+            for (int w = NW - 1; w >= 0; --w) {
+                const int id = at[2 * w], rk = at[2 * w + 1];
+                if (id >= 0) {
+                    a = id;
+                    rank = rk;
+                }
+            }
+            a = __builtin_amdgcn_readfirstlane(a);
+            rank = __builtin_amdgcn_readfirstlane(rank);
+            return a;
+        };
+        OU ou;
+        ou.init(wave, lane, q.ld_up);
+        auto issue = [&](int a, int left, int r0, char* dst) {
+            OU o;
+#pragma unroll
+            for (int j = 0; j < OU::IPW; ++j) {
+                const int slot = (wave * OU::IPW + j) * 64 + lane;
+                const int c = swz_chunk<OU::CPR, true>(slot / OU::CPR, slot % OU::CPR);
+                o.voff[j] = c * 8 < left ? ou.voff[j] : -16;          // past the rank: zeros
+            }
+            o.issue(q.up + a * q.s_up + (int64_t)n0 * q.ld_up * 2 + r0 * 2,
+                    rows_extent(min(p.N - n0, BN), q.ld_up * 2, row_tail<2, true>(q.R - r0)), q.ld_up, 0, 0, dst, wave);
+        };
+        bool found = false, first = true;
+        for (int r0 = 0; r0 < q.pitch; r0 += CH) {
+            bare_barrier();                            // LDS is free
+            if (tid == 0) *bad = 0;
+            d.left = all;
+            int rank;
+            int a = select(rank);
+            if (a < 0) return false;
+            int left = min(rank - r0, CH);
+            issue(a, left, r0, smem + 2 * V_BYTES);
+            stage_v(p, q, vh, vl, tab, m0, r0, tid);
+            int buf = 0;
+            for (;;) {
+                const uint64_t rows = __builtin_amdgcn_ballot_w64(d.id == a);
+                d.left &= ~rows;
+                int next_rank;
+                const int next = select(next_rank);    // its barrier: v is staged, the other buffer read
+                if (first) rescale(acc, tab, wm, lane);
+                first = false;
+                char* const u = smem + 2 * V_BYTES + buf * U_BYTES;
+                const int next_left = min(next_rank - r0, CH);
+                if (next >= 0) {
+                    issue(next, next_left, r0, smem + 2 * V_BYTES + (buf ^ 1) * U_BYTES);
+                    wait_vmcnt<OU::IPW>();
+                } else {
+                    wait_vmcnt<0>();
+                }
+                bare_barrier();
+                if (left > 0) {
+                    if (left % 8) {                    // zeros from the rank on in the chunk that holds it
+                        OU::template zero_tail<NT>(u, left, tid);
+                        __syncthreads();
+                    }
+                    clean(u, left, bad, tid);
+                    __syncthreads();
+                    if (rows) multiply(acc, vh, vl, u, rows, left, wm, wn, lane);
+                }
+                if (next < 0) break;
+                a = next;
+                left = next_left;
+                buf ^= 1;
+            }
+            found = found || *bad;
+        }
+        rescale(acc, tab + BM, wm, lane);
+        return found;
+    }
+
+    // fp16: the accumulators' rows by the power of two of each row of v (2^64
+    // at most: no product of fp16 values over 2^30 terms leaves fp32 by it).
+    __device__ static __forceinline__ void rescale(typename KT::Acc& acc, const float* tab, int wm, int lane)
+    {
+        if constexpr (TI == In::F16) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const f32x4 f = *(const f32x4*)(tab + wm * WTM + i * MI + lane / 16 * 4);
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) acc[i][j][x] *= f[x];
+            }
+        }
+    }
+
+    // Zeros in the place of the adapter's infinities and NaN; *bad: there were some.
+    __device__ static __forceinline__ void clean(char* u, int left, int* bad, int tid)
+    {
+        constexpr uint32_t EXP = TI == In::F16 ? 0x7c00u : 0x7f80u;
+        for (int x = tid; x < BN * 8; x += NT) {
+            const int row = x / 8, c = x % 8;
+            if (c * 8 >= left) continue;
+            i32x4* const at = (i32x4*)(u + row * 128 + swz_chunk<8, true>(row, c) * 16);
+            i32x4 v = *at;
+            bool any = false;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t d = (uint32_t)v[w];
+                const bool lo = (d & EXP) == EXP, hi = (d >> 16 & EXP) == EXP;
+                any = any || lo || hi;
+                v[w] = (int)(d & (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u));
+            }
+            if (any) {
+                *at = v;
+                *bad = 1;
+            }
+        }
+    }
+
+    // Add the terms of infinite and NaN adapter values to C, which holds the
+    // rest.  Rare, and only for the rows of such an adapter: column by column,
+    // straight from memory.
+    __device__ static __forceinline__ void repair(const Params& p, const Lora& q, int m0, int n0, int tid)
+    {
+        constexpr int EO = KT::OUT == Out::F32 ? 4 : 2;
+        constexpr uint32_t EXP = TI == In::F16 ? 0x7c00u : 0x7f80u;
+        __builtin_amdgcn_s_waitcnt(0);                 // the tile is stored
+        __syncthreads();
+        for (int n = n0 + tid; n < min(n0 + BN, p.N); n += NT) {
+            int last = -1, rank = 0;
+            bool harm = false;
+            for (int m = m0; m < min(m0 + BM, p.M); ++m) {
+                const int id = q.ids[m];
+                if (id < 0 || id >= q.slots) continue;
+                const uint16_t* u = (const uint16_t*)(q.up + id * q.s_up) + (int64_t)n * q.ld_up;
+                if (id != last) {
+                    last = id;
+                    rank = q.ranks ? min(max(q.ranks[id], 0), q.R) : q.R;
+                    harm = false;
+                    for (int r = 0; r < rank; ++r) harm = harm || (u[r] & EXP) == EXP;
+                }
+                if (!harm) continue;
+                float sum = 0.f;
+                for (int r = 0; r < rank; ++r) {
+                    if ((u[r] & EXP) != EXP) continue;
+                    float v = 0.f;
+                    for (int s = 0; s < q.splits; ++s) v += q.v[((int64_t)s * p.M + m) * q.pitch + r];
+                    const float w = TI == In::F16 ? (float)__builtin_bit_cast(_Float16, u[r])
+                                                  : __int_as_float((int)((uint32_t)u[r] << 16));
+                    sum += (q.scales ? q.scales[id] : 1.f) * v * w;
+                }
+                // past this CU's cache: other lanes stored this element
+                const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.C + ((int64_t)m * p.ldc + n) * EO, EO);
+                float c;
+                if constexpr (EO == 4) {
+                    c = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rc, 0, 0, kDeviceCoherent));
+                } else {
+                    const uint16_t h = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rc, 0, 0, kDeviceCoherent);
+                    c = load_out<KT::OUT>((const char*)&h, 0);
+                }
+                store_out<KT::OUT>(p.C, (int64_t)m * p.ldc + n, c + sum);
+            }
+        }
+    }
+
+    // scale * v of the tile's rows, columns r0 .. r0 + 63, as two terms of the
+    // input type in LDS.  fp16 rows are brought to a largest value of 2^13 ..
+    // 2^14 by a power of two (at most 2^64), so that neither term leaves
+    // fp16's range; tab: that power and its inverse.
+    __device__ static __forceinline__ void stage_v(const Params& p, const Lora& q, char* vh, char* vl, float* tab, int m0,
+                                                   int r0, int tid)
+    {
+        static_assert(NT % 16 == 0 && BM * 16 % NT == 0, "16 threads per row");
+        const int c4 = tid % 16 * 4;                   // this thread's 4 columns
+        for (int m = tid / 16; m < BM; m += NT / 16) {
+            const bool in = m0 + m < p.M;
+            const int id = in ? q.ids[m0 + m] : -1;
+            const bool has = id >= 0 && id < q.slots;
+            const float scale = has && q.scales ? q.scales[id] : 1.f;
+            const float* src = q.v + (int64_t)(m0 + m) * q.pitch;
+            auto load = [&](int r) {
+                f32x4 v = {0.f, 0.f, 0.f, 0.f};
+                if (has && r < q.pitch)
+                    for (int s = 0; s < q.splits; ++s) v += *(const f32x4*)(src + (int64_t)s * p.M * q.pitch + r);
+                return v * scale;
+            };
+            f32x4 v = load(r0 + c4);
+            if constexpr (TI == In::F16) {
+                float top = 0.f;
+                auto up_to = [&](f32x4 x) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float y = __builtin_fabsf(x[e]);
+                        if (y < __builtin_inff()) top = fmaxf(top, y);
+                    }
+                };
+                if (q.pitch <= CH) {
+                    up_to(v);
+                } else {
+                    for (int r = c4; r < q.pitch; r += CH) up_to(load(r));
+                }
+#pragma unroll
+                for (int o = 1; o < 16; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
+                int e;
+                __builtin_frexpf(top, &e);
+                e = top > 0.f ? min(14 - e, 64) : 0;
+                if (c4 == 0) {
+                    tab[m] = __builtin_ldexpf(1.f, e);
+                    tab[BM + m] = __builtin_ldexpf(1.f, -e);
+                }
+                v *= __builtin_ldexpf(1.f, e);
+            }
+            VFrag<TI> f;
+            const float x[8] = {v[0], v[1], v[2], v[3], 0.f, 0.f, 0.f, 0.f};
+            f.set(x);
+            const int off = m * 128 + swz_chunk<8, true>(m, c4 / 8) * 16 + c4 % 8 * 2;
+            typedef int i32x2 __attribute__((ext_vector_type(2)));
+            *(i32x2*)(vh + off) = i32x2{f.f[0][0], f.f[0][1]};
+            *(i32x2*)(vl + off) = i32x2{f.f[1][0], f.f[1][1]};
+        }
+    }
+
+    __device__ static __forceinline__ void multiply(typename KT::Acc& acc, const char* vh, const char* vl, const char* u,
+                                                    uint64_t rows, int left, int wm, int wn, int lane)
+    {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            if (g * 32 >= left) break;
+            i32x4 fh[TM], fl[TM];
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const bool own = rows >> (i * MI + lane % MI) & 1;
+                const i32x4 zero = {0, 0, 0, 0};
+                fh[i] = OV::template frag<MI>(vh, wm * WTM + i * MI, g * 32, lane);
+                fl[i] = OV::template frag<MI>(vl, wm * WTM + i * MI, g * 32, lane);
+                fh[i] = own ? fh[i] : zero;
+                fl[i] = own ? fl[i] : zero;
+            }
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                __builtin_amdgcn_sched_barrier(0);
+                const i32x4 f = OU::template frag<MI>(u, wn * WTN + j * MI, g * 32, lane);
+#pragma unroll
+                for (int i = 0; i < TM; ++i) mfma_step<TI, MI>(fh[i], f, acc[i][j]);
+#pragma unroll
+                for (int i = 0; i < TM; ++i) mfma_step<TI, MI>(fl[i], f, acc[i][j]);
+            }
+        }
+    }
+};
 
 // The shared product on the register-staged tile: any type and alignment.
 template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, bool BKM, bool VEC>
@@ -433,7 +743,8 @@ gemm_lora_kernel(Params p, Lora q)
             }
 }
 
-// ... on the direct-to-LDS ring (16-bit inputs).
+// ... on the direct-to-LDS ring (16-bit inputs).  NB: adapters at a time in
+// lora_add; 0: SharedLora.
 template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, int STAGES, int NB, bool BKM>
 __global__ void __launch_bounds__(WM * WN * 64)
 gemm_lora_dma_kernel(Params p, Lora q)
@@ -452,10 +763,119 @@ gemm_lora_dma_kernel(Params p, Lora q)
     oa.init(wave, lane, p.lda);
     ob.init(wave, lane, p.ldb);
     KT::mainloop(p, smem, oa, ob, m0, n0, 0, (p.K + BK - 1) / BK, acc, tid, lane, wave);
-    bare_barrier();       // no wave reads the ring any more
-    lora_add<TI, true, NB, MI, KT::TM, KT::TN>(p, q, acc, m0 + wave / WN * KT::WTM, n0 + wave % WN * KT::WTN, lane,
-                                               (float*)smem + 128 * wave);
+    bool bad = false;
+    if constexpr (NB > 0) {
+        bare_barrier();   // no wave reads the ring any more
+        lora_add<TI, true, NB, MI, KT::TM, KT::TN>(p, q, acc, m0 + wave / WN * KT::WTM, n0 + wave % WN * KT::WTN, lane,
+                                                   (float*)smem + 128 * wave);
+    } else {
+        bad = SharedLora<KT, TI>::add(p, q, smem, acc, m0, n0, tid, lane, wave);
+    }
     store_tile<KT, false>(p, smem, m0, n0, acc, tid, lane, wave);
+    if constexpr (NB == 0)
+        if (bad) SharedLora<KT, TI>::repair(p, q, m0, n0, tid);
+}
+
+// Few rows (a decoding step): the product streams B once and is bound by how
+// many of its bytes are in flight.  A workgroup has 16 MT rows and 16 NT
+// columns.  NW of its waves take the k-tiles in turn, each with a ring of ST
+// tiles of its own in LDS: nothing waits for another wave until the sums meet
+// at the end, in wave order.  A tile's slot is loaded again as soon as its
+// fragments are in registers.  NL more waves share out the rows' adapters: the
+// chain of loads they wait for (ids, then slots, then the adapters) runs
+// beside the stream.
+template <In TI, Out TO, int MT, int NT, int NW, int ST, int NL>
+__global__ void __launch_bounds__((NW + NL) * 64)
+gemm_lora_skinny_kernel(Params p, Lora q)
+{
+    constexpr int BK = 64, MI = 16, NG = 2, NT_ALL = (NW + NL) * 64;
+    using OA = DmaOperand<MT * 16, BK, 1, true, MI>;
+    using OB = DmaOperand<NT * 16, BK, 1, true, MI>;
+    constexpr int STAGE = OA::BYTES + OB::BYTES, L = OA::IPW + OB::IPW;
+    constexpr int PART = MT * 16 * NT * 16;            // sums of a wave
+    constexpr int RING = NW * ST * STAGE;
+    constexpr int NB = (MT * 16 + NL - 1) / NL > 8 ? 8 : (MT * 16 + NL - 1) / NL;   // adapters at a time
+    static_assert((NW + NL) * PART * 4 <= RING && (ST - 1) * L < 64, "sums fit the ring; vmcnt range");
+    static_assert(RING + NL * 512 <= 160 * 1024, "LDS budget");
+    __shared__ __attribute__((aligned(1024))) char smem[RING + NL * 512];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // The row tiles of one column tile sit on one XCD, so that its L2 gives
+    // them the same rows of B.
+    const int rt = p.tiles_m;
+    const int chunk = blockIdx.x / (8 * rt), in = blockIdx.x % (8 * rt);
+    const int tn = chunk * 8 + in % 8;
+    if (tn >= p.tiles_n) return;
+    const int m0 = in / 8 * (MT * 16), n0 = tn * (NT * 16);
+    f32x4 acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (wave >= NW) {
+        lora_add<TI, true, NB, MI, MT, NT>(p, q, acc, m0, n0, lane, (float*)(smem + RING) + 128 * (wave - NW), wave - NW, NL);
+    } else {
+        const int nkt = (p.K + BK - 1) / BK, left = p.K - (nkt - 1) * BK;
+        OA oa;
+        OB ob;
+        oa.init(0, lane, p.lda);
+        ob.init(0, lane, p.ldb);
+        char* const ring = smem + wave * ST * STAGE;
+        auto issue = [&](int t, int slot) {            // past the end: an empty extent, zeros
+            char* s = ring + slot * STAGE;
+            oa.issue(p.A, t < nkt ? p.a_bytes : 0, p.lda, m0, t * BK, s, 0);
+            ob.issue(p.B, t < nkt ? p.b_bytes : 0, p.ldb, n0, t * BK, s + OA::BYTES, 0);
+        };
+#pragma unroll
+        for (int i = 0; i < ST; ++i) issue(wave + i * NW, i);
+        int slot = 0;
+        for (int t = wave; t < nkt; t += NW) {
+            wait_vmcnt<(ST - 1) * L>();
+            char* s = ring + slot * STAGE;
+            if (t == nkt - 1 && left != BK) {
+                oa.template zero_tail<64>(s, left, lane);
+                ob.template zero_tail<64>(s + OA::BYTES, left, lane);
+                __builtin_amdgcn_s_waitcnt(0xc07f);
+            }
+            asm volatile("" ::: "memory");
+            i32x4 fa[NG][MT], fb[NG][NT];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i) fa[g][i] = oa.template frag<MI>(s, i * MI, g * 32, lane);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) fb[g][j] = ob.template frag<MI>(s + OA::BYTES, j * MI, g * 32, lane);
+            }
+            __builtin_amdgcn_s_waitcnt(0xc07f);        // lgkmcnt(0): the slot has been read
+            __builtin_amdgcn_sched_barrier(0);
+            issue(t + ST * NW, slot);
+            slot = slot + 1 == ST ? 0 : slot + 1;
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) mfma_step<TI, MI>(fa[g][i], fb[g][j], acc[i][j]);
+        }
+        wait_vmcnt<0>();                               // the empty loads have landed
+    }
+    __syncthreads();
+    float* const part = (float*)smem;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                part[wave * PART + (i * 16 + lane / 16 * 4 + e) * (NT * 16) + j * 16 + lane % 16] = acc[i][j][e];
+    __syncthreads();
+    for (int x = tid; x < PART; x += NT_ALL) {
+        const int m = m0 + x / (NT * 16), n = n0 + x % (NT * 16);
+        if (m >= p.M || n >= p.N) continue;
+        float v = part[x];
+#pragma unroll
+        for (int w = 1; w < NW + NL; ++w) v += part[w * PART + x];
+        store_out<TO>(p.C, (int64_t)m * p.ldc + n, v);
+    }
 }
 
 // ... on the ping-pong schedule (16-bit inputs, 256x256 tiles).
@@ -474,10 +894,9 @@ gemm_lora_pp_kernel(Params p, Lora q)
     typename KT::Acc acc;
     KT::zero(acc);
     PP::mainloop(p, smem, m0, n0, acc, tid, lane, wave);
-    bare_barrier();       // no wave reads the ring any more
-    lora_add<TI, true, 1, MI, KT::TM, KT::TN>(p, q, acc, m0 + wave / WN * KT::WTM, n0 + wave % WN * KT::WTN, lane,
-                                               (float*)smem + 128 * wave);
+    const bool bad = SharedLora<KT, TI>::add(p, q, smem, acc, m0, n0, tid, lane, wave);
     store_tile<KT, false>(p, smem, m0, n0, acc, tid, lane, wave);
+    if (bad) SharedLora<KT, TI>::repair(p, q, m0, n0, tid);
 }
 
 // ------------------------------------------------------------------ launchers
@@ -531,6 +950,19 @@ hipError_t launch_lora(Kernel kernel, const LoraCall& c, int BM, int BN, int thr
     return hipLaunchKernel((const void*)kernel, dim3((unsigned)((int64_t)p.tiles_m * p.tiles_n)), dim3(threads), args, 0, s);
 }
 
+// The few-row kernel's grid: column tiles in chunks of 8, one per XCD.
+template <class Kernel>
+hipError_t launch_skinny(Kernel kernel, const LoraCall& c, int BM, int BN, int threads, hipStream_t s)
+{
+    Params p = c.p;
+    Lora q = c.q;
+    p.tiles_m = (p.M + BM - 1) / BM;
+    p.tiles_n = (p.N + BN - 1) / BN;
+    void* args[] = {&p, &q};
+    const int64_t grid = (int64_t)(p.tiles_n + 7) / 8 * 8 * p.tiles_m;
+    return hipLaunchKernel((const void*)kernel, dim3((unsigned)grid), dim3(threads), args, 0, s);
+}
+
 template <In TI>
 hipError_t launch_shrink(const LoraCall& c, hipStream_t s)
 {
@@ -565,6 +997,27 @@ struct LoraInst {
             return staged<BKM, true>(c, s);
         } else {
             auto tiles = [&](int t) { return ((int64_t)c.p.M + t - 1) / t * ((c.p.N + t - 1) / t); };
+            if constexpr (BKM) {
+                const char* v = getenv("RV");
+                switch (v ? atoi(v) : 1) {
+                case 0: return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 1, 8, 4, 2>, c, 16, 16, 640, s);
+                case 1: return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 1, 8, 4, 4>, c, 16, 16, 768, s);
+                case 2: return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 2, 2, 8, 2, 4>, c, 32, 32, 768, s);
+                case 3: return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 2, 2, 4, 4, 4>, c, 32, 32, 512, s);
+                case 4: return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 2, 8, 3, 4>, c, 16, 32, 768, s);
+                case 5: return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 2, 1, 8, 3, 4>, c, 32, 16, 768, s);
+                case 6: return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 1, 4, 8, 4>, c, 16, 16, 512, s);
+                case 7: return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 1, 4, 4, 2>, c, 16, 16, 384, s);
+                case 10: return dma<32, 32, 128, 2, 2, 4, 0, BKM>(c, s);
+                case 11: return dma<64, 64, 64, 2, 2, 4, 0, BKM>(c, s);
+                case 12: return dma<128, 128, 64, 2, 2, 4, 0, BKM>(c, s);
+                case 13: return dma<64, 64, 64, 2, 2, 4, 1, BKM>(c, s);
+                case 14: return dma<128, 128, 64, 2, 2, 4, 1, BKM>(c, s);
+                case 15: return launch_lora(&gemm_lora_pp_kernel<TI, TO, BKM>, c, 256, 256, 512, s);
+                case 16: return dma<64, 128, 64, 2, 2, 3, 0, BKM>(c, s);
+                default: break;
+                }
+            }
             if (c.p.M <= 32) return dma<16, 32, 256, 1, 2, 4, 4, BKM>(c, s);
             if (c.p.M <= 96) return dma<32, 32, 128, 2, 2, 4, 4, BKM>(c, s);
             if (tiles(256) >= 100) return launch_lora(&gemm_lora_pp_kernel<TI, TO, BKM>, c, 256, 256, 512, s);

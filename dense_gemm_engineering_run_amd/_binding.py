@@ -7,6 +7,7 @@ been built.
 """
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmi355_gemm.so")
@@ -22,9 +23,9 @@ if not os.path.exists(LIB_PATH):
 # to that one copy; loading the library first would leave two HIP runtimes in
 # the process and kernel launches on torch's memory would fail.
 try:
-    import torch  # noqa: F401
+    import torch
 except ImportError:
-    pass
+    torch = None
 
 _lib = ctypes.CDLL(LIB_PATH)
 
@@ -62,6 +63,10 @@ class Lora(ctypes.Structure):
                 ("ids", ctypes.c_void_p), ("ranks", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
+_LORA = struct.Struct("qqPPqqqqPPP")      # the same, packed in one step
+assert _LORA.size == ctypes.sizeof(Lora)
+
+
 _RUN_ARGS = [_i64, _i64, _i64, _chr, _chr, _chr, _int, _vp, _vp, _vp, _i64, _i64, _i64, _vp]
 _lib.gemm_run.argtypes = _RUN_ARGS
 _lib.gemm_run.restype = _int
@@ -84,7 +89,7 @@ _lib.gemm_run_grouped.argtypes = _GROUPED_ARGS + [_vp]
 _lib.gemm_run_grouped.restype = _int
 _lib.gemm_run_grouped_k.argtypes = _GROUPED_ARGS + [_int, _vp]
 _lib.gemm_run_grouped_k.restype = _int
-_lib.gemm_run_lora.argtypes = _RUN_ARGS[:-1] + [ctypes.POINTER(Lora), _vp, ctypes.c_size_t, _vp]
+_lib.gemm_run_lora.argtypes = _RUN_ARGS[:-1] + [ctypes.c_char_p, _vp, ctypes.c_size_t, _vp]   # gemm_lora_t's bytes
 _lib.gemm_run_lora.restype = _int
 _lib.gemm_lora_workspace_size.argtypes = [_i64, _i64, _i64, _int, _i64, ctypes.POINTER(ctypes.c_size_t)]
 _lib.gemm_lora_workspace_size.restype = _int
@@ -201,8 +206,7 @@ def gemm_run_lora(M, N, K, a_major, b_major, c_major, dtype, A, B, C, lda, ldb, 
                   workspace=0, workspace_bytes=0, stream=0):
     """C ABI gemm_run_lora; `lora` is a Lora or None. Returns the status."""
     return _lib.gemm_run_lora(M, N, K, _c(a_major), _c(b_major), _c(c_major), dtype, A, B, C, lda, ldb, ldc,
-                              ctypes.byref(lora) if lora is not None else None, workspace, workspace_bytes,
-                              stream)
+                              bytes(lora) if lora is not None else None, workspace, workspace_bytes, stream)
 
 
 def gemm_lora_workspace_size(M, N, K, dtype, rank):
@@ -274,15 +278,17 @@ def _major(t, first, second):
     raise ValueError(f"tensor with strides {t.stride()} has no contiguous dimension")
 
 
+_DTYPE_CODES = {} if torch is None else {
+    (torch.float32, torch.float32): DTYPE_F32,
+    (torch.float16, torch.float32): DTYPE_F16_F32,
+    (torch.bfloat16, torch.bfloat16): DTYPE_BF16_BF16,
+    (torch.float16, torch.float16): DTYPE_F16_F16,
+    (torch.bfloat16, torch.float32): DTYPE_BF16_F32}
+
+
 def dtype_code(in_dtype, out_dtype):
-    import torch
-    table = {(torch.float32, torch.float32): DTYPE_F32,
-             (torch.float16, torch.float32): DTYPE_F16_F32,
-             (torch.bfloat16, torch.bfloat16): DTYPE_BF16_BF16,
-             (torch.float16, torch.float16): DTYPE_F16_F16,
-             (torch.bfloat16, torch.float32): DTYPE_BF16_F32}
     try:
-        return table[(in_dtype, out_dtype)]
+        return _DTYPE_CODES[(in_dtype, out_dtype)]
     except KeyError:
         raise ValueError(f"unsupported dtype pair {in_dtype} -> {out_dtype}") from None
 
@@ -325,36 +331,37 @@ def _ld(shape, stride, outer, inner):
     return stride[outer] if stride[outer] >= max(1, shape[inner]) else None
 
 
-def _on_stream(device, stream):
-    """The raw stream to launch on: torch's current one on `device` by default."""
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return getattr(stream, "cuda_stream", stream)
+# The grouped and adapter calls are short, so their checks are kept to what a
+# call has to look at (torch's raw current stream and device: the public
+# objects cost more than the launch).
 
-
-def _same_device(*tensors):
-    device = tensors[0].device
-    if device.type != "cuda" or any(t.device != device for t in tensors):
-        raise ValueError("tensors must be on one GPU: " + ", ".join(str(t.device) for t in tensors))
-    return device
+def _gpu_index(*tensors):
+    """The GPU that holds all the tensors."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != index or index < 0:
+            raise ValueError("tensors must be on one GPU: " + ", ".join(str(t.device) for t in tensors))
+    return index
 
 
 def _int32_vector(t, n, what):
-    import torch
-    if t.dtype != torch.int32 or t.dim() != 1 or (n is not None and t.shape[0] != n) or \
-            (t.shape[0] > 1 and t.stride(0) != 1):
-        raise ValueError(f"{what} must be a contiguous int32 vector" + ("" if n is None else f" of {n}"))
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous int32 vector of {n}")
 
 
-def _launch(fn, device, *args):
-    """Call a C ABI function with `device` current; raise on a bad status."""
-    import torch
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args)
+def _launch(fn, index, stream, *args):
+    """Call a C ABI function whose last argument is the stream (torch's
+    current one on GPU `index` by default) with that GPU current; raise on a
+    bad status."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
     else:
-        with torch.cuda.device(device):
-            st = fn(*args)
+        stream = getattr(stream, "cuda_stream", stream)
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, stream)
     if st != GEMM_OK:
         raise GemmError(st)
 
@@ -366,23 +373,23 @@ def grouped_gemm(a, b, ends, c, stream=None):
     rows.  Rows of c past the last end keep their values.  The output of a
     mixture's experts is grouped_gemm(x, w, ends, y); the gradient of x is
     grouped_gemm(dy, w.transpose(1, 2), ends, dx)."""
-    device = _same_device(a, b, ends, c)
-    if a.dim() != 2 or b.dim() != 3 or c.dim() != 2 or b.shape[2] != a.shape[1] or \
-            tuple(c.shape) != (a.shape[0], b.shape[1]):
+    index = _gpu_index(a, b, ends, c)
+    sa, sb, sc = a.shape, b.shape, c.shape
+    if len(sa) != 2 or len(sb) != 3 or sb[2] != sa[1] or sc != (sa[0], sb[1]):
         raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, c {tuple(c.shape)}")
     if b.dtype != a.dtype:
         raise ValueError("a and b must have the same dtype")
-    _int32_vector(ends, b.shape[0], "ends")
-    lda, ldc = _ld(a.shape, a.stride(), 0, 1), _ld(c.shape, c.stride(), 0, 1)
-    bm, ldb = "k", _ld(b.shape[1:], b.stride()[1:], 0, 1)
+    _int32_vector(ends, sb[0], "ends")
+    lda, ldc, tb = _ld(sa, a.stride(), 0, 1), _ld(sc, c.stride(), 0, 1), b.stride()
+    bm, ldb = b"k", _ld(sb, tb, 1, 2)
     if ldb is None:
-        bm, ldb = "n", _ld(b.shape[1:], b.stride()[1:], 1, 0)
+        bm, ldb = b"n", _ld(sb, tb, 2, 1)
     if lda is None or ldb is None or ldc is None:
         raise ValueError(f"a {a.stride()} and c {c.stride()} must be row-major, b {b.stride()} have one "
                          "contiguous dimension")
-    _launch(_lib.gemm_run_grouped, device, a.shape[0], b.shape[1], a.shape[1], b"k", _c(bm), b"n",
+    _launch(_lib.gemm_run_grouped, index, stream, sa[0], sb[1], sa[1], b"k", bm, b"n",
             dtype_code(a.dtype, c.dtype), a.data_ptr(), b.data_ptr(), c.data_ptr(), lda, ldb, ldc,
-            b.shape[0], b.stride(0), ends.data_ptr(), _on_stream(device, stream))
+            sb[0], tb[0], ends.data_ptr())
     return c
 
 
@@ -392,23 +399,23 @@ def grouped_gemm_k(a, b, ends, c, accumulate=False, stream=None):
     K x N), c is (G, M, N) with M or N contiguous, ends the G ascending ends of
     the groups' k.  Groups without any k get zeros; accumulate adds to c.  The
     gradient of a mixture's weights is grouped_gemm_k(dy.t(), x.t(), ends, dw)."""
-    device = _same_device(a, b, ends, c)
-    if a.dim() != 2 or b.dim() != 2 or c.dim() != 3 or b.shape[1] != a.shape[1] or \
-            tuple(c.shape[1:]) != (a.shape[0], b.shape[0]):
+    index = _gpu_index(a, b, ends, c)
+    sa, sb, sc = a.shape, b.shape, c.shape
+    if len(sa) != 2 or len(sb) != 2 or len(sc) != 3 or sb[1] != sa[1] or sc[1:] != (sa[0], sb[0]):
         raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, c {tuple(c.shape)}")
     if b.dtype != a.dtype:
         raise ValueError("a and b must have the same dtype")
-    _int32_vector(ends, c.shape[0], "ends")
-    lda, ldb = _ld(a.shape, a.stride(), 1, 0), _ld(b.shape, b.stride(), 1, 0)
-    cm, ldc = "n", _ld(c.shape[1:], c.stride()[1:], 0, 1)
+    _int32_vector(ends, sc[0], "ends")
+    lda, ldb, tc = _ld(sa, a.stride(), 1, 0), _ld(sb, b.stride(), 1, 0), c.stride()
+    cm, ldc = b"n", _ld(sc, tc, 1, 2)
     if ldc is None:
-        cm, ldc = "m", _ld(c.shape[1:], c.stride()[1:], 1, 0)
+        cm, ldc = b"m", _ld(sc, tc, 2, 1)
     if lda is None or ldb is None or ldc is None:
         raise ValueError(f"a {a.stride()} and b {b.stride()} must be transposed views of row-major matrices, "
                          f"c {c.stride()} have one contiguous dimension")
-    _launch(_lib.gemm_run_grouped_k, device, a.shape[0], b.shape[0], a.shape[1], b"m", b"n", _c(cm),
+    _launch(_lib.gemm_run_grouped_k, index, stream, sa[0], sb[0], sa[1], b"m", b"n", cm,
             dtype_code(a.dtype, c.dtype), a.data_ptr(), b.data_ptr(), c.data_ptr(), lda, ldb, ldc,
-            c.shape[0], c.stride(0), ends.data_ptr(), int(bool(accumulate)), _on_stream(device, stream))
+            sc[0], tc[0], ends.data_ptr(), bool(accumulate))
     return c
 
 
@@ -420,38 +427,43 @@ def gemm_lora(a, b, c, down, up, ids, workspace, ranks=None, scales=None, stream
     [0, L) has no adapter.  workspace is a contiguous GPU tensor of at least
     gemm_lora_workspace_size(M, N, K, dtype_code(a.dtype, c.dtype), R) bytes,
     kept by the caller and not shared by calls that may run at once."""
-    import torch
-    device = _same_device(a, b, c, down, up, ids, workspace, *(t for t in (ranks, scales) if t is not None))
-    M, K = a.shape if a.dim() == 2 else (-1, -1)
-    N = b.shape[0]
-    if b.dim() != 2 or c.dim() != 2 or down.dim() != 3 or up.dim() != 3 or b.shape[1] != K or \
-            tuple(c.shape) != (M, N) or down.shape[2] != K or tuple(up.shape) != (down.shape[0], N, down.shape[1]):
-        raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, c {tuple(c.shape)}, "
-                         f"down {tuple(down.shape)}, up {tuple(up.shape)}")
-    if not (a.dtype == b.dtype == down.dtype == up.dtype):
+    index = _gpu_index(a, b, c, down, up, ids, workspace)
+    sa, sb, sd, su = a.shape, b.shape, down.shape, up.shape
+    if len(sa) != 2 or len(sb) != 2 or len(sd) != 3 or sb[1] != sa[1] or sd[2] != sa[1] or \
+            c.shape != (sa[0], sb[0]) or su != (sd[0], sb[0], sd[1]):
+        raise ValueError(f"shape mismatch: a {tuple(sa)}, b {tuple(sb)}, c {tuple(c.shape)}, down {tuple(sd)}, "
+                         f"up {tuple(su)}")
+    (M, K), N, (L, R) = sa, sb[0], sd[:2]
+    dtype = a.dtype
+    if b.dtype is not dtype or down.dtype is not dtype or up.dtype is not dtype:
         raise ValueError("a, b, down and up must have the same dtype")
-    L, R = down.shape[:2]
     _int32_vector(ids, M, "ids")
+    ranks_at = scales_at = 0
     if ranks is not None:
+        _gpu_index(ids, ranks)
         _int32_vector(ranks, L, "ranks")
-    if scales is not None and (scales.dtype != torch.float32 or tuple(scales.shape) != (L,) or
-                               (L > 1 and scales.stride(0) != 1)):
-        raise ValueError(f"scales must be a contiguous float32 vector of {L}")
+        ranks_at = ranks.data_ptr()
+    if scales is not None:
+        _gpu_index(ids, scales)
+        if scales.dtype is not torch.float32 or scales.shape != (L,) or (L > 1 and scales.stride(0) != 1):
+            raise ValueError(f"scales must be a contiguous float32 vector of {L}")
+        scales_at = scales.data_ptr()
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    lda, ldc = _ld(a.shape, a.stride(), 0, 1), _ld(c.shape, c.stride(), 0, 1)
-    bm, ldb = "k", _ld(b.shape, b.stride(), 0, 1)
+    tb, td, tu = b.stride(), down.stride(), up.stride()
+    lda, ldc = _ld(sa, a.stride(), 0, 1), _ld(c.shape, c.stride(), 0, 1)
+    bm, ldb = b"k", _ld(sb, tb, 0, 1)
     if ldb is None:
-        bm, ldb = "n", _ld(b.shape, b.stride(), 1, 0)
-    ld_down, ld_up = (_ld(t.shape[1:], t.stride()[1:], 0, 1) for t in (down, up))
-    if None in (lda, ldb, ldc, ld_down, ld_up):
-        raise ValueError(f"a {a.stride()}, c {c.stride()} and the slots of down {down.stride()} and up {up.stride()} "
-                         f"must be row-major, b {b.stride()} have one contiguous dimension")
-    lora = Lora(L, R, down.data_ptr(), up.data_ptr(), ld_down, ld_up, down.stride(0), up.stride(0), ids.data_ptr(),
-                None if ranks is None else ranks.data_ptr(), None if scales is None else scales.data_ptr())
-    _launch(_lib.gemm_run_lora, device, M, N, K, b"k", _c(bm), b"n", dtype_code(a.dtype, c.dtype), a.data_ptr(),
-            b.data_ptr(), c.data_ptr(), lda, ldb, ldc, ctypes.byref(lora), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _on_stream(device, stream))
+        bm, ldb = b"n", _ld(sb, tb, 1, 0)
+    ld_down, ld_up = _ld(sd, td, 1, 2), _ld(su, tu, 1, 2)
+    if lda is None or ldb is None or ldc is None or ld_down is None or ld_up is None:
+        raise ValueError(f"a {a.stride()}, c {c.stride()} and the slots of down {td} and up {tu} must be row-major, "
+                         f"b {tb} have one contiguous dimension")
+    lora = _LORA.pack(L, R, down.data_ptr(), up.data_ptr(), ld_down, ld_up, td[0], tu[0], ids.data_ptr(), ranks_at,
+                      scales_at)
+    _launch(_lib.gemm_run_lora, index, stream, M, N, K, b"k", bm, b"n", dtype_code(dtype, c.dtype), a.data_ptr(),
+            b.data_ptr(), c.data_ptr(), lda, ldb, ldc, lora, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
     return c
 
 

@@ -18,8 +18,6 @@
 // read.
 #pragma once
 
-#include <cstdlib>
-
 #include "gemm_ragged.hpp"
 
 namespace mg {
@@ -166,7 +164,7 @@ lora_shrink_kernel(Params p, Lora q)
 // direct-to-LDS ring, so that each cache line of A and of the adapter is asked
 // for whole and once per workgroup (the fragments straight from memory above
 // ask for 64 bytes of 16 rows at a time: 41 us at 4096 rows, K = 4096, rank
-// 64, where this form takes SHRINK_US).
+// 64, where this form takes 13.6).
 template <In TI>
 using ShrinkTile = Dma16<TI, Out::F32, 64, 64, 64, 2, 2, 16, 4, true, true>;
 
@@ -416,7 +414,7 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
 // it are replaced by zeros in LDS and reported: `repair` then adds their terms
 // to the stored C, for the adapter's own rows.  Measured at 4096 rows, N = K =
 // 4096, rank 64 in bf16: the product with its adapters 121 us by lora_add,
-// whose every adapter waits for its own loads, SHARED_US here (plain 97).
+// whose every adapter waits for its own loads, 110 here (plain 97).
 template <class KT, In TI>
 struct SharedLora {
     static constexpr int BM = KT::TILE_M, BN = KT::TILE_N, NW = KT::NW, NT = KT::NT, MI = 16;
@@ -425,9 +423,9 @@ struct SharedLora {
     using OV = DmaOperand<BM, CH, NW, true, MI>;       // for its fragments
     using OU = DmaOperand<BN, CH, NW, true, MI>;
     static constexpr int V_BYTES = BM * CH * 2, U_BYTES = OU::BYTES;
-    static constexpr int TAB = 2 * V_BYTES + 2 * U_BYTES, PROP = TAB + BM * 8, BAD = PROP + 2 * NW * 8;
+    static constexpr int TAB = 2 * V_BYTES + 2 * U_BYTES, ROWS = TAB + BM * 8, BAD = ROWS + BM * 8;
     static_assert(BAD + 16 <= KT::SMEM, "fits the ring");
-    static_assert(WTM <= 64, "one lane per row");
+    static_assert(64 % WTM == 0, "a wave's rows in one mask");
 
     // True: an adapter held infinities or NaN (repair has work).
     __device__ static __forceinline__ bool add(const Params& p, const Lora& q, char* smem, typename KT::Acc& acc, int m0,
@@ -437,37 +435,54 @@ struct SharedLora {
         const int wm = wave / WN, wn = wave % WN;
         char* const vh = smem;
         char* const vl = smem + V_BYTES;
+        char* const ub = smem + 2 * V_BYTES;           // two buffers
         float* const tab = (float*)(smem + TAB);       // fp16: 2^e of each row, then 2^-e
-        int* const prop = (int*)(smem + PROP);
+        int* const row_id = (int*)(smem + ROWS);       // -1: none
+        float* const row_scale = (float*)(row_id + BM);
         int* const bad = (int*)(smem + BAD);
-        const int row = m0 + wm * WTM + lane;
-        const bool valid = lane < WTM && row < p.M;
-        Distinct d(q, row, valid);
-        const uint64_t all = d.left;
-        // The workgroup's next adapter: the first wave that has one left names it.
-        int parity = 0;
-        auto select = [&](int& rank) {
-            int* const at = prop + parity * 2 * NW;
-            parity ^= 1;
-            if (lane == 0) {
-                const int l = d.left ? (int)__builtin_ctzll(d.left) : 0;
-                const int id = __builtin_amdgcn_readlane(d.id, l), rk = __builtin_amdgcn_readlane(d.rank, l);
-                at[2 * wave] = d.left ? id : -1;
-                at[2 * wave + 1] = rk;
-            }
-            __syncthreads();
-            int a = -1;
-            rank = 0;
+        // Every wave walks the distinct adapters of all the tile's rows (NC
+        // rows a lane), so that no wave waits for another to name the next.
+        constexpr int NC = (BM + 63) / 64;
+        int id[NC], rank[NC];
+        uint64_t left_rows[NC];
+        bare_barrier();                                // LDS is free
 #pragma unroll
-            for (int w = NW - 1; w >= 0; --w) {
-                const int id = at[2 * w], rk = at[2 * w + 1];
-                if (id >= 0) {
-                    a = id;
-                    rank = rk;
-                }
+        for (int c = 0; c < NC; ++c) {
+            const int m = c * 64 + lane;
+            const bool valid = m < BM && m0 + m < p.M;
+            id[c] = valid ? q.ids[m0 + m] : -1;
+            if (id[c] >= q.slots) id[c] = -1;
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const bool has = id[c] >= 0;
+            rank[c] = has && q.ranks ? min(max(q.ranks[id[c]], 0), q.R) : q.R;
+            const float scale = has && q.scales ? q.scales[id[c]] : 1.f;
+            if (wave == c % NW && c * 64 + lane < BM) {
+                row_id[c * 64 + lane] = has ? id[c] : -1;
+                row_scale[c * 64 + lane] = scale;
             }
-            a = __builtin_amdgcn_readfirstlane(a);
-            rank = __builtin_amdgcn_readfirstlane(rank);
+        }
+        if (tid == 0) *bad = 0;
+        // The next adapter, its rank and this wave's rows of it.
+        auto next = [&](int& rk, uint64_t& rows) {
+            int a = -1;
+            rk = 0;
+#pragma unroll
+            for (int c = NC - 1; c >= 0; --c)
+                if (left_rows[c]) {
+                    const int l = (int)__builtin_ctzll(left_rows[c]);
+                    a = __builtin_amdgcn_readlane(id[c], l);
+                    rk = __builtin_amdgcn_readlane(rank[c], l);
+                }
+            rows = 0;
+            if (a < 0) return a;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const uint64_t m = __builtin_amdgcn_ballot_w64(id[c] == a);
+                left_rows[c] &= ~m;
+                if (wm * WTM / 64 == c) rows = m >> (wm * WTM % 64);
+            }
             return a;
         };
         OU ou;
@@ -485,46 +500,33 @@ struct SharedLora {
         };
         bool found = false, first = true;
         for (int r0 = 0; r0 < q.pitch; r0 += CH) {
-            bare_barrier();                            // LDS is free
-            if (tid == 0) *bad = 0;
-            d.left = all;
-            int rank;
-            int a = select(rank);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) left_rows[c] = __builtin_amdgcn_ballot_w64(id[c] >= 0);
+            __syncthreads();                           // row_id is written; v and U have been read
+            int rk;
+            uint64_t rows;
+            int a = next(rk, rows);
             if (a < 0) return false;
-            int left = min(rank - r0, CH);
-            issue(a, left, r0, smem + 2 * V_BYTES);
-            stage_v(p, q, vh, vl, tab, m0, r0, tid);
-            int buf = 0;
-            for (;;) {
-                const uint64_t rows = __builtin_amdgcn_ballot_w64(d.id == a);
-                d.left &= ~rows;
-                int next_rank;
-                const int next = select(next_rank);    // its barrier: v is staged, the other buffer read
+            issue(a, min(rk - r0, CH), r0, ub);
+            stage_v(p, q, vh, vl, tab, row_id, row_scale, m0, r0, tid);
+            for (int buf = 0; a >= 0; buf ^= 1) {
+                const int left = min(rk - r0, CH);
+                const uint64_t own = rows;
+                char* const u = ub + buf * U_BYTES;
+                wait_vmcnt<0>();
+                __syncthreads();                       // this adapter has landed, the other buffer been read
                 if (first) rescale(acc, tab, wm, lane);
                 first = false;
-                char* const u = smem + 2 * V_BYTES + buf * U_BYTES;
-                const int next_left = min(next_rank - r0, CH);
-                if (next >= 0) {
-                    issue(next, next_left, r0, smem + 2 * V_BYTES + (buf ^ 1) * U_BYTES);
-                    wait_vmcnt<OU::IPW>();
-                } else {
-                    wait_vmcnt<0>();
-                }
-                bare_barrier();
+                a = next(rk, rows);
+                if (a >= 0) issue(a, min(rk - r0, CH), r0, ub + (buf ^ 1) * U_BYTES);
                 if (left > 0) {
-                    if (left % 8) {                    // zeros from the rank on in the chunk that holds it
-                        OU::template zero_tail<NT>(u, left, tid);
-                        __syncthreads();
-                    }
                     clean(u, left, bad, tid);
-                    __syncthreads();
-                    if (rows) multiply(acc, vh, vl, u, rows, left, wm, wn, lane);
+                    __builtin_amdgcn_s_waitcnt(0xc07f);
+                    bare_barrier();                    // (no fence: the next adapter is on its way)
+                    if (own) multiply(acc, vh, vl, u, own, left, wm, wn, lane);
                 }
-                if (next < 0) break;
-                a = next;
-                left = next_left;
-                buf ^= 1;
             }
+            __syncthreads();
             found = found || *bad;
         }
         rescale(acc, tab + BM, wm, lane);
@@ -547,7 +549,8 @@ struct SharedLora {
         }
     }
 
-    // Zeros in the place of the adapter's infinities and NaN; *bad: there were some.
+    // Zeros from the rank on in the chunk that holds it, and in the place of the
+    // adapter's infinities and NaN (*bad: there were some).
     __device__ static __forceinline__ void clean(char* u, int left, int* bad, int tid)
     {
         constexpr uint32_t EXP = TI == In::F16 ? 0x7c00u : 0x7f80u;
@@ -556,6 +559,8 @@ struct SharedLora {
             if (c * 8 >= left) continue;
             i32x4* const at = (i32x4*)(u + row * 128 + swz_chunk<8, true>(row, c) * 16);
             i32x4 v = *at;
+            const bool cut = c * 8 + 8 > left;
+            if (cut) v = mask_k<TI>(v, c * 8, left);
             bool any = false;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
@@ -564,10 +569,8 @@ struct SharedLora {
                 any = any || lo || hi;
                 v[w] = (int)(d & (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u));
             }
-            if (any) {
-                *at = v;
-                *bad = 1;
-            }
+            if (any || cut) *at = v;
+            if (any) *bad = 1;
         }
     }
 
@@ -621,56 +624,95 @@ struct SharedLora {
     // input type in LDS.  fp16 rows are brought to a largest value of 2^13 ..
     // 2^14 by a power of two (at most 2^64), so that neither term leaves
     // fp16's range; tab: that power and its inverse.
-    __device__ static __forceinline__ void stage_v(const Params& p, const Lora& q, char* vh, char* vl, float* tab, int m0,
-                                                   int r0, int tid)
+    __device__ static __forceinline__ void stage_v(const Params& p, const Lora& q, char* vh, char* vl, float* tab,
+                                                   const int* row_id, const float* row_scale, int m0, int r0, int tid)
     {
-        static_assert(NT % 16 == 0 && BM * 16 % NT == 0, "16 threads per row");
+        constexpr int STEP = NT / 16, IT = BM / STEP;                     // 16 threads per row
+        constexpr int MOST = TI == In::F16 && TM * TN >= 32 ? 2 : 4, BATCH = IT < MOST ? IT : MOST;
+        static_assert(IT % BATCH == 0, "whole batches");
         const int c4 = tid % 16 * 4;                   // this thread's 4 columns
-        for (int m = tid / 16; m < BM; m += NT / 16) {
-            const bool in = m0 + m < p.M;
-            const int id = in ? q.ids[m0 + m] : -1;
-            const bool has = id >= 0 && id < q.slots;
-            const float scale = has && q.scales ? q.scales[id] : 1.f;
-            const float* src = q.v + (int64_t)(m0 + m) * q.pitch;
-            auto load = [&](int r) {
-                f32x4 v = {0.f, 0.f, 0.f, 0.f};
-                if (has && r < q.pitch)
-                    for (int s = 0; s < q.splits; ++s) v += *(const f32x4*)(src + (int64_t)s * p.M * q.pitch + r);
-                return v * scale;
-            };
-            f32x4 v = load(r0 + c4);
-            if constexpr (TI == In::F16) {
-                float top = 0.f;
-                auto up_to = [&](f32x4 x) {
+        const int64_t split = (int64_t)p.M * q.pitch;
+        // The rows of a batch: all their loads before the first is waited for.
+        auto load = [&](int mb, int r, f32x4 (&v)[BATCH]) {
+            const float* src[BATCH];
+            bool has[BATCH];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float y = __builtin_fabsf(x[e]);
-                        if (y < __builtin_inff()) top = fmaxf(top, y);
-                    }
+            for (int x = 0; x < BATCH; ++x) {
+                const int m = mb + x * STEP;
+                has[x] = r < q.pitch && row_id[m] >= 0;
+                src[x] = q.v + (int64_t)(m0 + m) * q.pitch + r;
+                v[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+            int s = 0;
+            for (; s + 1 < q.splits; s += 2) {
+                f32x4 t[2][BATCH];
+#pragma unroll
+                for (int x = 0; x < BATCH; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        t[y][x] = has[x] ? *(const f32x4*)(src[x] + (s + y) * split) : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int x = 0; x < BATCH; ++x) v[x] = v[x] + t[0][x] + t[1][x];
+            }
+            if (s < q.splits) {
+#pragma unroll
+                for (int x = 0; x < BATCH; ++x)
+                    if (has[x]) v[x] += *(const f32x4*)(src[x] + s * split);
+            }
+#pragma unroll
+            for (int x = 0; x < BATCH; ++x) v[x] *= row_scale[mb + x * STEP];
+        };
+#pragma unroll 1
+        for (int mb = tid / 16; mb < BM; mb += BATCH * STEP) {
+            f32x4 v[BATCH];
+            load(mb, r0 + c4, v);
+            if constexpr (TI == In::F16) {
+                float top[BATCH];
+                auto up_to = [&](const f32x4 (&x)[BATCH]) {
+#pragma unroll
+                    for (int y = 0; y < BATCH; ++y)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float a = __builtin_fabsf(x[y][e]);
+                            if (a < __builtin_inff()) top[y] = fmaxf(top[y], a);
+                        }
                 };
+#pragma unroll
+                for (int y = 0; y < BATCH; ++y) top[y] = 0.f;
                 if (q.pitch <= CH) {
                     up_to(v);
                 } else {
-                    for (int r = c4; r < q.pitch; r += CH) up_to(load(r));
+                    for (int r = c4; r < q.pitch; r += CH) {
+                        f32x4 w[BATCH];
+                        load(mb, r, w);
+                        up_to(w);
+                    }
                 }
 #pragma unroll
-                for (int o = 1; o < 16; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
-                int e;
-                __builtin_frexpf(top, &e);
-                e = top > 0.f ? min(14 - e, 64) : 0;
-                if (c4 == 0) {
-                    tab[m] = __builtin_ldexpf(1.f, e);
-                    tab[BM + m] = __builtin_ldexpf(1.f, -e);
+                for (int y = 0; y < BATCH; ++y) {
+#pragma unroll
+                    for (int o = 1; o < 16; o *= 2) top[y] = fmaxf(top[y], __shfl_xor(top[y], o));
+                    int e;
+                    __builtin_frexpf(top[y], &e);
+                    e = top[y] > 0.f ? min(14 - e, 64) : 0;
+                    if (c4 == 0) {
+                        tab[mb + y * STEP] = __builtin_ldexpf(1.f, e);
+                        tab[BM + mb + y * STEP] = __builtin_ldexpf(1.f, -e);
+                    }
+                    v[y] *= __builtin_ldexpf(1.f, e);
                 }
-                v *= __builtin_ldexpf(1.f, e);
             }
-            VFrag<TI> f;
-            const float x[8] = {v[0], v[1], v[2], v[3], 0.f, 0.f, 0.f, 0.f};
-            f.set(x);
-            const int off = m * 128 + swz_chunk<8, true>(m, c4 / 8) * 16 + c4 % 8 * 2;
-            typedef int i32x2 __attribute__((ext_vector_type(2)));
-            *(i32x2*)(vh + off) = i32x2{f.f[0][0], f.f[0][1]};
-            *(i32x2*)(vl + off) = i32x2{f.f[1][0], f.f[1][1]};
+#pragma unroll
+            for (int y = 0; y < BATCH; ++y) {
+                const int m = mb + y * STEP;
+                VFrag<TI> f;
+                const float x[8] = {v[y][0], v[y][1], v[y][2], v[y][3], 0.f, 0.f, 0.f, 0.f};
+                f.set(x);
+                const int off = m * 128 + swz_chunk<8, true>(m, c4 / 8) * 16 + c4 % 8 * 2;
+                typedef int i32x2 __attribute__((ext_vector_type(2)));
+                *(i32x2*)(vh + off) = i32x2{f.f[0][0], f.f[0][1]};
+                *(i32x2*)(vl + off) = i32x2{f.f[1][0], f.f[1][1]};
+            }
         }
     }
 
@@ -924,7 +966,6 @@ inline ShrinkPlan shrink_plan(int64_t M, int64_t K, bool tiled)
     const int64_t tiles = (M + s.rows - 1) / s.rows;
     int64_t n;
     if (tiled) {
-        s.z = 2;
         n = 256 / tiles;
     } else {
         s.z = (int)(tiles >= 64 ? 1 : M < kShrinkRows ? M : kShrinkRows);
@@ -933,6 +974,10 @@ inline ShrinkPlan shrink_plan(int64_t M, int64_t K, bool tiled)
     if (n > 8) n = 8;
     if (n > K / 256) n = K / 256;
     s.splits = (int)(n < 1 ? 1 : n);
+    if (tiled) {
+        n = 512 / (tiles * s.splits);
+        s.z = (int)(n < 2 ? 2 : n > 16 ? 16 : n);
+    }
     return s;
 }
 // The 64-row tile is for 16-bit operands that allow 16-byte loads.
@@ -996,33 +1041,31 @@ struct LoraInst {
         if constexpr (TI == In::F32) {
             return staged<BKM, true>(c, s);
         } else {
+            // Measured in bf16, N = K = 4096, us for both kernels (rows: one
+            // adapter each up to 64, packed above; rank):
+            //   rows rank  16x16 str. 32x16 str. 32x32   32x32 sh. 64x64 sh. 128x128 sh. 256x256 sh.
+            //      1  16   15.2       17.3       19.4
+            //     16  16   20.2       22.9       25.5
+            //     32  16   30.4       23.8       27.2
+            //     64  16   53.3       38.3       30.5    34.5      65.6
+            //    128  64                         42.9    31.9      37.4      62.6        100
+            //    256  64                         43.3    48.9      37.4      60.9        103
+            //   1024  64                                           82.2      64.4        102
+            //   2048  64                                          151       111         107
+            //   8192  64                                          482       367         234
+            // (str.: the streaming kernel for few rows, B k-major only; sh.:
+            // adapters through LDS for the whole workgroup.)
             auto tiles = [&](int t) { return ((int64_t)c.p.M + t - 1) / t * ((c.p.N + t - 1) / t); };
             if constexpr (BKM) {
-                const char* v = getenv("RV");
-                switch (v ? atoi(v) : 1) {
-                case 0: return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 1, 8, 4, 2>, c, 16, 16, 640, s);
-                case 1: return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 1, 8, 4, 4>, c, 16, 16, 768, s);
-                case 2: return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 2, 2, 8, 2, 4>, c, 32, 32, 768, s);
-                case 3: return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 2, 2, 4, 4, 4>, c, 32, 32, 512, s);
-                case 4: return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 2, 8, 3, 4>, c, 16, 32, 768, s);
-                case 5: return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 2, 1, 8, 3, 4>, c, 32, 16, 768, s);
-                case 6: return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 1, 4, 8, 4>, c, 16, 16, 512, s);
-                case 7: return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 1, 4, 4, 2>, c, 16, 16, 384, s);
-                case 10: return dma<32, 32, 128, 2, 2, 4, 0, BKM>(c, s);
-                case 11: return dma<64, 64, 64, 2, 2, 4, 0, BKM>(c, s);
-                case 12: return dma<128, 128, 64, 2, 2, 4, 0, BKM>(c, s);
-                case 13: return dma<64, 64, 64, 2, 2, 4, 1, BKM>(c, s);
-                case 14: return dma<128, 128, 64, 2, 2, 4, 1, BKM>(c, s);
-                case 15: return launch_lora(&gemm_lora_pp_kernel<TI, TO, BKM>, c, 256, 256, 512, s);
-                case 16: return dma<64, 128, 64, 2, 2, 3, 0, BKM>(c, s);
-                default: break;
-                }
+                if (c.p.M <= 16) return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 1, 8, 4, 4>, c, 16, 16, 768, s);
+                if (c.p.M <= 32) return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 2, 1, 8, 3, 4>, c, 32, 16, 768, s);
             }
             if (c.p.M <= 32) return dma<16, 32, 256, 1, 2, 4, 4, BKM>(c, s);
             if (c.p.M <= 96) return dma<32, 32, 128, 2, 2, 4, 4, BKM>(c, s);
+            if (c.p.M <= 144) return dma<32, 32, 128, 2, 2, 4, 0, BKM>(c, s);
             if (tiles(256) >= 100) return launch_lora(&gemm_lora_pp_kernel<TI, TO, BKM>, c, 256, 256, 512, s);
-            if (tiles(128) >= 96) return dma<128, 128, 64, 2, 2, 4, 1, BKM>(c, s);
-            return dma<64, 64, 64, 2, 2, 4, 1, BKM>(c, s);
+            if (tiles(64) <= 512) return dma<64, 64, 64, 2, 2, 4, 0, BKM>(c, s);
+            return dma<128, 128, 64, 2, 2, 4, 0, BKM>(c, s);
         }
     }
     static hipError_t launch(const LoraCall& c, hipStream_t s)

@@ -926,7 +926,7 @@ __global__ void __launch_bounds__(512)
 gemm_lora_pp_kernel(Params p, Lora q)
 {
     constexpr int BM = 256, BN = 256, WN = 2, MI = 16;
-    using PP = PingPong<TI, TO, BM, BN, 64, 4, WN, MI, true, BKM>;
+    using PP = PingPong<TI, TO, BM, BN, 64, 4, WN, MI, true, BKM, false>;
     using KT = typename PP::KT;
     __shared__ __attribute__((aligned(1024))) char smem[KT::SMEM];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);

@@ -12,15 +12,27 @@ struct RaggedF32 {
     template <bool AK, bool BKM, By BY, bool EPI, bool VEC>
     static hipError_t sized(const RaggedCall& c, hipStream_t s)
     {
-        auto tiles = [&](int t) {
-            const int64_t cols = (c.p.N + t - 1) / t;
-            if (!c.by_rows) return cols * ((c.p.M + t - 1) / t) * c.r.groups;
-            const int64_t avg = (c.r.rows + c.r.groups - 1) / c.r.groups;
-            return cols * ((avg + t - 1) / t) * c.r.groups;
+        // Measured, us (K = 1024 by rows; 64x64 in three stages, 64x128 in two,
+        // 128x128 in two):
+        //   by rows   64 rows in  4 groups of 1024     24.2    41.9   66.9
+        //           1024 rows in 16 groups of 2048     60.1    70.6  126
+        //           4096 rows in 16 groups of 2048    178     165    196
+        //          16384 rows in 16 groups of 2048    577     549    562
+        //   by k (64x64 in two stages, 128x128 in two), 4096 k:
+        //          16 groups of 512 x 512              28.1           43.4
+        //           4 groups of 1024 x 1024            75.7           98.6
+        //           4 groups of 4096 x 2048           550            503
+        auto tiles = [&](int64_t rows, int bm, int bn) {
+            return (rows + bm - 1) / bm * ((c.p.N + bn - 1) / bn) * c.r.groups;
         };
-        // RULE
-        if (tiles(128) >= 192 && (!c.by_rows || c.r.rows > 48 * (int64_t)c.r.groups)) return go<128, 128, 2, AK, BKM, BY, EPI, VEC>(c, s);
-        return go<64, 64, VEC ? 4 : 2, AK, BKM, BY, EPI, VEC>(c, s);
+        if constexpr (BY == By::Rows && VEC) {
+            const int64_t avg = (c.r.rows + c.r.groups - 1) / c.r.groups;
+            if (tiles(avg, 64, 128) >= 1024) return go<64, 128, 2, AK, BKM, BY, EPI, VEC>(c, s);
+            return go<64, 64, 3, AK, BKM, BY, EPI, VEC>(c, s);
+        } else {
+            if (BY == By::K && tiles(c.p.M, 128, 128) >= 512) return go<128, 128, 2, AK, BKM, BY, EPI, VEC>(c, s);
+            return go<64, 64, 2, AK, BKM, BY, EPI, VEC>(c, s);
+        }
     }
     template <bool VEC>
     static hipError_t any(const RaggedCall& c, hipStream_t s)

@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(256)
 lora_shrink_kernel(Params p, Lora q)
 {
     constexpr int ES = TI == In::F32 ? 4 : 2, CE = 16 / ES, KS = 4 * CE;   // k per step
-    constexpr int RJ = 4;                                                  // 16-column blocks at a time
+    constexpr int RJ = 2;                                                  // 16-column blocks at a time
     __shared__ float part[4][kShrinkRows][RJ * 16 + 4];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m0 = blockIdx.x * kShrinkRows;
@@ -99,11 +99,11 @@ lora_shrink_kernel(Params p, Lora q)
         make_rsrc(p.A + (int64_t)m0 * p.lda * ES, rows_extent(min(p.M - m0, kShrinkRows), p.lda * ES, row_tail<ES, VEC>(p.K)));
     const int aoff = (int)((lane % 16) * p.lda * ES);
     float* const out = q.v + ((int64_t)split * p.M + m0) * q.pitch;
-    for (int u = 0;; ++u) {
+    for (int u = 0;;) {
         const Adapter a = d.next();
         if (a.id < 0) break;
-        if (u % q.z != (int)blockIdx.z) continue;
-        for (int r0 = 0; r0 < q.pitch; r0 += RJ * 16) {
+        for (int r0 = 0; r0 < q.pitch; r0 += RJ * 16, ++u) {
+            if (u % q.z != (int)blockIdx.z) continue;
             f32x4 acc[RJ];
 #pragma unroll
             for (int j = 0; j < RJ; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -142,8 +142,7 @@ lora_shrink_kernel(Params p, Lora q)
                 }
             };
             if (nj == 1) body(std::integral_constant<int, 1>{});
-            else if (nj == 2) body(std::integral_constant<int, 2>{});
-            else if (nj > 0) body(std::integral_constant<int, RJ>{});
+            else if (nj > 1) body(std::integral_constant<int, RJ>{});
             __syncthreads();                           // the sums of the last adapter have been read
 #pragma unroll
             for (int j = 0; j < RJ; ++j)
@@ -258,13 +257,12 @@ struct VFrag {
 // holds rows i * MI and columns j * MI on.  NB: adapters whose loads are
 // in flight together.  Of the rows' distinct adapters, those with an index of
 // `share` modulo `shares` are added (all: 0 of 1).
-template <In TI, bool VEC, int NB, int MI, int TM, int TN, class AccT>
+template <In TI, bool VEC, int NB, int MI, int TM, int TN, class AccT, class Col>
 __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&acc)[TM][TN], int m0, int n0, int lane,
-                                         float* tab, int share = 0, int shares = 1)
+                                         float* tab, int share, int shares, Col col)
 {
     constexpr int ES = TI == In::F32 ? 4 : 2, CE = 16 / ES, KS = 64 / MI * CE, R4 = MI == 32 ? 16 : 4;
-    constexpr bool BIG = TM * TN * R4 >= 128;          // accumulators that leave few registers
-    constexpr int CH = TI == In::F32 || BIG ? 32 : 64;   // columns of v held at a time
+    constexpr int CH = TI == In::F32 ? 32 : 64;          // columns of v held at a time
     constexpr int NK = CH / KS;
     static_assert(TM * MI <= 64, "one lane per row");
     if (q.slots == 0 || q.R == 0) return;
@@ -325,7 +323,6 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int k = 0; k < NK; ++k) {
-                if constexpr (BIG) __builtin_amdgcn_sched_barrier(0);
                 float v[CE];
                 load_v(i, r0 + k * KS, v);
                 if constexpr (TI == In::F16) {
@@ -356,14 +353,13 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
             }
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
-                if constexpr (BIG) __builtin_amdgcn_sched_barrier(0);
                 i32x4 fu[NB][NK];
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int k = 0; k < NK; ++k) {
                         const int r = r0 + k * KS + fk;
-                        fu[b][k] = load_chunk<ES, VEC>(ru[b], r < a[b].rank ? fr * up_row + r * ES + j * MI * up_row : -16);
+                        fu[b][k] = load_chunk<ES, VEC>(ru[b], r < a[b].rank ? col(j) * up_row + r * ES : -16);
                     }
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
@@ -402,6 +398,14 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
             }
         }
     }
+}
+
+// ... with the columns of MFMA tile j next to each other from j * MI on.
+template <In TI, bool VEC, int NB, int MI, int TM, int TN, class AccT>
+__device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&acc)[TM][TN], int m0, int n0, int lane,
+                                         float* tab, int share = 0, int shares = 1)
+{
+    lora_add<TI, VEC, NB, MI>(p, q, acc, m0, n0, lane, tab, share, shares, [&](int j) { return j * MI + lane % MI; });
 }
 
 // The same for a whole workgroup on 16-bit inputs, through LDS (the ring, free
@@ -745,13 +749,14 @@ struct SharedLora {
     }
 };
 
-// The shared product on the register-staged tile: any type and alignment.
-template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, bool BKM, bool VEC>
+// The shared product on the register-staged tile: 16-bit inputs of any
+// alignment.
+template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, bool BKM>
 __global__ void __launch_bounds__(WM * WN * 64)
 gemm_lora_kernel(Params p, Lora q)
 {
     constexpr int MI = 16;
-    using T = GemmTile<TI, TO, BM, BN, BK, WM, WN, MI, true, BKM, true, VEC>;
+    using T = GemmTile<TI, TO, BM, BN, BK, WM, WN, MI, true, BKM, true, false>;
     __shared__ __attribute__((aligned(16))) char smem[2 * T::STAGE];
     T t;
     t.tid = threadIdx.x;
@@ -771,7 +776,7 @@ gemm_lora_kernel(Params p, Lora q)
         for (int j = 0; j < T::TN; ++j) t.acc[i][j] = typename T::Acc{};
     staged_mainloop<T, BK>(t, smem, p, m0, n0);
     __syncthreads();      // no wave reads the tiles any more
-    lora_add<TI, VEC, 1, MI, T::TM, T::TN>(p, q, t.acc, m0 + t.wm * T::WTM, n0 + t.wn * T::WTN, lane,
+    lora_add<TI, false, 1, MI, T::TM, T::TN>(p, q, t.acc, m0 + t.wm * T::WTM, n0 + t.wn * T::WTN, lane,
                                            (float*)smem + 128 * wave);
 #pragma unroll
     for (int i = 0; i < T::TM; ++i)
@@ -818,6 +823,30 @@ gemm_lora_dma_kernel(Params p, Lora q)
         if (bad) SharedLora<KT, TI>::repair(p, q, m0, n0, tid);
 }
 
+// ... on the fp32 ring of gemm_f32dma.hpp (VEC = false: 4-byte loads).
+template <int BM, int BN, int STAGES, bool BKM, bool VEC>
+__global__ void __launch_bounds__(256)
+gemm_lora_f32_kernel(Params p, Lora q)
+{
+    constexpr int BK = 32, WN = 2;
+    using KT = F32Dma<Out::F32, BM, BN, BK, 2, WN, STAGES, true, BKM, VEC>;
+    __shared__ __attribute__((aligned(1024))) char smem[KT::SMEM];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tm, tn;
+    tile_coords(p, tm, tn);
+    const int m0 = __builtin_amdgcn_readfirstlane(tm * BM), n0 = __builtin_amdgcn_readfirstlane(tn * BN);
+    typename KT::OA oa;
+    typename KT::OB ob;
+    oa.init(wave, lane, p.lda);
+    ob.init(wave, lane, p.ldb);
+    typename KT::Acc acc;
+    KT::zero(acc);
+    KT::mainloop(p, smem, oa, ob, m0, n0, 0, (p.K + BK - 1) / BK, acc, tid, lane, wave);
+    lora_add<In::F32, VEC, 2, 32>(p, q, acc, m0 + wave / WN * KT::WTM, n0 + wave % WN * KT::WTN, lane, nullptr, 0, 1,
+                                   [&](int j) { return KT::UB::row(j, lane % 32); });
+    KT::template store<false, false>(p, m0, n0, acc, lane, wave, smem);
+}
+
 // Few rows (a decoding step): the product streams B once and is bound by how
 // many of its bytes are in flight.  A workgroup has 16 MT rows and 16 NT
 // columns.  NW of its waves take the k-tiles in turn, each with a ring of ST
@@ -826,14 +855,17 @@ gemm_lora_dma_kernel(Params p, Lora q)
 // fragments are in registers.  NL more waves share out the rows' adapters: the
 // chain of loads they wait for (ids, then slots, then the adapters) runs
 // beside the stream.
-template <In TI, Out TO, int MT, int NT, int NW, int ST, int NL>
+template <In TI, Out TO, int MT, int NT, int NW, int ST, int NL, bool BKM = true, bool VEC = true>
 __global__ void __launch_bounds__((NW + NL) * 64)
 gemm_lora_skinny_kernel(Params p, Lora q)
 {
-    constexpr int BK = 64, MI = 16, NG = 2, NT_ALL = (NW + NL) * 64;
-    using OA = DmaOperand<MT * 16, BK, 1, true, MI>;
-    using OB = DmaOperand<NT * 16, BK, 1, true, MI>;
-    constexpr int STAGE = OA::BYTES + OB::BYTES, L = OA::IPW + OB::IPW;
+    // A k-tile is 128 bytes of a row: 64 or 32 of k.
+    constexpr bool F32 = TI == In::F32;
+    constexpr int ES = F32 ? 4 : 2, BK = 128 / ES, MI = 16, NG = 2, NT_ALL = (NW + NL) * 64;
+    using OA = std::conditional_t<F32, F32Operand<MT * 16, BK, 1, true, VEC>, DmaOperand<MT * 16, BK, 1, true, MI>>;
+    using OB = std::conditional_t<F32, F32Operand<NT * 16, BK, 1, BKM, VEC>, DmaOperand<NT * 16, BK, 1, true, MI>>;
+    static_assert(F32 || (BKM && VEC), "16-bit operands: k-major, 16-byte loads");
+    constexpr int STAGE = OA::BYTES + OB::BYTES, L = (OA::IPW + OB::IPW) * (VEC ? 1 : 4);
     constexpr int PART = MT * 16 * NT * 16;            // sums of a wave
     constexpr int RING = NW * ST * STAGE;
     constexpr int NB = (MT * 16 + NL - 1) / NL > 8 ? 8 : (MT * 16 + NL - 1) / NL;   // adapters at a time
@@ -854,7 +886,7 @@ gemm_lora_skinny_kernel(Params p, Lora q)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (wave >= NW) {
-        lora_add<TI, true, NB, MI, MT, NT>(p, q, acc, m0, n0, lane, (float*)(smem + RING) + 128 * (wave - NW), wave - NW, NL);
+        lora_add<TI, VEC, NB, MI, MT, NT>(p, q, acc, m0, n0, lane, (float*)(smem + RING) + 128 * (wave - NW), wave - NW, NL);
     } else {
         const int nkt = (p.K + BK - 1) / BK, left = p.K - (nkt - 1) * BK;
         OA oa;
@@ -875,17 +907,31 @@ gemm_lora_skinny_kernel(Params p, Lora q)
             char* s = ring + slot * STAGE;
             if (t == nkt - 1 && left != BK) {
                 oa.template zero_tail<64>(s, left, lane);
-                ob.template zero_tail<64>(s + OA::BYTES, left, lane);
+                if constexpr (BKM) ob.template zero_tail<64>(s + OA::BYTES, left, lane);
                 __builtin_amdgcn_s_waitcnt(0xc07f);
             }
             asm volatile("" ::: "memory");
+            // Fragment g: the 16 bytes of k-chunk 4 g + lane / 16 of a row.  A
+            // chunk of an n-major B is four values of one column.
+            auto chunk = [&](const char* tile, int row, int g) {
+                return *(const i32x4*)(tile + row * 128 + swz_chunk<8, true>(row, g * 4 + lane / 16) * 16);
+            };
             i32x4 fa[NG][MT], fb[NG][NT];
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
 #pragma unroll
-                for (int i = 0; i < MT; ++i) fa[g][i] = oa.template frag<MI>(s, i * MI, g * 32, lane);
+                for (int i = 0; i < MT; ++i) fa[g][i] = chunk(s, i * MI + lane % MI, g);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) fb[g][j] = ob.template frag<MI>(s + OA::BYTES, j * MI, g * 32, lane);
+                for (int j = 0; j < NT; ++j) {
+                    const int n = j * MI + lane % MI;
+                    if constexpr (BKM) {
+                        fb[g][j] = chunk(s + OA::BYTES, n, g);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            fb[g][j][e] = ((const int*)(s + OA::BYTES))[(g * 16 + lane / 16 * 4 + e) * (NT * MI) + n];
+                    }
+                }
             }
             __builtin_amdgcn_s_waitcnt(0xc07f);        // lgkmcnt(0): the slot has been read
             __builtin_amdgcn_sched_barrier(0);
@@ -958,7 +1004,7 @@ struct LoraCall {
 struct ShrinkPlan {
     int rows, splits, z;
 };
-inline ShrinkPlan shrink_plan(int64_t M, int64_t K, bool tiled)
+inline ShrinkPlan shrink_plan(int64_t M, int64_t K, bool tiled, int pitch = 32)
 {
     ShrinkPlan s;
     tiled = tiled && M >= 128;
@@ -977,10 +1023,17 @@ inline ShrinkPlan shrink_plan(int64_t M, int64_t K, bool tiled)
     if (tiled) {
         n = 512 / (tiles * s.splits);
         s.z = (int)(n < 2 ? 2 : n > 16 ? 16 : n);
+    } else {
+        n = 512 / (tiles * s.splits * s.z);
+        const int blocks = (pitch + 31) / 32;
+        s.z *= (int)(n < 1 ? 1 : n > blocks ? blocks : n);
     }
     return s;
 }
-// The 64-row tile is for 16-bit operands that allow 16-byte loads.
+
+// The 64-row tile is for 16-bit operands that allow 16-byte loads.  (In fp32
+// on 32x32 MFMAs it took 110 us against 97 at 256 rows, N = K = 4096, rank 16,
+// both kernels together, and 1261 against 1333 at 4096 rows of rank 128.)
 inline bool shrink_tiled(int in_bytes, bool vec) { return in_bytes == 2 && vec; }
 
 template <class Kernel>
@@ -1024,22 +1077,43 @@ hipError_t launch_shrink(const LoraCall& c, hipStream_t s)
 
 template <In TI, Out TO>
 struct LoraInst {
-    template <bool BKM, bool VEC>
-    static hipError_t staged(const LoraCall& c, hipStream_t s)
-    {
-        return launch_lora(&gemm_lora_kernel<TI, TO, 64, 64, TI == In::F32 ? 32 : 64, 2, 2, BKM, VEC>, c, 64, 64, 256, s);
-    }
     template <int BM, int BN, int BK, int WM, int WN, int ST, int NB, bool BKM>
     static hipError_t dma(const LoraCall& c, hipStream_t s)
     {
         return launch_lora(&gemm_lora_dma_kernel<TI, TO, BM, BN, BK, WM, WN, ST, NB, BKM>, c, BM, BN, WM * WN * 64, s);
     }
-    template <bool BKM>
+    template <int BM, int BN, int ST, bool BKM, bool VEC>
+    static hipError_t f32(const LoraCall& c, hipStream_t s)
+    {
+        return launch_lora(&gemm_lora_f32_kernel<BM, BN, ST, BKM, VEC>, c, BM, BN, 256, s);
+    }
+    template <bool BKM, bool VEC>
     static hipError_t product(const LoraCall& c, hipStream_t s)
     {
-        if (!c.vec) return staged<BKM, false>(c, s);
         if constexpr (TI == In::F32) {
-            return staged<BKM, true>(c, s);
+            // Measured, N = K = 4096, us for both kernels (rows: one adapter
+            // each of 16 up to 64, packed above; B n-major in brackets):
+            //   rows rank  16x16 str.    16x32 str.    32x32 str.    64x64        64x128
+            //      1  16    24.2 [31.3]   26.2 [28.5]   31.6 [31.6]    94 [ 95]
+            //     16 128    47.1 [61.1]   54.3 [68.3]   65.6 [78.9]   146 [182]
+            //     32  16    40.2 [55.4]   31.9 [37.0]   39.6 [44.8]   107 [113]
+            //     64  16    65.1 [86.8]   48.8 [58.8]   40.6 [43.5]   108 [113]
+            //    128  16    96.2 [141]    69.4 [94.0]   56.6 [70.3]    96 [110]
+            //    256 128                               158  [224]     130 [146]     238 [238]
+            //   1024  16                               419  [429]     298 [303]     283 [284]
+            //   4096  16                              1344           1110          1065
+            auto tiles = [&](int bm, int bn) { return ((int64_t)c.p.M + bm - 1) / bm * ((c.p.N + bn - 1) / bn); };
+            if (c.p.M <= 16) return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 1, 8, 4, 4, BKM, VEC>, c, 16, 16, 768, s);
+            if (c.p.M <= 32) return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 2, 8, 3, 4, BKM, VEC>, c, 16, 32, 768, s);
+            if (tiles(64, 64) <= 192) return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 2, 2, 8, 2, 4, BKM, VEC>, c, 32, 32, 768, s);
+            if constexpr (VEC) {
+                if (tiles(64, 128) >= 512) return f32<64, 128, 2, BKM, true>(c, s);
+                return f32<64, 64, 3, BKM, true>(c, s);
+            } else {
+                return f32<64, 64, 2, BKM, false>(c, s);
+            }
+        } else if constexpr (!VEC) {
+            return launch_lora(&gemm_lora_kernel<TI, TO, 64, 64, 64, 2, 2, BKM>, c, 64, 64, 256, s);
         } else {
             // Measured in bf16, N = K = 4096, us for both kernels (rows: one
             // adapter each up to 64, packed above; rank):
@@ -1074,7 +1148,8 @@ struct LoraInst {
             const hipError_t e = launch_shrink<TI>(c, s);
             if (e != hipSuccess) return e;
         }
-        return c.b_kmajor ? product<true>(c, s) : product<false>(c, s);
+        if (c.vec) return c.b_kmajor ? product<true, true>(c, s) : product<false, true>(c, s);
+        return c.b_kmajor ? product<true, false>(c, s) : product<false, false>(c, s);
     }
 };
 

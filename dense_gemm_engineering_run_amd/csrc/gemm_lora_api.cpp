@@ -40,7 +40,7 @@ uint64_t workspace(int64_t M, int64_t N, int64_t K, int64_t rank, bool tiled)
 uint64_t workspace_up_to(int64_t M, int64_t N, int64_t K, int dtype, int64_t rank)
 {
     uint64_t most = 0;
-    for (int tiled = 0; tiled <= (mg::in_bytes(dtype) == 2); ++tiled) {
+    for (int tiled = 0; tiled <= mg::shrink_tiled(mg::in_bytes(dtype), true); ++tiled) {
         most = std::max(most, workspace(M, N, K, rank, tiled));
         for (int64_t m = mg::kShrinkRows; m < std::min<int64_t>(M, 1 << 14); m += mg::kShrinkRows)
             most = std::max(most, std::max(workspace(m - 1, N, K, rank, tiled), workspace(m, N, K, rank, tiled)));
@@ -107,7 +107,7 @@ int run(int64_t M, int64_t N, int64_t K, char a, char b, char c, int dtype, cons
     p.b_bytes = reads ? ob.bytes(vec) : 0;
     p.c_vec = oc.aligned(16);
     if (with) {
-        const mg::ShrinkPlan s = mg::shrink_plan(M, K, mg::shrink_tiled(es, vec));
+        const mg::ShrinkPlan s = mg::shrink_plan(M, K, mg::shrink_tiled(es, vec), pitch(l.rank));
         q.shrink_rows = s.rows;
         q.q = mg::Lora{(const char*)l.down, (const char*)l.up, l.ids, l.ranks, l.scales, (float*)ws,
                        l.stride_down * es, l.stride_up * es, l.ld_down, l.ld_up,

@@ -630,6 +630,10 @@ struct RaggedInst {
     //     256         8     2048 x 1024                21.1   25.7   20.8   23.5
     //    1024         8     4096 x 2048               206    190    175    140
     //    4096         8     4096 x 4096                      1270   1150    847
+    // Products too small to fill the chip with those take the tile that spreads
+    // them further: 1 group of 48 rows of 1024 x 4096 14.6 on 32x64 (25.8 on
+    // 64x128), 4 groups of 128 20.2 (34.3 on 128x128), 4 groups of 300 28.0 on
+    // 128x64 (37.1 on 128x128).
     // 128x128 in two stages, two workgroups a CU: 18.5 us at 256 rows in 8
     // groups of 2048 x 1024 (64 tiles of 256x256), 33.4 at 512 (128 tiles;
     // 256x256: 25.7).
@@ -637,18 +641,20 @@ struct RaggedInst {
     static hipError_t rows(const RaggedCall& c, hipStream_t s)
     {
         const int64_t groups = c.r.groups, avg = (c.r.rows + groups - 1) / groups;
-        const int64_t cols256 = (c.p.N + 255) / 256;
+        auto tiles = [&](int bm, int bn) { return groups * ((avg + bm - 1) / bm) * ((c.p.N + bn - 1) / bn); };
+        if (tiles(32, 64) <= 320) return dma<32, 64, 128, 1, 4, 16, 3, true, BKM, By::Rows, false>(c, s);
+        if (avg > 80 && tiles(128, 64) <= 192) return dma<128, 64, 64, 2, 2, 16, 4, true, BKM, By::Rows, false>(c, s);
         if (avg <= 24) {
             if constexpr (BKM) return dma<32, 64, 128, 1, 4, 16, 3, true, BKM, By::Rows, false>(c, s);
             else return dma<64, 128, 64, 2, 2, 16, 3, true, BKM, By::Rows, false>(c, s);
         }
         if (avg <= 80) return dma<64, 128, 64, 2, 2, 16, 3, true, BKM, By::Rows, false>(c, s);
         if (avg < 192) {
-            if (groups * ((avg + 127) / 128) * cols256 >= 100)
+            if (tiles(128, 256) >= 100)
                 return dma<128, 256, 64, 2, 2, 32, 3, true, BKM, By::Rows, false>(c, s);
             return dma<128, 128, 64, 2, 2, 16, 4, true, BKM, By::Rows, false>(c, s);
         }
-        if (groups * ((avg + 255) / 256) * cols256 >= 100) return pp<true, BKM, By::Rows, false>(c, s);
+        if (tiles(256, 256) >= 100) return pp<true, BKM, By::Rows, false>(c, s);
         return dma<128, 128, 64, 2, 2, 32, 2, true, BKM, By::Rows, false>(c, s);
     }
     // By k: 256x256 tiles from half a CU's share of them up (bf16 -> fp32, 8

@@ -241,6 +241,16 @@ def test_wide_outputs(dtype, K):
     run_k([K, 0, 3, 2 * K, 65], 1100, 2104, dtype, "m", left=3, accumulate=True)
 
 
+@pytest.mark.parametrize("lens,N", [([48], 1000), ([20] * 100, 300), ([48] * 70, 300), ([100] * 4, 1500),
+                                    ([128] * 32, 500), ([100, 156] * 30, 500), ([300] * 16, 700)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_every_height_of_tile(dtype, lens, N):
+    """Few and many tiles of each height: 32x64, 64x128, 128x64, 128x128, 128x256."""
+    for b_major in "kn":
+        run_rows(lens, N, 200, dtype, b_major, left=3)
+        run_rows([n // 2 for n in lens] + lens, N, 72, dtype, b_major, kind="int5")
+
+
 @pytest.mark.parametrize("ends", [[50, 20, 90], [-5, 30, 30], [1000, 40, 99], [100, 100, 100], [-1, -1, -1],
                                   [2 ** 31 - 1, -2 ** 31, 5]])
 def test_ends_that_do_not_ascend_stay_in_bounds(ends):

@@ -8,7 +8,8 @@ terms of the input type: off by 2^-22 of itself for fp16 (two roundings of
 2^-11 and 2^-12), 2^-16 for bf16 (8 bits cut off, the rest rounded by 2^-9 of
 2^-7), not split in fp32; fp16 scales v by row, where the smaller term's
 smallest step is 2^-24 against a row's largest value of 2^13, 2^-37 of the
-row's largest V times sum |up|.  With 2R terms in the second sum:
+row's largest V times sum |up|.  With 2R terms in the second sum, a rounding
+for the scale (of the sum, or of v before it is split) and one for adding:
     E = (K + 2) 2^-24 S1 + ((K + 2) + (2R + 6)) 2^-24 S2 + split S2
 and eps(out) / 2 (|ref| + E) for the last rounding (2^-25 for fp16 subnormals).
 Integer inputs of at most 5 give integers that every step holds exactly.
@@ -148,6 +149,17 @@ def run(*args, **kw):
 @pytest.mark.parametrize("dtype", TYPES)
 def test_rows(dtype, M, ids):
     run(M, 136, 264, 9, 24, dtype, ids=ids)
+
+
+@pytest.mark.parametrize("K", [31, 32, 300, 1100])
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_few_rows(dtype, pad, K):
+    """The streaming kernels: every number of rows, order of B and last k-tile."""
+    for M in (1, 12, 16, 24, 32, 50, 90):
+        for b_major in "kn":
+            run(M, 200, K, 5, 40, dtype, b_major=b_major, pad=pad)
+            run(M, 33, K, 5, 136, dtype, b_major=b_major, pad=pad, ids="distinct", kind="int5")
 
 
 @pytest.mark.parametrize("R", [1, 3, 8, 16, 31, 32, 33, 64, 65, 100, 128, 200])

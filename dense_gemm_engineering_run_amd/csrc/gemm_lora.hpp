@@ -77,6 +77,29 @@ struct Distinct {
     }
 };
 
+// Chunks of rows from `base` on: of 16-byte aligned rows (VEC), fp32 rows, or
+// 16-bit rows that start at any element.  kNowhere: an offset that reads zeros
+// (also 20 bytes on).
+constexpr int kNowhere = -4096;
+template <int ES, bool VEC>
+struct Rows {
+    __amdgpu_buffer_rsrc_t r;
+    Rows() = default;
+    __device__ __forceinline__ Rows(const char* base, uint64_t bytes) : r(make_rsrc(base, bytes)) {}
+    __device__ __forceinline__ i32x4 chunk(int off) const { return load_chunk<ES, VEC>(r, off); }
+};
+template <>
+struct Rows<2, false> : OddRows {
+    Rows() = default;
+    using OddRows::OddRows;
+    __device__ __forceinline__ i32x4 chunk(int off) const
+    {
+        OddChunk c;
+        c.load(*this, off);
+        return c.get(lead, off);
+    }
+};
+
 // v: one workgroup per 16 rows, range of k and share of the rows' distinct
 // adapters.  Its four waves take k-steps in turn (operands straight from
 // memory into MFMA fragments: A's rows are read once per distinct adapter,
@@ -95,8 +118,8 @@ lora_shrink_kernel(Params p, Lora q)
     const int steps = (p.K + KS - 1) / KS;
     const int s0 = (int)((int64_t)steps * split / q.splits), s1 = (int)((int64_t)steps * (split + 1) / q.splits);
     Distinct d(q, m0 + lane, lane < kShrinkRows && m0 + lane < p.M);
-    const __amdgpu_buffer_rsrc_t ra =
-        make_rsrc(p.A + (int64_t)m0 * p.lda * ES, rows_extent(min(p.M - m0, kShrinkRows), p.lda * ES, row_tail<ES, VEC>(p.K)));
+    const Rows<ES, VEC> ra(p.A + (int64_t)m0 * p.lda * ES,
+                           rows_extent(min(p.M - m0, kShrinkRows), p.lda * ES, row_tail<ES, VEC>(p.K)));
     const int aoff = (int)((lane % 16) * p.lda * ES);
     float* const out = q.v + ((int64_t)split * p.M + m0) * q.pitch;
     for (int u = 0;;) {
@@ -108,8 +131,8 @@ lora_shrink_kernel(Params p, Lora q)
 #pragma unroll
             for (int j = 0; j < RJ; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
             const int left = max(0, min(a.rank - r0, RJ * 16));
-            const __amdgpu_buffer_rsrc_t rd = make_rsrc(q.down + a.id * q.s_down + (int64_t)r0 * q.ld_down * ES,
-                                                        rows_extent(left, q.ld_down * ES, row_tail<ES, VEC>(p.K)));
+            const Rows<ES, VEC> rd(q.down + a.id * q.s_down + (int64_t)r0 * q.ld_down * ES,
+                                   rows_extent(left, q.ld_down * ES, row_tail<ES, VEC>(p.K)));
             const int doff = (int)((lane % 16) * q.ld_down * ES);
             const int nj = (left + 15) / 16;
             auto body = [&](auto NJ) {
@@ -123,10 +146,10 @@ lora_shrink_kernel(Params p, Lora q)
                     for (int t = 0; t < UN; ++t) {
                         const int k = (s + t) * KS + (lane / 16) * CE;
                         const bool in = s + t < s1 && k < p.K;
-                        fa[t] = load_chunk<ES, VEC>(ra, in ? aoff + k * ES : -16);       // past the extent: zeros
+                        fa[t] = ra.chunk(in ? aoff + k * ES : kNowhere);       // past the extent: zeros
 #pragma unroll
                         for (int j = 0; j < n; ++j)
-                            fd[t][j] = load_chunk<ES, VEC>(rd, in ? doff + (int)(16 * j * q.ld_down * ES) + k * ES : -16);
+                            fd[t][j] = rd.chunk(in ? doff + (int)(16 * j * q.ld_down * ES) + k * ES : kNowhere);
                     }
 #pragma unroll
                     for (int t = 0; t < UN; ++t) {
@@ -273,7 +296,7 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
     auto load_v = [&](int i, int r, float (&v)[CE]) {
 #pragma unroll
         for (int e = 0; e < CE; ++e) v[e] = 0.f;
-        const int off = r + fk < q.pitch ? ((i * MI + fr) * q.pitch + r + fk) * 4 : -16;
+        const int off = r + fk < q.pitch ? ((i * MI + fr) * q.pitch + r + fk) * 4 : kNowhere;
         for (int s = 0; s < q.splits; ++s) {
             const __amdgpu_buffer_rsrc_t rs = make_rsrc((const char*)(q.v + (int64_t)m0 * q.pitch) + s * vsplit, vbytes);
 #pragma unroll
@@ -344,11 +367,11 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
         };
         while (d.left) {
             Adapter a[NB];
-            __amdgpu_buffer_rsrc_t ru[NB];
+            Rows<ES, VEC> ru[NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 a[b] = mine();
-                ru[b] = make_rsrc(q.up + max(a[b].id, 0) * q.s_up + (int64_t)n0 * q.ld_up * ES,
+                ru[b] = Rows<ES, VEC>(q.up + max(a[b].id, 0) * q.s_up + (int64_t)n0 * q.ld_up * ES,
                                   a[b].id < 0 || n0 >= p.N ? 0 : rows_extent(min(p.N - n0, TN * MI), q.ld_up * ES, row_tail<ES, VEC>(q.R)));
             }
 #pragma unroll
@@ -359,7 +382,7 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
 #pragma unroll
                     for (int k = 0; k < NK; ++k) {
                         const int r = r0 + k * KS + fk;
-                        fu[b][k] = load_chunk<ES, VEC>(ru[b], r < a[b].rank ? col(j) * up_row + r * ES : -16);
+                        fu[b][k] = ru[b].chunk(r < a[b].rank ? col(j) * up_row + r * ES : kNowhere);
                     }
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
@@ -497,7 +520,7 @@ struct SharedLora {
             for (int j = 0; j < OU::IPW; ++j) {
                 const int slot = (wave * OU::IPW + j) * 64 + lane;
                 const int c = swz_chunk<OU::CPR, true>(slot / OU::CPR, slot % OU::CPR);
-                o.voff[j] = c * 8 < left ? ou.voff[j] : -16;          // past the rank: zeros
+                o.voff[j] = c * 8 < left ? ou.voff[j] : kNowhere;          // past the rank: zeros
             }
             o.issue(q.up + a * q.s_up + (int64_t)n0 * q.ld_up * 2 + r0 * 2,
                     rows_extent(min(p.N - n0, BN), q.ld_up * 2, row_tail<2, true>(q.R - r0)), q.ld_up, 0, 0, dst, wave);
@@ -749,45 +772,25 @@ struct SharedLora {
     }
 };
 
-// The shared product on the register-staged tile: 16-bit inputs of any
-// alignment.
-template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, bool BKM>
+// The shared product, for 16-bit operands that are not 16-byte aligned.
+template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, int DEPTH, bool BKM>
 __global__ void __launch_bounds__(WM * WN * 64)
-gemm_lora_kernel(Params p, Lora q)
+gemm_lora_odd_kernel(Params p, Lora q)
 {
-    constexpr int MI = 16;
-    using T = GemmTile<TI, TO, BM, BN, BK, WM, WN, MI, true, BKM, true, false>;
-    __shared__ __attribute__((aligned(16))) char smem[2 * T::STAGE];
-    T t;
-    t.tid = threadIdx.x;
-    const int lane = t.tid & 63, wave = __builtin_amdgcn_readfirstlane(t.tid >> 6);
-    t.wm = wave / WN;
-    t.wn = wave % WN;
-    t.frow = lane % MI;
-    t.fq = lane / MI;
+    using T = OddTile<TI, TO, BM, BN, BK, WM, WN, DEPTH, true, BKM>;
+    using KT = typename T::KT;
+    __shared__ __attribute__((aligned(1024))) char smem[KT::SMEM];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int tm, tn;
     tile_coords(p, tm, tn);
-    const int m0 = tm * BM, n0 = tn * BN;
-    t.la.init(t.tid, p.lda);
-    t.lb.init(t.tid, p.ldb);
-#pragma unroll
-    for (int i = 0; i < T::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < T::TN; ++j) t.acc[i][j] = typename T::Acc{};
-    staged_mainloop<T, BK>(t, smem, p, m0, n0);
-    __syncthreads();      // no wave reads the tiles any more
-    lora_add<TI, false, 1, MI, T::TM, T::TN>(p, q, t.acc, m0 + t.wm * T::WTM, n0 + t.wn * T::WTN, lane,
-                                           (float*)smem + 128 * wave);
-#pragma unroll
-    for (int i = 0; i < T::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < T::TN; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int m = m0 + t.wm * T::WTM + i * MI + (lane / 16) * 4 + e;
-                const int n = n0 + t.wn * T::WTN + j * MI + lane % 16;
-                if (m < p.M && n < p.N) store_out<TO>(p.C, (int64_t)m * p.ldc + n, t.acc[i][j][e]);
-            }
+    const int m0 = __builtin_amdgcn_readfirstlane(tm * BM), n0 = __builtin_amdgcn_readfirstlane(tn * BN);
+    typename KT::Acc acc;
+    KT::zero(acc);
+    T::mainloop(p, smem, m0, n0, acc, lane, wave);
+    bare_barrier();       // no wave reads the tiles any more
+    lora_add<TI, false, 1, 16, KT::TM, KT::TN>(p, q, acc, m0 + wave / WN * KT::WTM, n0 + wave % WN * KT::WTN, lane,
+                                               (float*)smem + 128 * wave);
+    store_tile<KT, false>(p, smem, m0, n0, acc, tid, lane, wave);
 }
 
 // ... on the direct-to-LDS ring (16-bit inputs).  NB: adapters at a time in
@@ -1082,6 +1085,11 @@ struct LoraInst {
     {
         return launch_lora(&gemm_lora_dma_kernel<TI, TO, BM, BN, BK, WM, WN, ST, NB, BKM>, c, BM, BN, WM * WN * 64, s);
     }
+    template <int BM, int BN, int BK, int WM, int WN, int DEPTH, bool BKM>
+    static hipError_t odd(const LoraCall& c, hipStream_t s)
+    {
+        return launch_lora(&gemm_lora_odd_kernel<TI, TO, BM, BN, BK, WM, WN, DEPTH, BKM>, c, BM, BN, WM * WN * 64, s);
+    }
     template <int BM, int BN, int ST, bool BKM, bool VEC>
     static hipError_t f32(const LoraCall& c, hipStream_t s)
     {
@@ -1113,7 +1121,21 @@ struct LoraInst {
                 return f32<64, 64, 2, BKM, false>(c, s);
             }
         } else if constexpr (!VEC) {
-            return launch_lora(&gemm_lora_kernel<TI, TO, 64, 64, 64, 2, 2, BKM>, c, 64, 64, 256, s);
+            // Measured in bf16, N = 4096, K = 4095, us for both kernels (rows:
+            // one adapter each of 16 up to 64, packed above):
+            //   rows rank  32x32   64x64   128x128  256x128
+            //      1  16    29.4    41.5     71.4    104
+            //     64  16    38.3    58.2    105      154
+            //    128  64    45.2    54.4    100      127
+            //    256  64    77.7    55.6     98.0    143
+            //   1024  64   297     182      115      171
+            //   4096  64   971     517      383      315
+            // (Loads element by element: 123 at one row, 1853 at 4096.)
+            auto tiles = [&](int bm, int bn) { return ((int64_t)c.p.M + bm - 1) / bm * ((c.p.N + bn - 1) / bn); };
+            if (c.p.M <= 144) return odd<32, 32, 256, 2, 2, 2, BKM>(c, s);
+            if (tiles(64, 64) <= 512) return odd<64, 64, 128, 2, 4, 2, BKM>(c, s);
+            if (tiles(256, 128) >= 256) return odd<256, 128, 64, 4, 2, 2, BKM>(c, s);
+            return odd<128, 128, 64, 4, 2, 2, BKM>(c, s);
         } else {
             // Measured in bf16, N = K = 4096, us for both kernels (rows: one
             // adapter each up to 64, packed above; rank):

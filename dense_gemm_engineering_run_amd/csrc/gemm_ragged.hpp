@@ -169,90 +169,6 @@ __device__ __forceinline__ bool select_group(Params& p, const Ragged& r, int lan
     return true;
 }
 
-// Main loop of the register-staged tile over all of p.K, adding to t.acc:
-// k-tile kt is multiplied out of LDS while kt + 1 goes from registers to the
-// other LDS stage and kt + 2 from memory to registers.
-template <class T, int BK>
-__device__ __forceinline__ void staged_mainloop(T& t, char* smem, const Params& p, int m0, int n0)
-{
-    const int nkt = (p.K + BK - 1) / BK;
-    if (nkt == 0) return;
-    const bool ragged = p.K % BK != 0;
-    auto load = [&](int kt) {
-        t.la.load(p.A, p.a_bytes, p.lda, m0, kt * BK, t.tid);
-        t.lb.load(p.B, p.b_bytes, p.ldb, n0, kt * BK, t.tid);
-    };
-    auto mask = [&](int kt) {
-        if (!ragged || kt != nkt - 1) return;
-        t.la.mask(kt * BK, p.K, t.tid);
-        t.lb.mask(kt * BK, p.K, t.tid);
-    };
-    load(0);
-    mask(0);
-    t.la.store(smem, t.tid);
-    t.lb.store(smem + T::A_BYTES, t.tid);
-    if (nkt > 1) load(1);
-    __syncthreads();
-    t.read_frags(smem, 0, 0);
-    int kt = 0;
-    for (; kt + 2 < nkt; ++kt) t.template tile<true, true, true>(smem, kt & 1, p, m0, n0, (kt + 2) * BK);
-    if (kt + 1 < nkt) {
-        mask(kt + 1);
-        t.template tile<true, false, true>(smem, kt & 1, p, m0, n0, 0);
-        ++kt;
-    }
-    t.template tile<false, false, false>(smem, kt & 1, p, m0, n0, 0);
-}
-
-// The grouped product on the register-staged tile of gemm_kernel.hpp: right
-// for every type, layout and alignment (VEC = false: element-aligned operands).
-template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, int MI, bool AK, bool BKM, By BY, bool EPI, bool VEC>
-__global__ void __launch_bounds__(WM * WN * 64)
-gemm_ragged_kernel(Params p, Ragged r)
-{
-    using T = GemmTile<TI, TO, BM, BN, BK, WM, WN, MI, AK, BKM, true, VEC>;
-    static_assert(MI == 16, "accumulator layout of the store below");
-    __shared__ __attribute__((aligned(16))) char smem[2 * T::STAGE];
-    T t;
-    t.tid = threadIdx.x;
-    const int lane = t.tid & 63, wave = t.tid >> 6;
-    t.wm = wave / WN;
-    t.wn = wave % WN;
-    t.frow = lane % MI;
-    t.fq = lane / MI;
-    int tm, tn;
-    if (!select_group<TI, TO, BM, BN, BY, VEC>(p, r, lane, tm, tn)) return;
-    const int m0 = tm * BM, n0 = tn * BN;
-    t.la.init(t.tid, p.lda);
-    t.lb.init(t.tid, p.ldb);
-#pragma unroll
-    for (int i = 0; i < T::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < T::TN; ++j) t.acc[i][j] = typename T::Acc{};
-
-    staged_mainloop<T, BK>(t, smem, p, m0, n0);
-    if constexpr (EPI) {
-        store_tile_via_lds<TO, BM, BN, T::NT, T::TM * T::TN * 4, 2 * T::STAGE>(
-            p, smem, m0, n0, t.tid, [&](int v) { return t.acc[v / (T::TN * 4)][(v / 4) % T::TN][v % 4]; },
-            [&](int v, int& row, int& col) {
-                const int i = v / (T::TN * 4), j = (v / 4) % T::TN, q = v % 4;
-                row = t.wm * T::WTM + i * MI + (lane / 16) * 4 + q;
-                col = t.wn * T::WTN + j * MI + lane % 16;
-            });
-    } else {
-#pragma unroll
-        for (int i = 0; i < T::TM; ++i)
-#pragma unroll
-            for (int j = 0; j < T::TN; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int m = m0 + t.wm * T::WTM + i * MI + (lane / 16) * 4 + q;
-                    const int n = n0 + t.wn * T::WTN + j * MI + lane % 16;
-                    if (m < p.M && n < p.N) store_out<TO>(p.C, (int64_t)m * p.ldc + n, t.acc[i][j][q]);
-                }
-    }
-}
-
 // ------------------------------------------------------- direct-to-LDS kernels
 
 // Store a tile held by a Dma16 engine: through the elementwise epilogue (EPI),
@@ -271,6 +187,149 @@ __device__ __forceinline__ void store_tile(const Params& p, char* smem, int m0, 
             KT::store_direct(p, m0, n0, acc, lane, wave);
         }
     }
+}
+
+// 16-bit operands whose rows start at any element.  A 16-byte chunk of one is
+// the 20 bytes from the 4-byte word that holds its first element, shifted into
+// place: two loads that are aligned as the hardware wants them, where loads
+// element by element are eight.  The words at either end may hold a neighbour's
+// element: they are words that the operand's own elements share, so nothing
+// outside its memory is touched, and what lies past an inner extent is masked
+// by whoever uses it.
+struct OddRows {
+    __amdgpu_buffer_rsrc_t r;
+    int lead;             // bytes from the first word to the first element: 0 or 2
+
+    OddRows() = default;
+    __device__ __forceinline__ OddRows(const char* base, uint64_t bytes)
+        : r(make_rsrc(base - ((uint64_t)base & 2), bytes ? (bytes + ((uint64_t)base & 2) + 3) / 4 * 4 : 0)),
+          lead((int)((uint64_t)base & 2))
+    {
+    }
+};
+struct OddChunk {
+    i32x4 words;
+    int last;
+    // The chunk at `off` bytes from the rows' base (multiple of 2; far below 0: zeros).
+    __device__ __forceinline__ void load(const OddRows& s, int off)
+    {
+        const int at = (off + s.lead) & ~3;
+        words = buf_load16(s.r, at);
+        last = __builtin_amdgcn_raw_buffer_load_b32(s.r, at + 16, 0, 0);
+    }
+    __device__ __forceinline__ i32x4 get(int lead, int off) const
+    {
+        const uint32_t sh = ((uint32_t)(off + lead) & 2) * 8;
+        i32x4 v;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            v[d] = (int)__builtin_amdgcn_alignbit((uint32_t)(d < 3 ? words[d + 1] : last), (uint32_t)words[d], sh);
+        return v;
+    }
+};
+
+// One such operand's k-tiles, from memory to registers (DEPTH tiles ahead) to
+// the LDS layout of DmaOperand.
+template <int ROWS, int BK, int NW, bool KMAJ, int DEPTH>
+struct OddOperand {
+    using LDS = DmaOperand<ROWS, BK, NW, KMAJ, 16>;
+    LDS at;
+    OddChunk q[DEPTH][LDS::IPW];
+
+    __device__ __forceinline__ void load(int d, const char* base, uint64_t bytes, int64_t ld, int row0, int k0)
+    {
+        const int64_t origin = (KMAJ ? (int64_t)row0 * ld + k0 : (int64_t)k0 * ld + row0) * 2;
+        const OddRows s(base + origin, (uint64_t)origin < bytes ? bytes - (uint64_t)origin : 0);
+#pragma unroll
+        for (int j = 0; j < LDS::IPW; ++j) q[d][j].load(s, at.voff[j]);
+    }
+    // ... of the tile at k0; elements from K on as zeros.  (row0 * ld and k0
+    // are even, so every tile's first element lies in its word as the base's.)
+    __device__ __forceinline__ void store(int d, char* tile, const char* base, int k0, int K, int wave, int lane) const
+    {
+#pragma unroll
+        for (int j = 0; j < LDS::IPW; ++j) {
+            const int slot = (wave * LDS::IPW + j) * 64 + lane;
+            i32x4 v = q[d][j].get((int)((uint64_t)base & 2), at.voff[j]);
+            if (k0 + BK > K) {
+                if constexpr (KMAJ) {
+                    v = mask_k<In::F16>(v, k0 + swz_chunk<LDS::CPR, true>(slot / LDS::CPR, slot % LDS::CPR) * 8, K);
+                } else {
+                    const i32x4 zero = {0, 0, 0, 0};
+                    v = k0 + slot / LDS::RCH < K ? v : zero;
+                }
+            }
+            *(i32x4*)(tile + slot * 16) = v;
+        }
+    }
+};
+
+// A tile of such operands: LDS in two stages, DEPTH tiles of loads in flight.
+template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, int DEPTH, bool AK, bool BKM>
+struct OddTile {
+    using KT = Dma16<TI, TO, BM, BN, BK, WM, WN, 16, 2, AK, BKM>;
+    static_assert(DEPTH % 2 == 0, "a tile's stage is known at compile time");
+    // Adds all of p.K to acc.
+    __device__ static __forceinline__ void mainloop(const Params& p, char* smem, int m0, int n0, typename KT::Acc& acc,
+                                                    int lane, int wave)
+    {
+        const int wm = wave / WN, wn = wave % WN, nkt = (p.K + BK - 1) / BK;
+        OddOperand<BM, BK, KT::NW, AK, DEPTH> oa;
+        OddOperand<BN, BK, KT::NW, BKM, DEPTH> ob;
+        oa.at.init(wave, lane, p.lda);
+        ob.at.init(wave, lane, p.ldb);
+        auto load = [&](int t, int d) {               // past the end: empty extents
+            oa.load(d, p.A, t < nkt ? p.a_bytes : 0, p.lda, m0, t * BK);
+            ob.load(d, p.B, t < nkt ? p.b_bytes : 0, p.ldb, n0, t * BK);
+        };
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) load(d, d);
+        for (int t0 = 0; t0 < nkt; t0 += DEPTH) {
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d) {
+                const int t = t0 + d;
+                if (t >= nkt) break;
+                char* const sa = smem + d % 2 * KT::STAGE;
+                char* const sb = sa + KT::OA::BYTES;
+                oa.store(d, sa, p.A, t * BK, p.K, wave, lane);
+                ob.store(d, sb, p.B, t * BK, p.K, wave, lane);
+                load(t + DEPTH, d);
+                // One barrier a tile: the other stage is written after the
+                // next one, when every wave has read it.
+                __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0)
+                bare_barrier();
+#pragma unroll
+                for (int g = 0; g < KT::NG; ++g) {
+                    i32x4 fa[KT::TM], fb[KT::TN];
+#pragma unroll
+                    for (int i = 0; i < KT::TM; ++i) fa[i] = KT::OA::template frag<16>(sa, wm * KT::WTM + i * 16, g * 32, lane);
+#pragma unroll
+                    for (int j = 0; j < KT::TN; ++j) fb[j] = KT::OB::template frag<16>(sb, wn * KT::WTN + j * 16, g * 32, lane);
+#pragma unroll
+                    for (int i = 0; i < KT::TM; ++i)
+#pragma unroll
+                        for (int j = 0; j < KT::TN; ++j) mfma_step<TI, 16>(fa[i], fb[j], acc[i][j]);
+                }
+            }
+        }
+    }
+};
+
+template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, int DEPTH, bool AK, bool BKM, By BY, bool EPI>
+__global__ void __launch_bounds__(WM * WN * 64)
+gemm_ragged_odd_kernel(Params p, Ragged r)
+{
+    using T = OddTile<TI, TO, BM, BN, BK, WM, WN, DEPTH, AK, BKM>;
+    using KT = typename T::KT;
+    __shared__ __attribute__((aligned(1024))) char smem[KT::SMEM];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tm, tn;
+    if (!select_group<TI, TO, BM, BN, BY, false>(p, r, lane, tm, tn)) return;
+    const int m0 = tm * BM, n0 = tn * BN;
+    typename KT::Acc acc;
+    KT::zero(acc);
+    T::mainloop(p, smem, m0, n0, acc, lane, wave);
+    store_tile<KT, EPI>(p, smem, m0, n0, acc, tid, lane, wave);
 }
 
 // 16-bit inputs on the direct-to-LDS ring of gemm_dma.hpp.
@@ -595,16 +654,38 @@ hipError_t launch_ragged(Kernel kernel, const RaggedCall& c, int BM, int BN, int
 
 template <In TI, Out TO>
 struct RaggedInst {
-    // Element-by-element loads: any alignment, any type but fp32.
-    template <bool BKM>
-    static hipError_t scalar_rows(const RaggedCall& c, hipStream_t s)
+    template <int BM, int BN, int BK, int WM, int WN, int DEPTH, bool AK, bool BKM, By BY, bool EPI>
+    static hipError_t odd(const RaggedCall& c, hipStream_t s)
     {
-        return launch_ragged<By::Rows>(&gemm_ragged_kernel<TI, TO, 64, 64, 64, 2, 2, 16, true, BKM, By::Rows, false, false>, c, 64, 64, 256, s);
+        return launch_ragged<BY>(&gemm_ragged_odd_kernel<TI, TO, BM, BN, BK, WM, WN, DEPTH, AK, BKM, BY, EPI>, c, BM, BN, WM * WN * 64, s);
     }
-    template <bool EPI>
-    static hipError_t scalar_k(const RaggedCall& c, hipStream_t s)
+    // Operands that are not 16-byte aligned, eight waves a tile.  Measured in
+    // bf16, B k-major (n-major in brackets where it differs), us, in brackets
+    // behind the 128x128 tile: on four waves:
+    //   rows/group  groups  N x K         32x64   64x128       128x128           256x128
+    //       2         8     4095 x 4095    54.8    70.6         72.7 ( 90.4)      98.3
+    //      16        64     1023 x 2047    72.0    67.4 [58.4]  72.0 ( 99.7)     107
+    //      50         2     4095 x 1023    10.9    17.0         20.2 ( 26.7)      28.4
+    //      64        32     2047 x 2047   117      97.5 [86.8] 110   (149)       116
+    //     128        32     2047 x 2047   189     142          116   (160)       168
+    //     512        16     4095 x 2047   635     397          298   (446) [278] 345 [350]
+    // Loads element by element took 181, 190, -, -, -, 1657 us.
+    template <bool BKM>
+    static hipError_t odd_rows(const RaggedCall& c, hipStream_t s)
     {
-        return launch_ragged<By::K>(&gemm_ragged_kernel<TI, TO, 64, 64, 64, 2, 2, 16, false, false, By::K, EPI, false>, c, 64, 64, 256, s);
+        const int64_t groups = c.r.groups, avg = (c.r.rows + groups - 1) / groups;
+        if (avg <= 8 || groups * ((avg + 31) / 32) * ((c.p.N + 63) / 64) <= 320)
+            return odd<32, 64, 128, 2, 4, 2, true, BKM, By::Rows, false>(c, s);
+        if (avg <= 80) return odd<64, 128, 64, 2, 4, 2, true, BKM, By::Rows, false>(c, s);
+        return odd<128, 128, 64, 2, 4, 2, true, BKM, By::Rows, false>(c, s);
+    }
+    // 8192 k in 16 groups of 4095 x 2047, bf16 -> fp32: 893 us; on 64x64 tiles
+    // of four waves 997, on 256x128 890.  In 8 groups of 511 x 511 (128 tiles)
+    // 48.6, 60 and 50.
+    template <bool EPI>
+    static hipError_t odd_k(const RaggedCall& c, hipStream_t s)
+    {
+        return odd<128, 128, 64, 4, 2, 2, false, false, By::K, EPI>(c, s);
     }
     template <int BM, int BN, int BK, int WM, int WN, int MI, int ST, bool AK, bool BKM, By BY, bool EPI>
     static hipError_t dma(const RaggedCall& c, hipStream_t s)
@@ -675,10 +756,10 @@ struct RaggedInst {
     {
         if (c.by_rows) {
             if (c.vec) return c.b_kmajor ? rows<true>(c, s) : rows<false>(c, s);
-            return c.b_kmajor ? scalar_rows<true>(c, s) : scalar_rows<false>(c, s);
+            return c.b_kmajor ? odd_rows<true>(c, s) : odd_rows<false>(c, s);
         }
         if (c.vec) return c.p.epi ? by_k<true>(c, s) : by_k<false>(c, s);
-        return c.p.epi ? scalar_k<true>(c, s) : scalar_k<false>(c, s);
+        return c.p.epi ? odd_k<true>(c, s) : odd_k<false>(c, s);
     }
 };
 

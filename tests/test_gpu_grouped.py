@@ -249,6 +249,15 @@ def test_every_height_of_tile(dtype, lens, N):
     for b_major in "kn":
         run_rows(lens, N, 200, dtype, b_major, left=3)
         run_rows([n // 2 for n in lens] + lens, N, 72, dtype, b_major, kind="int5")
+        run_rows(lens, N + 1, 201, dtype, b_major, left=3)
+
+
+@pytest.mark.parametrize("M,N", [(129, 255), (301, 1023)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_unaligned_gradients_of_matrices(dtype, M, N):
+    for c_major in "nm":
+        run_k([65, 0, 1, 300, 129], M, N, dtype, c_major, left=3)
+        run_k([64, 128, 63], M, N, dtype, c_major, kind="int5", accumulate=True, pad=2)
 
 
 @pytest.mark.parametrize("ends", [[50, 20, 90], [-5, 30, 30], [1000, 40, 99], [100, 100, 100], [-1, -1, -1],

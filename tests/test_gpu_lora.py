@@ -193,6 +193,9 @@ def test_large_tiles(dtype, K):
         run(2100, 2600, K, 5, 40, dtype, b_major=b_major, ids="packed", mixed=False)
         run(700, 1100, K, 7, 64, dtype, b_major=b_major, ids="mixed", kind="int5")
         run(300, 700, K, 7, 16, dtype, b_major=b_major, ids="packed")
+        run(4000, 2601, K + 1, 5, 40, dtype, b_major=b_major, ids="packed", mixed=False)
+        run(1500, 1501, K + 1, 7, 24, dtype, b_major=b_major, ids="mixed")
+        run(300, 701, K + 1, 7, 16, dtype, b_major=b_major, ids="packed")
 
 
 @pytest.mark.parametrize("M", [1, 48, 600])

@@ -434,7 +434,7 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
 // The same for a whole workgroup on 16-bit inputs, through LDS (the ring, free
 // after the main loop): v of the tile's rows, scaled and split, is put there
 // once for all waves, and each adapter's rows for the tile's columns come in
-// by direct loads, one adapter ahead of the one that is multiplied.  The MFMAs
+// by direct loads, up to three adapters ahead of the one that is multiplied.  The MFMAs
 // add straight into the accumulators (temporaries beside the 256x256 tile's
 // accumulators spilled); rows of other adapters enter them as zeros.  That
 // keeps rows apart only while the adapter is finite, so infinities and NaN in
@@ -450,8 +450,10 @@ struct SharedLora {
     using OV = DmaOperand<BM, CH, NW, true, MI>;       // for its fragments
     using OU = DmaOperand<BN, CH, NW, true, MI>;
     static constexpr int V_BYTES = BM * CH * 2, U_BYTES = OU::BYTES;
-    static constexpr int TAB = 2 * V_BYTES + 2 * U_BYTES, ROWS = TAB + BM * 8, BAD = ROWS + BM * 8;
-    static_assert(BAD + 16 <= KT::SMEM, "fits the ring");
+    static constexpr int SMALL = BM * 16 + 16;         // tables
+    static constexpr int FIT = (KT::SMEM - 2 * V_BYTES - SMALL) / U_BYTES, NU = FIT < 4 ? FIT : 4;   // adapters in LDS
+    static constexpr int TAB = 2 * V_BYTES + NU * U_BYTES, ROWS = TAB + BM * 8, BAD = ROWS + BM * 8;
+    static_assert(NU >= 2 && (NU - 2) * OU::IPW < 64, "fits the ring; vmcnt range");
     static_assert(64 % WTM == 0, "a wave's rows in one mask");
 
     // True: an adapter held infinities or NaN (repair has work).
@@ -462,7 +464,7 @@ struct SharedLora {
         const int wm = wave / WN, wn = wave % WN;
         char* const vh = smem;
         char* const vl = smem + V_BYTES;
-        char* const ub = smem + 2 * V_BYTES;           // two buffers
+        char* const ub = smem + 2 * V_BYTES;           // NU buffers
         float* const tab = (float*)(smem + TAB);       // fp16: 2^e of each row, then 2^-e
         int* const row_id = (int*)(smem + ROWS);       // -1: none
         float* const row_scale = (float*)(row_id + BM);
@@ -522,37 +524,49 @@ struct SharedLora {
                 const int c = swz_chunk<OU::CPR, true>(slot / OU::CPR, slot % OU::CPR);
                 o.voff[j] = c * 8 < left ? ou.voff[j] : kNowhere;          // past the rank: zeros
             }
-            o.issue(q.up + a * q.s_up + (int64_t)n0 * q.ld_up * 2 + r0 * 2,
-                    rows_extent(min(p.N - n0, BN), q.ld_up * 2, row_tail<2, true>(q.R - r0)), q.ld_up, 0, 0, dst, wave);
+            // Past the last adapter: an empty extent, zeros that nobody reads.
+            o.issue(q.up + max(a, 0) * q.s_up + (int64_t)n0 * q.ld_up * 2 + r0 * 2,
+                    a < 0 ? 0 : rows_extent(min(p.N - n0, BN), q.ld_up * 2, row_tail<2, true>(q.R - r0)), q.ld_up, 0, 0, dst, wave);
         };
         bool found = false, first = true;
         for (int r0 = 0; r0 < q.pitch; r0 += CH) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) left_rows[c] = __builtin_amdgcn_ballot_w64(id[c] >= 0);
             __syncthreads();                           // row_id is written; v and U have been read
-            int rk;
-            uint64_t rows;
-            int a = next(rk, rows);
-            if (a < 0) return false;
-            issue(a, min(rk - r0, CH), r0, ub);
+            int a[NU - 1], rk[NU - 1];                 // the adapters in LDS or on their way
+            uint64_t rows[NU - 1];
+#pragma unroll
+            for (int i = 0; i < NU - 1; ++i) {
+                a[i] = next(rk[i], rows[i]);
+                if (a[0] < 0) return false;
+                issue(a[i], min(rk[i] - r0, CH), r0, ub + i * U_BYTES);
+            }
             stage_v(p, q, vh, vl, tab, row_id, row_scale, m0, r0, tid);
-            for (int buf = 0; a >= 0; buf ^= 1) {
-                const int left = min(rk - r0, CH);
-                const uint64_t own = rows;
+            for (int buf = 0; a[0] >= 0; buf = buf + 1 == NU ? 0 : buf + 1) {
+                const int left = min(rk[0] - r0, CH);
+                const uint64_t own = rows[0];
                 char* const u = ub + buf * U_BYTES;
-                wait_vmcnt<0>();
-                __syncthreads();                       // this adapter has landed, the other buffer been read
+                wait_vmcnt<(NU - 2) * OU::IPW>();
+                __builtin_amdgcn_s_waitcnt(0xc07f);
+                bare_barrier();                        // this adapter has landed, the last one been read
                 if (first) rescale(acc, tab, wm, lane);
                 first = false;
-                a = next(rk, rows);
-                if (a >= 0) issue(a, min(rk - r0, CH), r0, ub + (buf ^ 1) * U_BYTES);
+#pragma unroll
+                for (int i = 0; i + 1 < NU - 1; ++i) {
+                    a[i] = a[i + 1];
+                    rk[i] = rk[i + 1];
+                    rows[i] = rows[i + 1];
+                }
+                a[NU - 2] = next(rk[NU - 2], rows[NU - 2]);
+                issue(a[NU - 2], min(rk[NU - 2] - r0, CH), r0, ub + (buf == 0 ? NU - 1 : buf - 1) * U_BYTES);
                 if (left > 0) {
                     clean(u, left, bad, tid);
                     __builtin_amdgcn_s_waitcnt(0xc07f);
-                    bare_barrier();                    // (no fence: the next adapter is on its way)
+                    bare_barrier();                    // (no fence: the next adapters are on their way)
                     if (own) multiply(acc, vh, vl, u, own, left, wm, wn, lane);
                 }
             }
+            wait_vmcnt<0>();                           // the empty loads have landed
             __syncthreads();
             found = found || *bad;
         }
@@ -1145,12 +1159,16 @@ struct LoraInst {
             //     32  16   30.4       23.8       27.2
             //     64  16   53.3       38.3       30.5    34.5      65.6
             //    128  64                         42.9    31.9      37.4      62.6        100
-            //    256  64                         43.3    48.9      37.4      60.9        103
-            //   1024  64                                           82.2      64.4        102
-            //   2048  64                                          151       111         107
+            //    256  64                         43.3    48.9      33.9      56.1        103
+            //    512  64                                           49.5      55.0        103
+            //   1024  64                                           86.4      59.5        102
+            //   2048  64                                          151       109         107
             //   8192  64                                          482       367         234
             // (str.: the streaming kernel for few rows, B k-major only; sh.:
-            // adapters through LDS for the whole workgroup.)
+            // adapters through LDS for the whole workgroup, of eight waves from
+            // 64x64 on: 1024 rows 66.5 on four.)  64x64 tiles that the chip
+            // holds at once take 128 of k at a time in three stages (33.9 us at
+            // 256 rows, 36.6 with 64 in four; at 512 rows 56.9 and 49.5).
             auto tiles = [&](int t) { return ((int64_t)c.p.M + t - 1) / t * ((c.p.N + t - 1) / t); };
             if constexpr (BKM) {
                 if (c.p.M <= 16) return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 1, 8, 4, 4>, c, 16, 16, 768, s);
@@ -1160,8 +1178,9 @@ struct LoraInst {
             if (c.p.M <= 96) return dma<32, 32, 128, 2, 2, 4, 4, BKM>(c, s);
             if (c.p.M <= 144) return dma<32, 32, 128, 2, 2, 4, 0, BKM>(c, s);
             if (tiles(256) >= 100) return launch_lora(&gemm_lora_pp_kernel<TI, TO, BKM>, c, 256, 256, 512, s);
-            if (tiles(64) <= 512) return dma<64, 64, 64, 2, 2, 4, 0, BKM>(c, s);
-            return dma<128, 128, 64, 2, 2, 4, 0, BKM>(c, s);
+            if (tiles(64) <= 256) return dma<64, 64, 128, 2, 4, 3, 0, BKM>(c, s);
+            if (tiles(64) <= 512) return dma<64, 64, 64, 2, 4, 4, 0, BKM>(c, s);
+            return dma<128, 128, 64, 2, 4, 4, 0, BKM>(c, s);
         }
     }
     static hipError_t launch(const LoraCall& c, hipStream_t s)

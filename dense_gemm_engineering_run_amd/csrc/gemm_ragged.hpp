@@ -705,19 +705,20 @@ struct RaggedInst {
     //      16         8     4096 x 4096   55.9  53.2 [62.8] 61.8 [47.5] 62.5  74.1  75
     //      16        64     2048 x 1024   60.3  56.9   51.5   61.1   59.0   85
     //      64         8     4096 x 4096  100    77.4   67.3   90.4   78.7   88.9
-    //     128         8     4096 x 4096  168   118     95.6   89.0   81.5   89.2
-    //     128        32     2048 x 4096                155    143    154    194
-    //     256         8     4096 x 4096               132    121    131     90.9
-    //     256         8     2048 x 1024                21.1   25.7   20.8   23.5
+    //     128         8     4096 x 4096  168   118     95.6   89.0   80.2   89.2
+    //     128        32     2048 x 4096                155    143    153    194
+    //     256         8     4096 x 4096               132    121    126     90.9
+    //     256         8     2048 x 1024                21.1   25.7   20.2   23.5
     //    1024         8     4096 x 2048               206    190    175    140
     //    4096         8     4096 x 4096                      1270   1150    847
+    // (128x256 on eight waves of 16x16 MFMAs; on four of 32x32: 82.8 and 160 at
+    // 128 rows.)  Too few tiles of 128x256: 128x128, from 192 rows on in two
+    // stages, two workgroups a CU (22.9 us at 256 rows in 8 groups of 2048 x
+    // 1024, 24.6 in four stages).
     // Products too small to fill the chip with those take the tile that spreads
     // them further: 1 group of 48 rows of 1024 x 4096 14.6 on 32x64 (25.8 on
     // 64x128), 4 groups of 128 20.2 (34.3 on 128x128), 4 groups of 300 28.0 on
     // 128x64 (37.1 on 128x128).
-    // 128x128 in two stages, two workgroups a CU: 18.5 us at 256 rows in 8
-    // groups of 2048 x 1024 (64 tiles of 256x256), 33.4 at 512 (128 tiles;
-    // 256x256: 25.7).
     template <bool BKM>
     static hipError_t rows(const RaggedCall& c, hipStream_t s)
     {
@@ -730,12 +731,9 @@ struct RaggedInst {
             else return dma<64, 128, 64, 2, 2, 16, 3, true, BKM, By::Rows, false>(c, s);
         }
         if (avg <= 80) return dma<64, 128, 64, 2, 2, 16, 3, true, BKM, By::Rows, false>(c, s);
-        if (avg < 192) {
-            if (tiles(128, 256) >= 100)
-                return dma<128, 256, 64, 2, 2, 32, 3, true, BKM, By::Rows, false>(c, s);
-            return dma<128, 128, 64, 2, 2, 16, 4, true, BKM, By::Rows, false>(c, s);
-        }
-        if (tiles(256, 256) >= 100) return pp<true, BKM, By::Rows, false>(c, s);
+        if (avg >= 192 && tiles(256, 256) >= 100) return pp<true, BKM, By::Rows, false>(c, s);
+        if (tiles(128, 256) >= 100) return dma<128, 256, 64, 2, 4, 16, 3, true, BKM, By::Rows, false>(c, s);
+        if (avg < 192) return dma<128, 128, 64, 2, 2, 16, 4, true, BKM, By::Rows, false>(c, s);
         return dma<128, 128, 64, 2, 2, 32, 2, true, BKM, By::Rows, false>(c, s);
     }
     // By k: 256x256 tiles from half a CU's share of them up (bf16 -> fp32, 8

@@ -171,6 +171,36 @@ __device__ __forceinline__ bool select_group(Params& p, const Ragged& r, int lan
 
 // ------------------------------------------------------- direct-to-LDS kernels
 
+// Rows of C from LDS, where a wave has put KT::RPP of them, to memory in
+// 16-byte chunks.  The stores are non-temporal: nothing here reads C again, and
+// what the caches would keep of it is room for the operands (256x256 tiles, us,
+// with plain stores in brackets: 8192 k in 16 and 32 groups of 4096 x 2048 into
+// fp32 188 (211) and 284 (323), into bf16 in 32 groups 201 (245); 8192 rows in
+// 16 groups, 4096 x 2048, 144 (151)).
+template <class KT>
+__device__ __forceinline__ void copy_rows(const Params& p, const char* w, int m0, int n0, int lane)
+{
+    constexpr int EO = KT::OBY, EPC = 16 / EO, RPI = 64 / KT::SCPR;
+#pragma unroll
+    for (int r0 = 0; r0 < KT::RPP; r0 += RPI) {
+        const int r = r0 + lane / KT::SCPR, ch = lane % KT::SCPR;
+        const i32x4 v = *(const i32x4*)(w + r * KT::SPITCH + ch * 16);
+        const int m = m0 + r, n = n0 + ch * EPC;
+        if (m >= p.M) continue;
+        char* dst = p.C + ((int64_t)m * p.ldc + n) * EO;
+        if (p.c_vec && n + EPC <= p.N) {
+            __builtin_nontemporal_store(v, (i32x4*)dst);
+        } else {
+#pragma unroll
+            for (int e = 0; e < EPC; ++e)
+                if (n + e < p.N) {
+                    if constexpr (EO == 4) ((int*)dst)[e] = v[e];
+                    else ((uint16_t*)dst)[e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e % 2)));
+                }
+        }
+    }
+}
+
 // Store a tile held by a Dma16 engine: through the elementwise epilogue (EPI),
 // as whole rows through LDS, or element by element.
 template <class KT, bool EPI>
@@ -182,7 +212,22 @@ __device__ __forceinline__ void store_tile(const Params& p, char* smem, int m0, 
     } else {
         if (KT::ROWS_OK && p.c_vec) {
             bare_barrier();   // every wave's loads have landed and its ring reads are done
-            if constexpr (KT::ROWS_OK) KT::store_rows(p, smem, m0, n0, acc, lane, wave);
+            if constexpr (KT::ROWS_OK) {
+                constexpr int WN = KT::TILE_N / KT::WTN, MI = KT::WTM / KT::TM;
+                char* const w = smem + wave * KT::SHARE;
+#pragma unroll
+                for (int pass = 0; pass < KT::WTM / KT::RPP; ++pass) {
+#pragma unroll
+                    for (int i = pass * KT::RPP / MI; i < (pass + 1) * KT::RPP / MI; ++i)
+#pragma unroll
+                        for (int j = 0; j < KT::TN; ++j)
+#pragma unroll
+                            for (int q = 0; q < KT::R; ++q)
+                                store_out<KT::OUT>(w + (KT::row(0, i, q, lane) - pass * KT::RPP) * KT::SPITCH,
+                                                   KT::col(0, j, lane), acc[i][j][q]);
+                    copy_rows<KT>(p, w, m0 + wave / WN * KT::WTM + pass * KT::RPP, n0 + wave % WN * KT::WTN, lane);
+                }
+            }
         } else {
             KT::store_direct(p, m0, n0, acc, lane, wave);
         }
@@ -533,7 +578,7 @@ struct PingPong {
                                                  int lane, int wave)
     {
         static_assert(SWAP, "a lane's accumulators run along a row");
-        constexpr int EO = KT::OBY, EPC = 16 / EO, RPI = 64 / KT::SCPR;
+        constexpr int EO = KT::OBY;
         const int wm = wave / WN, wn = wave % WN;
         char* const w = smem + wave * KT::SHARE;
         const int mb = m0 + wm * WTM, nb = n0 + wn * WTN;
@@ -557,24 +602,7 @@ struct PingPong {
                         *(u32x2*)d = u32x2{(unsigned)h[0] | ((unsigned)h[1] << 16), (unsigned)h[2] | ((unsigned)h[3] << 16)};
                     }
                 }
-#pragma unroll
-            for (int r0 = 0; r0 < KT::RPP; r0 += RPI) {
-                const int r = r0 + lane / KT::SCPR, ch = lane % KT::SCPR;
-                i32x4 v = *(const i32x4*)(w + r * KT::SPITCH + ch * 16);
-                const int m = mb + pass * KT::RPP + r, n = nb + ch * EPC;
-                if (m >= p.M) continue;
-                char* dst = p.C + ((int64_t)m * p.ldc + n) * EO;
-                if (p.c_vec && n + EPC <= p.N) {
-                    *(i32x4*)dst = v;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < EPC; ++e)
-                        if (n + e < p.N) {
-                            if constexpr (EO == 4) ((int*)dst)[e] = v[e];
-                            else ((uint16_t*)dst)[e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e % 2)));
-                        }
-                }
-            }
+            copy_rows<KT>(p, w, mb + pass * KT::RPP, nb, lane);
         }
     }
 };

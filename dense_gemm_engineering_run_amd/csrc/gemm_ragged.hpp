@@ -181,6 +181,21 @@ template <class KT>
 __device__ __forceinline__ void copy_rows(const Params& p, const char* w, int m0, int n0, int lane)
 {
     constexpr int EO = KT::OBY, EPC = 16 / EO, RPI = 64 / KT::SCPR;
+    if (!p.c_vec) {               // rows that start at any element: one element a lane (4095 for 4096: 156 us)
+        using E = std::conditional_t<EO == 4, int, uint16_t>;
+        constexpr int AT = 64 / KT::WTN > 0 ? 64 / KT::WTN : 1, STEP = KT::WTN < 64 ? KT::WTN : 64;
+        static_assert(STEP * AT == 64 && KT::RPP % AT == 0 && KT::WTN % STEP == 0, "64 elements at a time");
+        const int r1 = lane / STEP, c1 = lane % STEP;
+        E* const dst = (E*)p.C + (int64_t)(m0 + r1) * p.ldc + n0 + c1;
+#pragma unroll 8
+        for (int r0 = 0; r0 < KT::RPP; r0 += AT)
+#pragma unroll
+            for (int c0 = 0; c0 < KT::WTN; c0 += STEP) {
+                const E v = ((const E*)(w + (r0 + r1) * KT::SPITCH))[c0 + c1];
+                if (m0 + r0 + r1 < p.M && n0 + c0 + c1 < p.N) __builtin_nontemporal_store(v, dst + (int64_t)r0 * p.ldc + c0);
+            }
+        return;
+    }
 #pragma unroll
     for (int r0 = 0; r0 < KT::RPP; r0 += RPI) {
         const int r = r0 + lane / KT::SCPR, ch = lane % KT::SCPR;
@@ -188,7 +203,7 @@ __device__ __forceinline__ void copy_rows(const Params& p, const char* w, int m0
         const int m = m0 + r, n = n0 + ch * EPC;
         if (m >= p.M) continue;
         char* dst = p.C + ((int64_t)m * p.ldc + n) * EO;
-        if (p.c_vec && n + EPC <= p.N) {
+        if (n + EPC <= p.N) {
             __builtin_nontemporal_store(v, (i32x4*)dst);
         } else {
 #pragma unroll
@@ -211,8 +226,8 @@ __device__ __forceinline__ void store_tile(const Params& p, char* smem, int m0, 
         KT::store_staged(p, smem, m0, n0, acc, tid, lane, wave);
     } else {
         if (KT::ROWS_OK && p.c_vec) {
-            bare_barrier();   // every wave's loads have landed and its ring reads are done
             if constexpr (KT::ROWS_OK) {
+                bare_barrier();   // every wave's loads have landed and its ring reads are done
                 constexpr int WN = KT::TILE_N / KT::WTN, MI = KT::WTM / KT::TM;
                 char* const w = smem + wave * KT::SHARE;
 #pragma unroll
@@ -707,12 +722,15 @@ struct RaggedInst {
         if (avg <= 80) return odd<64, 128, 64, 2, 4, 2, true, BKM, By::Rows, false>(c, s);
         return odd<128, 128, 64, 2, 4, 2, true, BKM, By::Rows, false>(c, s);
     }
-    // 8192 k in 16 groups of 4095 x 2047, bf16 -> fp32: 893 us; on 64x64 tiles
-    // of four waves 997, on 256x128 890.  In 8 groups of 511 x 511 (128 tiles)
-    // 48.6, 60 and 50.
+    // bf16 -> fp32, us: 8192 k in 16 groups of 4095 x 2047 402 (on 64x64 tiles
+    // 561); 4096 k in 4 groups of 1023 x 1023, 256 tiles, 30.0 (38.2 on 64x64
+    // with 128 k at a time); 8192 k in 8 groups of 511 x 511, 128 tiles, 34.6
+    // (26.7); in 4 groups of 255 x 255 47.1 (29.8).
     template <bool EPI>
     static hipError_t odd_k(const RaggedCall& c, hipStream_t s)
     {
+        const int64_t tiles = ((int64_t)c.p.M + 127) / 128 * ((c.p.N + 127) / 128) * c.r.groups;
+        if (tiles <= 128) return odd<64, 64, 128, 2, 4, 2, false, false, By::K, EPI>(c, s);
         return odd<128, 128, 64, 4, 2, 2, false, false, By::K, EPI>(c, s);
     }
     template <int BM, int BN, int BK, int WM, int WN, int MI, int ST, bool AK, bool BKM, By BY, bool EPI>

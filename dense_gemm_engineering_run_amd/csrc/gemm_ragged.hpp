@@ -782,18 +782,21 @@ struct RaggedInst {
         if (avg < 192) return dma<128, 128, 64, 2, 2, 16, 4, true, BKM, By::Rows, false>(c, s);
         return dma<128, 128, 64, 2, 2, 32, 2, true, BKM, By::Rows, false>(c, s);
     }
-    // By k: 256x256 tiles from half a CU's share of them up (bf16 -> fp32, 8
-    // groups: 4096 x 2048 of 8192 k 161 us against 197 on 128x128; 64 groups of
-    // 512 x 512, 256 tiles, 22.3 against 23.6), then 128x128 in two stages (8
-    // groups of 1024 x 1024, 128 tiles of 256x256: 36.4 against 48.3), and
-    // 64x64 where even those leave CUs idle (8 groups of 512 x 512 of 8192 k:
-    // 19.8 against 27.6).
+    // By k: 256x256 tiles from three quarters of a CU's share of them up (bf16 ->
+    // fp32, 8 groups: 4096 x 2048 of 8192 k 161 us against 197 on 128x128; 4
+    // groups of 2048 x 2048 of 4096 k, 256 tiles, 43.2 against 48.1), then
+    // 128x128 in two stages, two workgroups a CU (8 groups of 1024 x 1024, 128
+    // tiles of 256x256: 36.4 against 47.1), up to one a CU in four (4 groups of
+    // 1024 x 1024: 19.5 against 24.4), and 64x64 where even those leave CUs idle
+    // (8 groups of 512 x 512 of 8192 k: 19.9 against 22.1; in 4 groups of 256 x
+    // 256 19.7 against 29.3).
     template <bool EPI>
     static hipError_t by_k(const RaggedCall& c, hipStream_t s)
     {
         auto tiles = [&](int t) { return ((int64_t)c.p.M + t - 1) / t * ((c.p.N + t - 1) / t) * c.r.groups; };
         if (tiles(256) >= 192) return pp<false, false, By::K, EPI>(c, s);
-        if (tiles(128) >= 192) return dma<128, 128, 64, 2, 2, 32, 2, false, false, By::K, EPI>(c, s);
+        if (tiles(128) > 256) return dma<128, 128, 64, 2, 2, 32, 2, false, false, By::K, EPI>(c, s);
+        if (tiles(128) >= 192) return dma<128, 128, 64, 2, 4, 16, 4, false, false, By::K, EPI>(c, s);
         return dma<64, 64, 64, 2, 2, 32, 4, false, false, By::K, EPI>(c, s);
     }
     static hipError_t launch(const RaggedCall& c, hipStream_t s)

@@ -864,31 +864,17 @@ gemm_lora_f32_kernel(Params p, Lora q)
     KT::template store<false, false>(p, m0, n0, acc, lane, wave, smem);
 }
 
-// Few rows (a decoding step): the product streams B once and is bound by how
-// many of its bytes are in flight.  A workgroup has 16 MT rows and 16 NT
-// columns.  NW of its waves take the k-tiles in turn, each with a ring of ST
-// tiles of its own in LDS: nothing waits for another wave until the sums meet
-// at the end, in wave order.  A tile's slot is loaded again as soon as its
-// fragments are in registers.  NL more waves share out the rows' adapters: the
-// chain of loads they wait for (ids, then slots, then the adapters) runs
-// beside the stream.
+// Few rows (a decoding step), on the streaming tile: NL more waves share out
+// the rows' adapters, so that the chain of loads they wait for (ids, then
+// slots, then the adapters) runs beside the stream.
 template <In TI, Out TO, int MT, int NT, int NW, int ST, int NL, bool BKM = true, bool VEC = true>
 __global__ void __launch_bounds__((NW + NL) * 64)
 gemm_lora_skinny_kernel(Params p, Lora q)
 {
-    // A k-tile is 128 bytes of a row: 64 or 32 of k.
-    constexpr bool F32 = TI == In::F32;
-    constexpr int ES = F32 ? 4 : 2, BK = 128 / ES, MI = 16, NG = 2, NT_ALL = (NW + NL) * 64;
-    using OA = std::conditional_t<F32, F32Operand<MT * 16, BK, 1, true, VEC>, DmaOperand<MT * 16, BK, 1, true, MI>>;
-    using OB = std::conditional_t<F32, F32Operand<NT * 16, BK, 1, BKM, VEC>, DmaOperand<NT * 16, BK, 1, true, MI>>;
-    static_assert(F32 || (BKM && VEC), "16-bit operands: k-major, 16-byte loads");
-    constexpr int STAGE = OA::BYTES + OB::BYTES, L = (OA::IPW + OB::IPW) * (VEC ? 1 : 4);
-    constexpr int PART = MT * 16 * NT * 16;            // sums of a wave
-    constexpr int RING = NW * ST * STAGE;
+    using T = Skinny<TI, MT, NT, NW, ST, BKM, VEC>;
     constexpr int NB = (MT * 16 + NL - 1) / NL > 8 ? 8 : (MT * 16 + NL - 1) / NL;   // adapters at a time
-    static_assert((NW + NL) * PART * 4 <= RING && (ST - 1) * L < 64, "sums fit the ring; vmcnt range");
-    static_assert(RING + NL * 512 <= 160 * 1024, "LDS budget");
-    __shared__ __attribute__((aligned(1024))) char smem[RING + NL * 512];
+    static_assert((NW + NL) * T::PART * 4 <= T::RING && T::RING + NL * 512 <= 160 * 1024, "sums fit the ring; LDS budget");
+    __shared__ __attribute__((aligned(1024))) char smem[T::RING + NL * 512];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // The row tiles of one column tile sit on one XCD, so that its L2 gives
     // them the same rows of B.
@@ -897,90 +883,13 @@ gemm_lora_skinny_kernel(Params p, Lora q)
     const int tn = chunk * 8 + in % 8;
     if (tn >= p.tiles_n) return;
     const int m0 = in / 8 * (MT * 16), n0 = tn * (NT * 16);
-    f32x4 acc[MT][NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (wave >= NW) {
-        lora_add<TI, VEC, NB, MI, MT, NT>(p, q, acc, m0, n0, lane, (float*)(smem + RING) + 128 * (wave - NW), wave - NW, NL);
-    } else {
-        const int nkt = (p.K + BK - 1) / BK, left = p.K - (nkt - 1) * BK;
-        OA oa;
-        OB ob;
-        oa.init(0, lane, p.lda);
-        ob.init(0, lane, p.ldb);
-        char* const ring = smem + wave * ST * STAGE;
-        auto issue = [&](int t, int slot) {            // past the end: an empty extent, zeros
-            char* s = ring + slot * STAGE;
-            oa.issue(p.A, t < nkt ? p.a_bytes : 0, p.lda, m0, t * BK, s, 0);
-            ob.issue(p.B, t < nkt ? p.b_bytes : 0, p.ldb, n0, t * BK, s + OA::BYTES, 0);
-        };
-#pragma unroll
-        for (int i = 0; i < ST; ++i) issue(wave + i * NW, i);
-        int slot = 0;
-        for (int t = wave; t < nkt; t += NW) {
-            wait_vmcnt<(ST - 1) * L>();
-            char* s = ring + slot * STAGE;
-            if (t == nkt - 1 && left != BK) {
-                oa.template zero_tail<64>(s, left, lane);
-                if constexpr (BKM) ob.template zero_tail<64>(s + OA::BYTES, left, lane);
-                __builtin_amdgcn_s_waitcnt(0xc07f);
-            }
-            asm volatile("" ::: "memory");
-            // Fragment g: the 16 bytes of k-chunk 4 g + lane / 16 of a row.  A
-            // chunk of an n-major B is four values of one column.
-            auto chunk = [&](const char* tile, int row, int g) {
-                return *(const i32x4*)(tile + row * 128 + swz_chunk<8, true>(row, g * 4 + lane / 16) * 16);
-            };
-            i32x4 fa[NG][MT], fb[NG][NT];
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-#pragma unroll
-                for (int i = 0; i < MT; ++i) fa[g][i] = chunk(s, i * MI + lane % MI, g);
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const int n = j * MI + lane % MI;
-                    if constexpr (BKM) {
-                        fb[g][j] = chunk(s + OA::BYTES, n, g);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            fb[g][j][e] = ((const int*)(s + OA::BYTES))[(g * 16 + lane / 16 * 4 + e) * (NT * MI) + n];
-                    }
-                }
-            }
-            __builtin_amdgcn_s_waitcnt(0xc07f);        // lgkmcnt(0): the slot has been read
-            __builtin_amdgcn_sched_barrier(0);
-            issue(t + ST * NW, slot);
-            slot = slot + 1 == ST ? 0 : slot + 1;
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) mfma_step<TI, MI>(fa[g][i], fb[g][j], acc[i][j]);
-        }
-        wait_vmcnt<0>();                               // the empty loads have landed
-    }
-    __syncthreads();
-    float* const part = (float*)smem;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                part[wave * PART + (i * 16 + lane / 16 * 4 + e) * (NT * 16) + j * 16 + lane % 16] = acc[i][j][e];
-    __syncthreads();
-    for (int x = tid; x < PART; x += NT_ALL) {
-        const int m = m0 + x / (NT * 16), n = n0 + x % (NT * 16);
-        if (m >= p.M || n >= p.N) continue;
-        float v = part[x];
-#pragma unroll
-        for (int w = 1; w < NW + NL; ++w) v += part[w * PART + x];
-        store_out<TO>(p.C, (int64_t)m * p.ldc + n, v);
-    }
+    typename T::Acc acc;
+    T::zero(acc);
+    if (wave >= NW)
+        lora_add<TI, VEC, NB, 16, MT, NT>(p, q, acc, m0, n0, lane, (float*)(smem + T::RING) + 128 * (wave - NW), wave - NW, NL);
+    else
+        T::stream(p, smem, m0, n0, acc, lane, wave);
+    T::template join<TO, NW + NL>(p, smem, m0, n0, acc, tid, lane, wave);
 }
 
 // ... on the ping-pong schedule (16-bit inputs, 256x256 tiles).

@@ -662,6 +662,138 @@ gemm_ragged_f32_kernel(Params p, Ragged r)
     KT::template store<false, EPI>(p, m0, n0, acc, lane, wave, smem);
 }
 
+// Few rows: the product streams B once and is bound by how many of its bytes
+// are in flight.  A workgroup has 16 MT rows and 16 NT columns.  NW waves take
+// the k-tiles in turn, each with a ring of ST tiles of its own in LDS: nothing
+// waits for another wave until the sums meet at the end, in wave order.  A
+// tile's slot is loaded again as soon as its fragments are in registers.
+template <In TI, int MT, int NT, int NW, int ST, bool BKM, bool VEC>
+struct Skinny {
+    // A k-tile is 128 bytes of a row: 64 or 32 of k.
+    static constexpr bool F32 = TI == In::F32;
+    static constexpr int ES = F32 ? 4 : 2, BK = 128 / ES, MI = 16, NG = 2;
+    using OA = std::conditional_t<F32, F32Operand<MT * 16, BK, 1, true, VEC>, DmaOperand<MT * 16, BK, 1, true, MI>>;
+    using OB = std::conditional_t<F32, F32Operand<NT * 16, BK, 1, BKM, VEC>, DmaOperand<NT * 16, BK, 1, true, MI>>;
+    static_assert(F32 || (BKM && VEC), "16-bit operands: k-major, 16-byte loads");
+    static constexpr int STAGE = OA::BYTES + OB::BYTES, L = (OA::IPW + OB::IPW) * (VEC ? 1 : 4);
+    static constexpr int PART = MT * 16 * NT * 16;            // sums of a wave
+    static constexpr int RING = NW * ST * STAGE;
+    static_assert((ST - 1) * L < 64, "vmcnt range");
+    typedef f32x4 Acc[MT][NT];
+
+    __device__ static __forceinline__ void zero(Acc& acc)
+    {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // This wave's k-tiles.
+    __device__ static __forceinline__ void stream(const Params& p, char* smem, int m0, int n0, Acc& acc, int lane, int wave)
+    {
+        const int nkt = (p.K + BK - 1) / BK, left = p.K - (nkt - 1) * BK;
+        OA oa;
+        OB ob;
+        oa.init(0, lane, p.lda);
+        ob.init(0, lane, p.ldb);
+        char* const ring = smem + wave * ST * STAGE;
+        auto issue = [&](int t, int slot) {            // past the end: an empty extent, zeros
+            char* s = ring + slot * STAGE;
+            oa.issue(p.A, t < nkt ? p.a_bytes : 0, p.lda, m0, t * BK, s, 0);
+            ob.issue(p.B, t < nkt ? p.b_bytes : 0, p.ldb, n0, t * BK, s + OA::BYTES, 0);
+        };
+#pragma unroll
+        for (int i = 0; i < ST; ++i) issue(wave + i * NW, i);
+        int slot = 0;
+        for (int t = wave; t < nkt; t += NW) {
+            wait_vmcnt<(ST - 1) * L>();
+            char* s = ring + slot * STAGE;
+            if (t == nkt - 1 && left != BK) {
+                oa.template zero_tail<64>(s, left, lane);
+                if constexpr (BKM) ob.template zero_tail<64>(s + OA::BYTES, left, lane);
+                __builtin_amdgcn_s_waitcnt(0xc07f);
+            }
+            asm volatile("" ::: "memory");
+            // Fragment g: the 16 bytes of k-chunk 4 g + lane / 16 of a row.  A
+            // chunk of an n-major B is four values of one column.
+            auto chunk = [&](const char* tile, int row, int g) {
+                return *(const i32x4*)(tile + row * 128 + swz_chunk<8, true>(row, g * 4 + lane / 16) * 16);
+            };
+            i32x4 fa[NG][MT], fb[NG][NT];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i) fa[g][i] = chunk(s, i * MI + lane % MI, g);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const int n = j * MI + lane % MI;
+                    if constexpr (BKM) {
+                        fb[g][j] = chunk(s + OA::BYTES, n, g);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            fb[g][j][e] = ((const int*)(s + OA::BYTES))[(g * 16 + lane / 16 * 4 + e) * (NT * MI) + n];
+                    }
+                }
+            }
+            __builtin_amdgcn_s_waitcnt(0xc07f);        // lgkmcnt(0): the slot has been read
+            __builtin_amdgcn_sched_barrier(0);
+            issue(t + ST * NW, slot);
+            slot = slot + 1 == ST ? 0 : slot + 1;
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) mfma_step<TI, MI>(fa[g][i], fb[g][j], acc[i][j]);
+        }
+        wait_vmcnt<0>();                               // the empty loads have landed
+    }
+
+    // The sums of all WAVES waves, stored.
+    template <Out TO, int WAVES>
+    __device__ static __forceinline__ void join(const Params& p, char* smem, int m0, int n0, const Acc& acc, int tid, int lane,
+                                                int wave)
+    {
+        static_assert(WAVES * PART * 4 <= RING, "sums fit the ring");
+        __syncthreads();
+        float* const part = (float*)smem;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    part[wave * PART + (i * 16 + lane / 16 * 4 + e) * (NT * 16) + j * 16 + lane % 16] = acc[i][j][e];
+        __syncthreads();
+        for (int x = tid; x < PART; x += WAVES * 64) {
+            const int m = m0 + x / (NT * 16), n = n0 + x % (NT * 16);
+            if (m >= p.M || n >= p.N) continue;
+            float v = part[x];
+#pragma unroll
+            for (int w = 1; w < WAVES; ++w) v += part[w * PART + x];
+            store_out<TO>(p.C, (int64_t)m * p.ldc + n, v);
+        }
+    }
+};
+
+template <int MT, int NT, int NW, int ST, bool BKM, bool VEC>
+__global__ void __launch_bounds__(NW * 64)
+gemm_ragged_skinny_kernel(Params p, Ragged r)
+{
+    using T = Skinny<In::F32, MT, NT, NW, ST, BKM, VEC>;
+    static_assert(T::RING <= 160 * 1024, "LDS budget");
+    __shared__ __attribute__((aligned(1024))) char smem[T::RING];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tm, tn;
+    if (!select_group<In::F32, Out::F32, MT * 16, NT * 16, By::Rows, VEC>(p, r, lane, tm, tn)) return;
+    typename T::Acc acc;
+    T::zero(acc);
+    T::stream(p, smem, tm * (MT * 16), tn * (NT * 16), acc, lane, wave);
+    T::template join<Out::F32, NW>(p, smem, tm * (MT * 16), tn * (NT * 16), acc, tid, lane, wave);
+}
+
 // ------------------------------------------------------------------ launchers
 
 // What the host asks of a dtype's launchers (gemm_ragged_<dtype>.hip).

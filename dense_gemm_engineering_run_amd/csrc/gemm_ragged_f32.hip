@@ -9,6 +9,11 @@ struct RaggedF32 {
     {
         return launch_ragged<BY>(&gemm_ragged_f32_kernel<BM, BN, 32, 2, 2, ST, AK, BKM, BY, EPI, VEC>, c, BM, BN, 256, s);
     }
+    template <int MT, int NT, int NW, int ST, bool BKM, bool VEC>
+    static hipError_t skinny(const RaggedCall& c, hipStream_t s)
+    {
+        return launch_ragged<By::Rows>(&gemm_ragged_skinny_kernel<MT, NT, NW, ST, BKM, VEC>, c, MT * 16, NT * 16, NW * 64, s);
+    }
     template <bool AK, bool BKM, By BY, bool EPI, bool VEC>
     static hipError_t sized(const RaggedCall& c, hipStream_t s)
     {
@@ -25,8 +30,22 @@ struct RaggedF32 {
         auto tiles = [&](int64_t rows, int bm, int bn) {
             return (rows + bm - 1) / bm * ((c.p.N + bn - 1) / bn) * c.r.groups;
         };
+        const int64_t avg = (c.r.rows + c.r.groups - 1) / c.r.groups;
+        if constexpr (BY == By::Rows) {
+            // Few rows stream (16x32, 32x64 and 32x32 tiles; B k-major, n-major
+            // in brackets), against 64x64, us:
+            //        1 row  in 122 groups of  384 x 4224   86.7 [ 95.8]    95.1          94.9   157
+            //       16 rows in   8 groups of 4096 x 4096  109   [121]     113           110     164
+            //       22 rows in  14 groups of 7192 x 5264  569   [632]     455   [441]   505     611
+            //       48 rows in  16 groups of 2048 x 2048   99.5 [107]      92.7          91.8   112
+            //       64 rows in  16 groups of 2048 x 1024                   69.3          68.9    62.9
+            //      300 rows in   1 group  of 1024 x 4096                   40.8          39.8    83.6
+            // (Four waves that share a row's k-tiles also round less than one.)
+            if (avg <= 16) return skinny<1, 2, 4, 3, BKM, VEC>(c, s);
+            if (avg <= 48) return skinny<2, 4, 4, 2, BKM, VEC>(c, s);
+            if (tiles(avg, 64, 64) <= 192) return skinny<2, 2, 4, 2, BKM, VEC>(c, s);
+        }
         if constexpr (BY == By::Rows && VEC) {
-            const int64_t avg = (c.r.rows + c.r.groups - 1) / c.r.groups;
             if (tiles(avg, 64, 128) >= 1024) return go<64, 128, 2, AK, BKM, BY, EPI, VEC>(c, s);
             return go<64, 64, 3, AK, BKM, BY, EPI, VEC>(c, s);
         } else {

@@ -234,8 +234,9 @@ lora_shrink_dma_kernel(Params p, Lora q)
 
 // 8 (16-bit) or 4 (fp32) values of v as MFMA fragments.  v is fp32 and the
 // adapters are 16-bit, so v is split into the part that the type holds and
-// the type's rounding of the rest, one MFMA each: fp16 keeps 22 bits, bf16 16
-// (truncated, so that the first part cannot round up to an infinity).
+// the type's rounding of the rest, one MFMA each: off by at most 2^-22 of
+// itself in fp16, 2^-16 in bf16.  (One term alone would be off by 2^-8 there,
+// more than the output's own rounding where that is fp32.)
 template <In TI>
 struct VFrag {
     static constexpr int N = TI == In::F32 ? 1 : 2;
@@ -256,8 +257,9 @@ struct VFrag {
                     const bool inf = __builtin_fabsf(x) == __builtin_inff();   // then the rest is inf - inf
                     uint32_t a, b;
                     if constexpr (TI == In::BF16) {
-                        a = (uint32_t)__float_as_int(x) >> 16;
-                        if (x != x) a |= 0x40;                                  // a NaN must stay one
+                        // (Not past bf16's largest: that would be an infinity.)
+                        const float most = 0x1.fep127f;
+                        a = __builtin_bit_cast(uint16_t, (__bf16)(inf ? x : fminf(fmaxf(x, -most), most)));
                         const float rest = x - __int_as_float((int)(a << 16));
                         b = __builtin_bit_cast(uint16_t, (__bf16)(inf ? 0.f : rest));
                     } else {

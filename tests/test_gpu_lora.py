@@ -5,8 +5,7 @@ Tolerance, element by element, with S1 = sum_k |a||b|, V_r = sum_k |a||down_r|
 and S2 = |scale| sum_r V_r |up_r|: every sum of n terms is off by at most
 (n + 2) 2^-24 of its magnitudes.  v enters the second product split in two
 terms of the input type: off by 2^-22 of itself for fp16 (two roundings of
-2^-11 and 2^-12), 2^-16 for bf16 (8 bits cut off, the rest rounded by 2^-9 of
-2^-7), not split in fp32; fp16 scales v by row, where the smaller term's
+2^-11), 2^-16 for bf16 (two of 2^-8), not split in fp32; fp16 scales v by row, where the smaller term's
 smallest step is 2^-24 against a row's largest value of 2^13, 2^-37 of the
 row's largest V times sum |up|.  With 2R terms in the second sum, a rounding
 for the scale (of the sum, or of v before it is split) and one for adding:

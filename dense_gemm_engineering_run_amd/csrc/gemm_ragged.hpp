@@ -814,7 +814,11 @@ hipError_t launch_ragged(Kernel kernel, const RaggedCall& c, int BM, int BN, int
     Ragged r = c.r;
     p.tiles_m = (p.M + BM - 1) / BM;
     p.tiles_n = (p.N + BN - 1) / BN;
-    p.group_m = p.tiles_m < 8 ? p.tiles_m : 8;
+    // By k an XCD has 16 tiles of 4096 x 2048 outputs: 4 x 4 of them read fewer
+    // rows of A and B than 8 x 2 (8192 k in 16 groups into fp32 187 us against
+    // 192, in 32 groups 270 against 288).
+    const int high = BY == By::K ? 4 : 8;
+    p.group_m = p.tiles_m < high ? p.tiles_m : high;
     dim3 grid;
     if (BY == By::K) {
         grid = dim3((unsigned)(p.tiles_m * p.tiles_n), (unsigned)r.groups);

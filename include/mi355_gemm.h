@@ -292,10 +292,10 @@ int gemm_run_config(int64_t M, int64_t N, int64_t K, char a_major, char b_major,
  * instead, in fp32 before the rounding to C's type (a group without any k is
  * then left as it was).  C_g must not overlap (GEMM_ERR_BAD_LD).
  *
- * Sizes, alignment (operands that are not 16-byte aligned run element by
- * element; C's own alignment only decides the width of its stores), the
- * checks and their order, asynchrony and errors are those of gemm_run; ends
- * must be 4-byte aligned and not overlap C.  groups <= 65535; groups == 0
+ * Sizes, alignment (operands that are not 16-byte aligned run other kernels;
+ * C's own alignment only decides the width of its stores), the checks and
+ * their order, asynchrony and errors are those of gemm_run; ends must be
+ * 4-byte aligned and not overlap C.  groups <= 65535; groups == 0
  * launches nothing.  No workspace; results are deterministic.  The tile
  * config is the library's choice (gemm_last_config does not record it).
  */
@@ -339,8 +339,8 @@ typedef struct {
 /*
  * The product above, rounded once.  a_major 'k', c_major 'n' (else
  * GEMM_ERR_BAD_MAJOR), b_major 'k' or 'n'.  v and all sums are fp32; v enters
- * the second product as two terms of the input type (22 bits for fp16, 16 for
- * bf16).  Infinities and NaN in one slot reach only the rows that use it.
+ * the second product as two terms of the input type (off by at most 2^-22 of
+ * itself for fp16, 2^-16 for bf16).  Infinities and NaN in one slot reach only the rows that use it.
  * lora NULL, adapters 0, rank 0 or K 0 is the plain product.
  *
  * workspace: at least gemm_lora_workspace_size() bytes of device memory,
@@ -351,7 +351,7 @@ typedef struct {
  * call takes what the arrays hold at each replay.  The workspace, the adapters
  * and the three arrays must not overlap C, nor the workspace any input
  * (GEMM_ERR_ALIAS).  Sizes, alignment (any operand that is not 16-byte
- * aligned: all run element by element), the checks and their order, asynchrony
+ * aligned: the kernels for that run), the checks and their order, asynchrony
  * and errors are otherwise those of gemm_run_ws; results are deterministic.
  */
 int gemm_run_lora(int64_t M, int64_t N, int64_t K, char a_major, char b_major, char c_major,

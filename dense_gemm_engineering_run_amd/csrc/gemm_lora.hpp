@@ -34,6 +34,7 @@ struct Lora {
     int slots, R, pitch;            // pitch: R rounded up to 32
     int splits;                     // ranges of k whose partial sums of v add up
     int z;                          // workgroups sharing a row tile's adapters
+    bool odd_up;          // up's rows are not 16-byte aligned (with any vec)
 };
 
 // R rounded up to whole MFMA steps of any input type.
@@ -430,7 +431,9 @@ template <In TI, bool VEC, int NB, int MI, int TM, int TN, class AccT>
 __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&acc)[TM][TN], int m0, int n0, int lane,
                                          float* tab, int share = 0, int shares = 1)
 {
-    lora_add<TI, VEC, NB, MI>(p, q, acc, m0, n0, lane, tab, share, shares, [&](int j) { return j * MI + lane % MI; });
+    const auto col = [&](int j) { return j * MI + lane % MI; };
+    if (VEC && q.odd_up) lora_add<TI, false, NB < 4 ? NB : 4, MI>(p, q, acc, m0, n0, lane, tab, share, shares, col);
+    else lora_add<TI, VEC, NB, MI>(p, q, acc, m0, n0, lane, tab, share, shares, col);
 }
 
 // The same for a whole workgroup on 16-bit inputs, through LDS (the ring, free
@@ -519,6 +522,19 @@ struct SharedLora {
         OU ou;
         ou.init(wave, lane, q.ld_up);
         auto issue = [&](int a, int left, int r0, char* dst) {
+            if (q.odd_up) {       // through registers (rows of few columns: no loads ahead)
+                const OddRows s(q.up + max(a, 0) * q.s_up + (int64_t)n0 * q.ld_up * 2 + r0 * 2,
+                                a < 0 ? 0 : rows_extent(min(p.N - n0, BN), q.ld_up * 2, (q.R - r0) * 2));
+#pragma unroll 1
+                for (int slot = wave * OU::IPW * 64 + lane; slot < (wave + 1) * OU::IPW * 64; slot += 64) {
+                    const int row = slot / OU::CPR, c = swz_chunk<OU::CPR, true>(row, slot % OU::CPR);
+                    const int off = c * 8 < left ? (int)(row * q.ld_up * 2) + c * 16 : kNowhere;
+                    OddChunk v;
+                    v.load(s, off);
+                    *(i32x4*)(dst + slot * 16) = v.get(s.lead, off);
+                }
+                return;
+            }
             OU o;
 #pragma unroll
             for (int j = 0; j < OU::IPW; ++j) {
@@ -861,8 +877,10 @@ gemm_lora_f32_kernel(Params p, Lora q)
     typename KT::Acc acc;
     KT::zero(acc);
     KT::mainloop(p, smem, oa, ob, m0, n0, 0, (p.K + BK - 1) / BK, acc, tid, lane, wave);
-    lora_add<In::F32, VEC, 2, 32>(p, q, acc, m0 + wave / WN * KT::WTM, n0 + wave % WN * KT::WTN, lane, nullptr, 0, 1,
-                                   [&](int j) { return KT::UB::row(j, lane % 32); });
+    const auto col = [&](int j) { return KT::UB::row(j, lane % 32); };
+    const int rm0 = m0 + wave / WN * KT::WTM, cn0 = n0 + wave % WN * KT::WTN;
+    if (VEC && q.odd_up) lora_add<In::F32, false, 2, 32>(p, q, acc, rm0, cn0, lane, nullptr, 0, 1, col);
+    else lora_add<In::F32, VEC, 2, 32>(p, q, acc, rm0, cn0, lane, nullptr, 0, 1, col);
     KT::template store<false, false>(p, m0, n0, acc, lane, wave, smem);
 }
 

@@ -79,12 +79,13 @@ int run(int64_t M, int64_t N, int64_t K, char a, char b, char c, int dtype, cons
     if (with && (!od.aligned(es) || !ou.aligned(es) ||
                  (((uintptr_t)l.ids | (uintptr_t)l.ranks | (uintptr_t)l.scales) & 3)))
         return GEMM_ERR_MISALIGNED;
-    const bool vec = !reads || (oa.aligned(16) && ob.aligned(16) && (!with || (od.aligned(16) && ou.aligned(16))));
+    const bool vec = !reads || (oa.aligned(16) && ob.aligned(16) && (!with || od.aligned(16)));
+    const bool odd_up = with && !ou.aligned(16);
     const uint64_t cn = oc.bytes(false), need = with ? workspace(M, N, K, l.rank, mg::shrink_tiled(es, vec)) : 0;
     // What is read, against what is written: C and the part of the workspace in use.
     const struct { const void* p; uint64_t n; } in[] = {
         {A, reads ? oa.bytes(vec) : 0}, {B, reads ? ob.bytes(vec) : 0},
-        {l.down, with ? od.bytes(vec) : 0}, {l.up, with ? ou.bytes(vec) : 0}, {l.ids, with ? (uint64_t)M * 4 : 0},
+        {l.down, with ? od.bytes(vec) : 0}, {l.up, with ? ou.bytes(vec && !odd_up) : 0}, {l.ids, with ? (uint64_t)M * 4 : 0},
         {l.ranks, with ? (uint64_t)l.adapters * 4 : 0}, {l.scales, with ? (uint64_t)l.adapters * 4 : 0}};
     for (const auto& x : in)
         if (mg::overlap(C, cn, x.p, x.n) || mg::overlap(ws, need, x.p, x.n)) return GEMM_ERR_ALIAS;
@@ -111,7 +112,7 @@ int run(int64_t M, int64_t N, int64_t K, char a, char b, char c, int dtype, cons
         q.shrink_rows = s.rows;
         q.q = mg::Lora{(const char*)l.down, (const char*)l.up, l.ids, l.ranks, l.scales, (float*)ws,
                        l.stride_down * es, l.stride_up * es, l.ld_down, l.ld_up,
-                       (int)l.adapters, (int)l.rank, (int)pitch(l.rank), s.splits, s.z};
+                       (int)l.adapters, (int)l.rank, (int)pitch(l.rank), s.splits, s.z, odd_up};
     }
     q.b_kmajor = b == 'k';
     q.vec = vec;

@@ -350,7 +350,7 @@ typedef struct {
  * reads none of ids, ranks and scales: nothing synchronises, and a captured
  * call takes what the arrays hold at each replay.  The workspace, the adapters
  * and the three arrays must not overlap C, nor the workspace any input
- * (GEMM_ERR_ALIAS).  Sizes, alignment (any operand that is not 16-byte
+ * (GEMM_ERR_ALIAS).  Sizes, alignment (A, B or down not 16-byte
  * aligned: the kernels for that run), the checks and their order, asynchrony
  * and errors are otherwise those of gemm_run_ws; results are deterministic.
  */

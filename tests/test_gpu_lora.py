@@ -197,6 +197,15 @@ def test_large_tiles(dtype, K):
         run(300, 701, K + 1, 7, 16, dtype, b_major=b_major, ids="packed")
 
 
+@pytest.mark.parametrize("R", [1, 4, 12, 100])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_unaligned_up_beside_aligned_operands(dtype, R):
+    """Rows of up of few columns, in every kernel of the aligned product."""
+    for M, N in ((1, 72), (24, 72), (40, 136), (140, 136), (300, 520), (1500, 1504), (2100, 2600)):
+        run(M, N, 264, 5, R, dtype, ids="mixed" if M < 1000 else "packed", mixed=R > 4)
+    run(300, 520, 72, 5, R, dtype, b_major="n", kind="int5")
+
+
 @pytest.mark.parametrize("M", [1, 48, 600])
 @pytest.mark.parametrize("dtype", ["bf16_bf16", "f16_f16", "f32"])
 def test_ranks_and_scales_may_be_left_out(dtype, M):
@@ -204,12 +213,13 @@ def test_ranks_and_scales_may_be_left_out(dtype, M):
     run(M, 264, 264, 5, 32, dtype, mixed=True, scales=False)
 
 
+@pytest.mark.parametrize("R", [24, 27])
 @pytest.mark.parametrize("M,N", [(40, 136), (300, 136), (2048, 2304)])
 @pytest.mark.parametrize("dtype", TYPES)
-def test_requests_do_not_see_each_other(dtype, M, N):
+def test_requests_do_not_see_each_other(dtype, M, N, R):
     """Infinities and NaN of one slot, of a row, and past a slot's rank."""
-    x = Case(M, N, 200, 6, 24, dtype, ids="mixed", mixed=False)
-    x.ranks = torch.tensor([24, 10, 24, 0, 24, 3], dtype=torch.int32, device="cuda")
+    x = Case(M, N, 200, 6, R, dtype, ids="mixed", mixed=False)
+    x.ranks = torch.tensor([R, 10, R, 0, R, 3], dtype=torch.int32, device="cuda")
     x.down[2, 3, 5] = float("nan")
     x.up[4, 1] = float("inf")
     x.up[1, :, 10:] = float("nan")

@@ -1082,17 +1082,18 @@ struct LoraInst {
         } else {
             // Measured in bf16, N = K = 4096, us for both kernels (rows: one
             // adapter each up to 64, packed above; rank):
-            //   rows rank  16x16 str. 32x16 str. 32x32   32x32 sh. 64x64 sh. 128x128 sh. 256x256 sh.
-            //      1  16   15.2       17.3       19.4
-            //     16  16   20.2       22.9       25.5
-            //     32  16   30.4       23.8       27.2
-            //     64  16   53.3       38.3       30.5    34.5      65.6
-            //    128  64                         42.9    31.9      37.4      62.6        100
-            //    256  64                         43.3    48.9      33.9      56.1        103
-            //    512  64                                           49.5      55.0        103
-            //   1024  64                                           86.4      59.5        102
-            //   2048  64                                          151       109         107
-            //   8192  64                                          482       367         234
+            //   rows rank  16x16 str. 16x32 str. 32x16 str. 32x32   32x32 sh. 64x64 sh. 128x128 sh. 256x256 sh.
+            //      1  16   15.2                  17.3       19.4
+            //     16  16   20.2                  22.9       25.5
+            //     32  16   30.4       23.4       23.8       27.2
+            //     32 128              42.6       57.2
+            //     64  16   53.3       35.4       38.3       30.5    34.5      65.6
+            //    128  64                                    42.9    31.9      37.4      62.6        100
+            //    256  64                                    43.3    48.9      33.9      56.1        103
+            //    512  64                                                      49.5      55.0        103
+            //   1024  64                                                      86.4      59.5        102
+            //   2048  64                                                     151       109          107
+            //   8192  64                                                     482       367          234
             // (str.: the streaming kernel for few rows, B k-major only; sh.:
             // adapters through LDS for the whole workgroup, of eight waves from
             // 64x64 on: 1024 rows 66.5 on four.)  64x64 tiles that the chip
@@ -1101,7 +1102,7 @@ struct LoraInst {
             auto tiles = [&](int t) { return ((int64_t)c.p.M + t - 1) / t * ((c.p.N + t - 1) / t); };
             if constexpr (BKM) {
                 if (c.p.M <= 16) return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 1, 8, 4, 4>, c, 16, 16, 768, s);
-                if (c.p.M <= 32) return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 2, 1, 8, 3, 4>, c, 32, 16, 768, s);
+                if (c.p.M <= 32) return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 2, 8, 3, 4>, c, 16, 32, 768, s);
             }
             if (c.p.M <= 32) return dma<16, 32, 256, 1, 2, 4, 4, BKM>(c, s);
             if (c.p.M <= 96) return dma<32, 32, 128, 2, 2, 4, 4, BKM>(c, s);

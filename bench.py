@@ -125,7 +125,7 @@ HEADLINE = "fp32_8192"
 # (the probes, the allocation-free entry point's wrapper and the grouped and
 # adapter operators do not change them).
 _NOT_KERNEL_SOURCES = {"gemm_probe.hip", "gemm_noalloc.hip", "gemm_plan.hpp", "gemm_checks.hpp"}
-_NOT_KERNEL_PREFIXES = ("gemm_ragged", "gemm_lora", "gemm_skinny")
+_NOT_KERNEL_PREFIXES = ("gemm_ragged", "gemm_lora")
 
 
 def kernel_source_hash():

@@ -207,6 +207,22 @@ def test_aligned_operands_with_an_unaligned_c(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+def test_largest_tiles_with_an_unaligned_c(dtype):
+    say("unaligned c", dtype)
+    run_rows([700, 0, 1, 900, 511], 5400, 136, dtype, "k", c_pad=1, left=3)
+    for accumulate in (False, True):
+        a, b, ends, c = k_case([300, 0, 65], 2104, 2600, dtype, "n", left=3)
+        c = padded(c, 1, SENTINEL, 1)
+        before, whole = c.clone(), c._base
+        padding = whole.clone()
+        g.grouped_gemm_k(a, b, ends, c, accumulate=accumulate)
+        torch.cuda.synchronize()
+        check_k(a, b, ends, c, before, accumulate, False)
+        c.copy_(before)
+        assert torch.equal(whole, padding), "written outside C"
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_more_groups_than_a_wave(dtype):
     rng = np.random.default_rng(7)
     lens = [int(x) for x in rng.integers(0, 9, size=200)]

@@ -206,6 +206,12 @@ def test_unaligned_up_beside_aligned_operands(dtype, R):
     run(300, 520, 72, 5, R, dtype, b_major="n", kind="int5")
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_unaligned_c_beside_aligned_operands(dtype):
+    for M, N in ((20, 73), (140, 137), (300, 521), (1500, 1501), (2100, 2601)):
+        run(M, N, 264, 5, 16, dtype, ids="packed")
+
+
 @pytest.mark.parametrize("M", [1, 48, 600])
 @pytest.mark.parametrize("dtype", ["bf16_bf16", "f16_f16", "f32"])
 def test_ranks_and_scales_may_be_left_out(dtype, M):

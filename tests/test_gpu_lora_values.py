@@ -1,0 +1,104 @@
+"""Infinities, NaN and the last bits of adapters, in every kernel.
+
+The inputs are integers whose sums every step of the operator holds exactly,
+so what comes out is the definition's value, bit for bit: an infinity where
+the definition has one, of its sign, and NaN only where it has that.
+"""
+import pytest
+import torch
+
+from test_gpu_lora import TYPES, Case, say
+
+pytestmark = pytest.mark.gpu
+
+# Rows, columns and padding (1: operands that are not 16-byte aligned): every
+# kernel of the product.
+STREAM = [(1, 72, 0), (24, 72, 0), (48, 136, 0)] + [(M, N, 1) for M, N in ((1, 72), (300, 520), (515, 2056), (1500, 1504), (4008, 2600))]
+SHARED = [(140, 136, 0), (300, 520, 0), (515, 2056, 0), (1500, 1504, 0), (2312, 2568, 0)]
+KERNELS = STREAM + SHARED
+
+
+def definition(x):
+    """C of integer inputs, infinities and NaN among them, in 64 bits."""
+    ref = x.a.double() @ x.b.double().t()
+    L, R, _ = x.down.shape
+    for i in sorted(set(x.ids.tolist())):
+        if not 0 <= i < L:
+            continue
+        m = (x.ids == i).nonzero().flatten()
+        r = R if x.ranks is None else min(max(int(x.ranks[i]), 0), R)
+        s = 1.0 if x.scales is None else float(x.scales[i])
+        v, u = x.a[m].double() @ x.down[i, :r].double().t(), x.up[i, :, :r].double()
+        total = torch.zeros((len(m), u.shape[0]), dtype=torch.float64, device="cuda")
+        for k in range(r):
+            total += v[:, k:k + 1] * u[:, k]
+        ref[m] += s * total
+    return ref
+
+
+def same(x):
+    want = definition(x).float().to(x.tout)
+    wrong = ~((x.c == want) | (x.c.isnan() & want.isnan()))
+    if wrong.any():
+        m, n = wrong.nonzero()[0].tolist()
+        raise AssertionError((int(wrong.sum()), (m, n), float(x.c[m, n]), float(want[m, n])))
+
+
+def inner(M):
+    return 64 if M > 1000 else 104
+
+
+@pytest.mark.parametrize("M,N,pad", KERNELS)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_one_infinity_of_an_adapter_keeps_its_sign(dtype, M, N, pad):
+    """v_r up[n][r] of a finite v_r and an infinite up is an infinity of the
+    product's sign (NaN for v_r = 0), whatever v_r's bits."""
+    for b_major in "kn":
+        say(dtype, M, N, pad, b_major)
+        x = Case(M, N, inner(M), 3, 24, dtype, ids="distinct" if M < 300 else "packed", b_major=b_major, kind="int5", pad=pad,
+                 mixed=False)
+        if M > 1:
+            x.ids[M // 2] = -1
+        x.up[0, 3, 5] = float("inf")
+        x.up[0, N - 1, 23] = -float("inf")
+        x.up[1, 0, 0] = float("inf")
+        x.up[1, 0, 9] = float("inf")          # two: NaN where their signs differ
+        x.up[1, 40, 11] = float("nan")
+        x.run()
+        torch.cuda.synchronize()
+        same(x)
+
+
+@pytest.mark.parametrize("M,N,pad", STREAM)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_infinite_rows_meet_infinite_adapters(dtype, M, N, pad):
+    """v = +inf in every column and up positive, here and there infinite: +inf."""
+    say(dtype, M, N, pad)
+    x = Case(M, N, inner(M), 2, 24, dtype, ids="one", kind="int5", pad=pad, mixed=False)
+    x.up.copy_(x.up.abs() + 1)
+    x.a[:, 7] = float("inf")
+    x.b[:, 7], x.down[:, :, 7] = 1, 1
+    x.up[1, 3, 5] = x.up[1, 3, 6] = x.up[1, 40, 23] = float("inf")
+    x.run()
+    torch.cuda.synchronize()
+    assert (x.c == float("inf")).all(), (x.c != float("inf")).nonzero()[0].tolist()
+
+
+@pytest.mark.parametrize("M,N,pad", KERNELS)
+@pytest.mark.parametrize("dtype", ["f16_f16", "f16_f32"])
+def test_small_v_meets_an_infinite_adapter(dtype, M, N, pad):
+    """v_1 is below 2^-40 of v_0, which the finite part of fp16's two terms
+    cannot hold beside it, but its product with an infinity is one."""
+    say(dtype, M, N, pad)
+    x = Case(M, N, inner(M), 2, 16, dtype, ids="one", kind="int5", pad=pad, mixed=False, scales=False)
+    x.a.fill_(1)
+    x.down.zero_()
+    x.up.zero_()
+    x.down[1, 0] = 2.0 ** 15
+    x.down[1, 1, 3] = 2.0 ** -24
+    x.up[1, :, 1] = float("inf")
+    x.up[1, 1::2, 1] = -float("inf")
+    x.run()
+    torch.cuda.synchronize()
+    sign = 1 - 2 * (torch.arange(N, device="cuda") % 2)
+    assert (x.c == sign * float("inf")).all(), (x.c != sign * float("inf")).nonzero()[0].tolist()

@@ -233,16 +233,21 @@ lora_shrink_dma_kernel(Params p, Lora q)
     }
 }
 
-// A chunk with zeros in the place of infinities and NaN of a 16-bit type:
-// adding the exponent's lowest bit carries into the sign where it is all ones.
+// Infinities and NaN among two values of a 16-bit type, at their sign bits:
+// adding the exponent's lowest bit carries there where it is all ones.
+template <In TI>
+__device__ __forceinline__ uint32_t not_finite(int word)
+{
+    return (((uint32_t)word & 0x7fff7fffu) + (TI == In::F16 ? 0x04000400u : 0x00800080u)) & 0x80008000u;
+}
+// A chunk with zeros in their place.
 template <In TI>
 __device__ __forceinline__ i32x4 finite_part(i32x4 v)
 {
-    constexpr uint32_t ONE = TI == In::F16 ? 0x04000400u : 0x00800080u;
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-        const uint32_t x = (uint32_t)v[d], over = ((x & 0x7fff7fffu) + ONE) & 0x80008000u;
-        v[d] = (int)(x & ~((over << 1) - (over >> 15)));
+        const uint32_t over = not_finite<TI>(v[d]);
+        v[d] = (int)((uint32_t)v[d] & ~((over << 1) - (over >> 15)));
     }
     return v;
 }
@@ -503,10 +508,11 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
 // once for all waves, and each adapter's rows for the tile's columns come in
 // by direct loads, up to three adapters ahead of the one that is multiplied.  The MFMAs
 // add straight into the accumulators (temporaries beside the 256x256 tile's
-// accumulators spilled); rows of other adapters enter them as zeros.  That
-// keeps rows apart only while the adapter is finite, so infinities and NaN in
-// it are replaced by zeros in LDS and reported: `repair` then adds their terms
-// to the stored C, for the adapter's own rows.  Measured at 4096 rows, N = K =
+// accumulators spilled, as did any other use of them here); rows of other
+// adapters enter them as zeros.  That keeps rows apart only while the adapter
+// is finite, so infinities and NaN in it are replaced by finite values in LDS
+// and reported: `repair` then adds their terms to the stored C, for the
+// adapter's own rows.  Measured at 4096 rows, N = K =
 // 4096, rank 64 in bf16: the product with its adapters 121 us by lora_add,
 // whose every adapter waits for its own loads, 110 here (plain 97).
 template <class KT, In TI>
@@ -670,11 +676,13 @@ struct SharedLora {
         }
     }
 
-    // Zeros from the rank on in the chunk that holds it, and in the place of the
-    // adapter's infinities and NaN (*bad: there were some).
+    // Zeros from the rank on in the chunk that holds it, and values of one to two
+    // with their signs in the place of the adapter's infinities and NaN (*bad:
+    // there were some).  What finite values of v make of them does not count
+    // beside the terms that `repair` adds; an infinite one makes the same
+    // infinity, where zeros would make NaN.
     __device__ static __forceinline__ void clean(char* u, int left, int* bad, int tid)
     {
-        constexpr uint32_t EXP = TI == In::F16 ? 0x7c00u : 0x7f80u;
         for (int x = tid; x < BN * 8; x += NT) {
             const int row = x / 8, c = x % 8;
             if (c * 8 >= left) continue;
@@ -682,13 +690,12 @@ struct SharedLora {
             i32x4 v = *at;
             const bool cut = c * 8 + 8 > left;
             if (cut) v = mask_k<TI>(v, c * 8, left);
-            bool any = false;
+            uint32_t any = 0;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                const uint32_t d = (uint32_t)v[w];
-                const bool lo = (d & EXP) == EXP, hi = (d >> 16 & EXP) == EXP;
-                any = any || lo || hi;
-                v[w] = (int)(d & (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u));
+                const uint32_t over = not_finite<TI>(v[w]);
+                any |= over;
+                v[w] = (int)((uint32_t)v[w] & ~(over >> 1));               // the exponent's highest bit
             }
             if (any || cut) *at = v;
             if (any) *bad = 1;

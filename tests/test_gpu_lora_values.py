@@ -13,9 +13,8 @@ pytestmark = pytest.mark.gpu
 
 # Rows, columns and padding (1: operands that are not 16-byte aligned): every
 # kernel of the product.
-STREAM = [(1, 72, 0), (24, 72, 0), (48, 136, 0)] + [(M, N, 1) for M, N in ((1, 72), (300, 520), (515, 2056), (1500, 1504), (4008, 2600))]
-SHARED = [(140, 136, 0), (300, 520, 0), (515, 2056, 0), (1500, 1504, 0), (2312, 2568, 0)]
-KERNELS = STREAM + SHARED
+KERNELS = [(1, 72, 0), (24, 72, 0), (48, 136, 0)] + [(M, N, 1) for M, N in ((1, 72), (300, 520), (515, 2056), (1500, 1504), (4008, 2600))]
+KERNELS += [(140, 136, 0), (300, 520, 0), (515, 2056, 0), (1500, 1504, 0), (2312, 2568, 0)]
 
 
 def definition(x):
@@ -69,7 +68,7 @@ def test_one_infinity_of_an_adapter_keeps_its_sign(dtype, M, N, pad):
         same(x)
 
 
-@pytest.mark.parametrize("M,N,pad", STREAM)
+@pytest.mark.parametrize("M,N,pad", KERNELS)
 @pytest.mark.parametrize("dtype", TYPES)
 def test_infinite_rows_meet_infinite_adapters(dtype, M, N, pad):
     """v = +inf in every column and up positive, here and there infinite: +inf."""

@@ -704,11 +704,17 @@ struct SharedLora {
 
     // Add the terms of infinite and NaN adapter values to C, which holds the
     // rest.  Rare, and only for the rows of such an adapter: column by column,
-    // straight from memory.
+    // straight from memory.  A rest that C's type holds as an infinity of the
+    // other sign may have been finite before it was rounded: such an element is
+    // summed again from its definition.
+    template <bool BKM>
     __device__ static __forceinline__ void repair(const Params& p, const Lora& q, int m0, int n0, int tid)
     {
         constexpr int EO = KT::OUT == Out::F32 ? 4 : 2;
         constexpr uint32_t EXP = TI == In::F16 ? 0x7c00u : 0x7f80u;
+        const auto value = [](uint16_t h) {
+            return TI == In::F16 ? (float)__builtin_bit_cast(_Float16, h) : __int_as_float((int)((uint32_t)h << 16));
+        };
         __builtin_amdgcn_s_waitcnt(0);                 // the tile is stored
         __syncthreads();
         for (int n = n0 + tid; n < min(n0 + BN, p.N); n += NT) {
@@ -725,15 +731,19 @@ struct SharedLora {
                     for (int r = 0; r < rank; ++r) harm = harm || (u[r] & EXP) == EXP;
                 }
                 if (!harm) continue;
-                float sum = 0.f;
-                for (int r = 0; r < rank; ++r) {
-                    if ((u[r] & EXP) != EXP) continue;
-                    float v = 0.f;
-                    for (int s = 0; s < q.splits; ++s) v += q.v[((int64_t)s * p.M + m) * q.pitch + r];
-                    const float w = TI == In::F16 ? (float)__builtin_bit_cast(_Float16, u[r])
-                                                  : __int_as_float((int)((uint32_t)u[r] << 16));
-                    sum += (q.scales ? q.scales[id] : 1.f) * v * w;
-                }
+                const float scale = q.scales ? q.scales[id] : 1.f;
+                // scale v up_i^T over the terms whose up is not finite, or over all
+                auto terms = [&](bool all) {
+                    float sum = 0.f;
+                    for (int r = 0; r < rank; ++r) {
+                        if (!all && (u[r] & EXP) != EXP) continue;
+                        float v = 0.f;
+                        for (int s = 0; s < q.splits; ++s) v += q.v[((int64_t)s * p.M + m) * q.pitch + r];
+                        sum += scale * v * value(u[r]);
+                    }
+                    return sum;
+                };
+                const float sum = terms(false);
                 // past this CU's cache: other lanes stored this element
                 const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.C + ((int64_t)m * p.ldc + n) * EO, EO);
                 float c;
@@ -743,7 +753,15 @@ struct SharedLora {
                     const uint16_t h = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rc, 0, 0, kDeviceCoherent);
                     c = load_out<KT::OUT>((const char*)&h, 0);
                 }
-                store_out<KT::OUT>(p.C, (int64_t)m * p.ldc + n, c + sum);
+                float y = c + sum;
+                if (EO == 2 && c == -sum) {            // infinities
+                    const uint16_t* const a = (const uint16_t*)p.A + (int64_t)m * p.lda;
+                    y = 0.f;
+                    for (int k = 0; k < p.K; ++k)
+                        y += value(a[k]) * value(((const uint16_t*)p.B)[BKM ? (int64_t)n * p.ldb + k : (int64_t)k * p.ldb + n]);
+                    y += terms(true);
+                }
+                store_out<KT::OUT>(p.C, (int64_t)m * p.ldc + n, y);
             }
         }
     }
@@ -924,7 +942,7 @@ gemm_lora_dma_kernel(Params p, Lora q)
     }
     store_tile<KT, false>(p, smem, m0, n0, acc, tid, lane, wave);
     if constexpr (NB == 0)
-        if (bad) SharedLora<KT, TI>::repair(p, q, m0, n0, tid);
+        if (bad) SharedLora<KT, TI>::template repair<BKM>(p, q, m0, n0, tid);
 }
 
 // ... on the fp32 ring of gemm_f32dma.hpp (VEC = false: 4-byte loads).
@@ -999,7 +1017,7 @@ gemm_lora_pp_kernel(Params p, Lora q)
     PP::mainloop(p, smem, m0, n0, acc, tid, lane, wave);
     const bool bad = SharedLora<KT, TI>::add(p, q, smem, acc, m0, n0, tid, lane, wave);
     store_tile<KT, false>(p, smem, m0, n0, acc, tid, lane, wave);
-    if (bad) SharedLora<KT, TI>::repair(p, q, m0, n0, tid);
+    if (bad) SharedLora<KT, TI>::template repair<BKM>(p, q, m0, n0, tid);
 }
 
 // ------------------------------------------------------------------ launchers

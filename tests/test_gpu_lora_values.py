@@ -101,3 +101,26 @@ def test_small_v_meets_an_infinite_adapter(dtype, M, N, pad):
     torch.cuda.synchronize()
     sign = 1 - 2 * (torch.arange(N, device="cuda") % 2)
     assert (x.c == sign * float("inf")).all(), (x.c != sign * float("inf")).nonzero()[0].tolist()
+
+
+@pytest.mark.parametrize("M,N,pad", KERNELS)
+def test_an_infinity_counts_before_the_rounding(M, N, pad):
+    """The shared product is past fp16's largest value, the adapter's term an
+    infinity of the other sign: the sum is that infinity.  (An infinite shared
+    product makes it NaN.)"""
+    say(M, N, pad)
+    for b_major in "kn":
+        x = Case(M, N, inner(M), 2, 16, "f16_f16", ids="one", b_major=b_major, kind="int5", pad=pad, mixed=False, scales=False)
+        x.a.fill_(50)
+        x.b.fill_(-50)                        # -2500 inner(M) < -65504
+        x.down.fill_(1)
+        x.up.zero_()
+        x.up[1, 40:, 3] = float("inf")
+        x.b[50] = -float("inf")
+        x.run()
+        torch.cuda.synchronize()
+        want = torch.full((N,), -float("inf"), device="cuda")
+        want[40:] = float("inf")
+        want[50] = float("nan")
+        got = x.c.float()
+        assert ((got == want) | (got.isnan() & want.isnan())).all()

@@ -252,17 +252,22 @@ __device__ __forceinline__ i32x4 finite_part(i32x4 v)
     return v;
 }
 
-// 8 (16-bit) or 4 (fp32) values of v as MFMA fragments.  v is fp32 and the
-// adapters are 16-bit, so v is split into the part that the type holds and
-// the type's rounding of the rest, one MFMA each: off by at most 2^-22 of
-// itself in fp16, 2^-16 in bf16.  (One term alone would be off by 2^-8 there,
-// more than the output's own rounding where that is fp32.)  APART: the first
-// term meets infinities of the adapter, so it is zero for v = 0 only; the rest,
-// of either sign, meets finite values only.
-template <In TI>
+// Terms of the input type that a value of v is split into, one MFMA each: the
+// part that the type holds, then its rounding of the rest.  v is fp32: two
+// terms are off by at most 2^-22 of it in fp16 and by 2^-16 in bf16, three in
+// bf16 by 2^-24.  (One alone would be off by 2^-8 there.)  bf16 takes the third
+// where the output is fp32 and would show it; a bf16 output is rounded to 2^-8.
+constexpr int terms_of_v(In ti, Out to)
+{
+    return ti == In::F32 ? 1 : ti == In::BF16 && to == Out::F32 ? 3 : 2;
+}
+
+// 8 (16-bit) or 4 (fp32) values of v as MFMA fragments.  APART: the first term
+// meets infinities of the adapter, so it is zero for v = 0 only; the others, of
+// either sign, meet finite values only.
+template <In TI, int TERMS>
 struct VFrag {
-    static constexpr int N = TI == In::F32 ? 1 : 2;
-    i32x4 f[N];
+    i32x4 f[TERMS];
 
     template <bool APART = false>
     __device__ __forceinline__ void set(const float (&v)[TI == In::F32 ? 4 : 8])
@@ -273,28 +278,30 @@ struct VFrag {
         } else {
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
-                uint32_t hi = 0, lo = 0;
+                uint32_t w[TERMS] = {};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float x = v[2 * d + h];
+                    float x = v[2 * d + h];
                     const bool inf = __builtin_fabsf(x) == __builtin_inff();   // then the rest is inf - inf
-                    uint32_t a, b;
-                    if constexpr (TI == In::BF16) {
-                        // (Not past bf16's largest: that would be an infinity.)
-                        const float most = 0x1.fep127f;
-                        a = __builtin_bit_cast(uint16_t, (__bf16)(inf ? x : fminf(fmaxf(x, -most), most)));
-                        const float rest = x - __int_as_float((int)(a << 16));
-                        b = __builtin_bit_cast(uint16_t, (__bf16)(inf ? 0.f : rest));
-                    } else {
-                        a = __builtin_bit_cast(uint16_t, (_Float16)x);
-                        if (APART && x != 0.f && (a & 0x7fff) == 0) a |= 1;   // (the rest takes it back)
-                        b = __builtin_bit_cast(uint16_t, (_Float16)(inf ? 0.f : x - (float)__builtin_bit_cast(_Float16, (uint16_t)a)));
+#pragma unroll
+                    for (int t = 0; t < TERMS; ++t) {
+                        uint32_t a;
+                        if constexpr (TI == In::BF16) {
+                            // (Not past bf16's largest: that would be an infinity.)
+                            const float most = 0x1.fep127f;
+                            a = __builtin_bit_cast(uint16_t, (__bf16)(t > 0 || inf ? x : fminf(fmaxf(x, -most), most)));
+                            x -= __int_as_float((int)(a << 16));
+                        } else {
+                            a = __builtin_bit_cast(uint16_t, (_Float16)x);
+                            if (APART && t == 0 && x != 0.f && (a & 0x7fff) == 0) a |= 1;   // (the rest takes it back)
+                            x -= (float)__builtin_bit_cast(_Float16, (uint16_t)a);
+                        }
+                        if (inf) x = 0.f;
+                        w[t] |= a << (16 * h);
                     }
-                    hi |= a << (16 * h);
-                    lo |= b << (16 * h);
                 }
-                f[0][d] = (int)hi;
-                f[1][d] = (int)lo;
+#pragma unroll
+                for (int t = 0; t < TERMS; ++t) f[t][d] = (int)w[t];
             }
         }
     }
@@ -305,7 +312,7 @@ struct VFrag {
 // holds rows i * MI and columns j * MI on.  NB: adapters whose loads are
 // in flight together.  Of the rows' distinct adapters, those with an index of
 // `share` modulo `shares` are added (all: 0 of 1).
-template <In TI, bool VEC, int NB, int MI, int TM, int TN, class AccT, class Col>
+template <In TI, bool VEC, int TERMS, int NB, int MI, int TM, int TN, class AccT, class Col>
 __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&acc)[TM][TN], int m0, int n0, int lane,
                                          float* tab, int share, int shares, Col col)
 {
@@ -370,7 +377,7 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
     auto pass = [&](auto apart, uint64_t which) {
         constexpr bool APART = decltype(apart)::value;
         for (int r0 = 0; r0 < q.pitch; r0 += CH) {
-            VFrag<TI> fv[TM][NK];
+            VFrag<TI, TERMS> fv[TM][NK];
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -428,7 +435,7 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
                             for (int k = 0; k < NK; ++k) {
                                 if (r0 + k * KS >= a[b].rank) continue;
 #pragma unroll
-                                for (int h = 0; h < VFrag<TI>::N; ++h)
+                                for (int h = 0; h < TERMS; ++h)
                                     mfma_step<TI, MI>(fv[i][k].f[h], APART && h > 0 ? finite_part<TI>(fu[b][k]) : fu[b][k], t);
                             }
 #pragma unroll
@@ -494,13 +501,13 @@ __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&
 }
 
 // ... with the columns of MFMA tile j next to each other from j * MI on.
-template <In TI, bool VEC, int NB, int MI, int TM, int TN, class AccT>
+template <In TI, bool VEC, int TERMS, int NB, int MI, int TM, int TN, class AccT>
 __device__ __forceinline__ void lora_add(const Params& p, const Lora& q, AccT (&acc)[TM][TN], int m0, int n0, int lane,
                                          float* tab, int share = 0, int shares = 1)
 {
     const auto col = [&](int j) { return j * MI + lane % MI; };
-    if (VEC && q.odd_up) lora_add<TI, false, NB < 4 ? NB : 4, MI>(p, q, acc, m0, n0, lane, tab, share, shares, col);
-    else lora_add<TI, VEC, NB, MI>(p, q, acc, m0, n0, lane, tab, share, shares, col);
+    if (VEC && q.odd_up) lora_add<TI, false, TERMS, NB < 4 ? NB : 4, MI>(p, q, acc, m0, n0, lane, tab, share, shares, col);
+    else lora_add<TI, VEC, TERMS, NB, MI>(p, q, acc, m0, n0, lane, tab, share, shares, col);
 }
 
 // The same for a whole workgroup on 16-bit inputs, through LDS (the ring, free
@@ -519,13 +526,18 @@ template <class KT, In TI>
 struct SharedLora {
     static constexpr int BM = KT::TILE_M, BN = KT::TILE_N, NW = KT::NW, NT = KT::NT, MI = 16;
     static constexpr int TM = KT::TM, TN = KT::TN, WTM = KT::WTM, WTN = KT::WTN, WN = BN / WTN;
-    static constexpr int CH = 64, NG = 2;              // columns of v at a time, in MFMA steps
+    static constexpr int TERMS = terms_of_v(TI, KT::OUT);
+    // Columns of v at a time, in MFMA steps.  64, or 32 where three terms of them
+    // leave no room for two adapters (256x256 tiles; 4096 rows, N = K = 4096,
+    // bf16 into fp32, us: rank 64 124.0, 119.7 with 64 columns of two terms;
+    // rank 16 114.0, 115.5).
+    static constexpr int SMALL = BM * 16 + 16;         // tables
+    static constexpr int CH = KT::SMEM - SMALL >= (TERMS * BM + 2 * BN) * 64 * 2 ? 64 : 32, NG = CH / 32, CPR = CH / 8;
     using OV = DmaOperand<BM, CH, NW, true, MI>;       // for its fragments
     using OU = DmaOperand<BN, CH, NW, true, MI>;
     static constexpr int V_BYTES = BM * CH * 2, U_BYTES = OU::BYTES;
-    static constexpr int SMALL = BM * 16 + 16;         // tables
-    static constexpr int FIT = (KT::SMEM - 2 * V_BYTES - SMALL) / U_BYTES, NU = FIT < 4 ? FIT : 4;   // adapters in LDS
-    static constexpr int TAB = 2 * V_BYTES + NU * U_BYTES, ROWS = TAB + BM * 8, BAD = ROWS + BM * 8;
+    static constexpr int FIT = (KT::SMEM - TERMS * V_BYTES - SMALL) / U_BYTES, NU = FIT < 4 ? FIT : 4;   // adapters in LDS
+    static constexpr int TAB = TERMS * V_BYTES + NU * U_BYTES, ROWS = TAB + BM * 8, BAD = ROWS + BM * 8;
     static_assert(NU >= 2 && (NU - 2) * OU::IPW < 64, "fits the ring; vmcnt range");
     static_assert(64 % WTM == 0, "a wave's rows in one mask");
 
@@ -535,9 +547,8 @@ struct SharedLora {
     {
         if (q.slots == 0 || q.R == 0) return false;
         const int wm = wave / WN, wn = wave % WN;
-        char* const vh = smem;
-        char* const vl = smem + V_BYTES;
-        char* const ub = smem + 2 * V_BYTES;           // NU buffers
+        char* const vt = smem;                         // the terms of v
+        char* const ub = smem + TERMS * V_BYTES;       // NU buffers
         float* const tab = (float*)(smem + TAB);       // fp16: 2^e of each row, then 2^-e
         int* const row_id = (int*)(smem + ROWS);       // -1: none
         float* const row_scale = (float*)(row_id + BM);
@@ -627,7 +638,7 @@ struct SharedLora {
                 if (a[0] < 0) return false;
                 issue(a[i], min(rk[i] - r0, CH), r0, ub + i * U_BYTES);
             }
-            stage_v(p, q, vh, vl, tab, row_id, row_scale, m0, r0, tid);
+            stage_v(p, q, vt, tab, row_id, row_scale, m0, r0, tid);
             for (int buf = 0; a[0] >= 0; buf = buf + 1 == NU ? 0 : buf + 1) {
                 const int left = min(rk[0] - r0, CH);
                 const uint64_t own = rows[0];
@@ -649,7 +660,7 @@ struct SharedLora {
                     clean(u, left, bad, tid);
                     __builtin_amdgcn_s_waitcnt(0xc07f);
                     bare_barrier();                    // (no fence: the next adapters are on their way)
-                    if (own) multiply(acc, vh, vl, u, own, left, wm, wn, lane);
+                    if (own) multiply(acc, vt, u, own, left, wm, wn, lane);
                 }
             }
             wait_vmcnt<0>();                           // the empty loads have landed
@@ -683,10 +694,10 @@ struct SharedLora {
     // infinity, where zeros would make NaN.
     __device__ static __forceinline__ void clean(char* u, int left, int* bad, int tid)
     {
-        for (int x = tid; x < BN * 8; x += NT) {
-            const int row = x / 8, c = x % 8;
+        for (int x = tid; x < BN * CPR; x += NT) {
+            const int row = x / CPR, c = x % CPR;
             if (c * 8 >= left) continue;
-            i32x4* const at = (i32x4*)(u + row * 128 + swz_chunk<8, true>(row, c) * 16);
+            i32x4* const at = (i32x4*)(u + row * (CH * 2) + swz_chunk<CPR, true>(row, c) * 16);
             i32x4 v = *at;
             const bool cut = c * 8 + 8 > left;
             if (cut) v = mask_k<TI>(v, c * 8, left);
@@ -766,17 +777,17 @@ struct SharedLora {
         }
     }
 
-    // scale * v of the tile's rows, columns r0 .. r0 + 63, as two terms of the
-    // input type in LDS.  fp16 rows are brought to a largest value of 2^13 ..
+    // scale * v of the tile's rows, CH columns from r0 on, as terms of the input
+    // type in LDS.  fp16 rows are brought to a largest value of 2^13 ..
     // 2^14 by a power of two (at most 2^64), so that neither term leaves
     // fp16's range; tab: that power and its inverse.
-    __device__ static __forceinline__ void stage_v(const Params& p, const Lora& q, char* vh, char* vl, float* tab,
+    __device__ static __forceinline__ void stage_v(const Params& p, const Lora& q, char* vt, float* tab,
                                                    const int* row_id, const float* row_scale, int m0, int r0, int tid)
     {
-        constexpr int STEP = NT / 16, IT = BM / STEP;                     // 16 threads per row
-        constexpr int MOST = TI == In::F16 && TM * TN >= 32 ? 2 : 4, BATCH = IT < MOST ? IT : MOST;
+        constexpr int TPR = CH / 4, STEP = NT / TPR, IT = BM / STEP;      // threads per row, rows at a time
+        constexpr int MOST = (TI == In::F16 || TERMS > 2) && TM * TN >= 32 ? 2 : 4, BATCH = IT < MOST ? IT : MOST;
         static_assert(IT % BATCH == 0, "whole batches");
-        const int c4 = tid % 16 * 4;                   // this thread's 4 columns
+        const int c4 = tid % TPR * 4;                  // this thread's 4 columns
         const int64_t split = (int64_t)p.M * q.pitch;
         // The rows of a batch: all their loads before the first is waited for.
         auto load = [&](int mb, int r, f32x4 (&v)[BATCH]) {
@@ -809,7 +820,7 @@ struct SharedLora {
             for (int x = 0; x < BATCH; ++x) v[x] *= row_scale[mb + x * STEP];
         };
 #pragma unroll 1
-        for (int mb = tid / 16; mb < BM; mb += BATCH * STEP) {
+        for (int mb = tid / TPR; mb < BM; mb += BATCH * STEP) {
             f32x4 v[BATCH];
             load(mb, r0 + c4, v);
             if constexpr (TI == In::F16) {
@@ -837,7 +848,7 @@ struct SharedLora {
 #pragma unroll
                 for (int y = 0; y < BATCH; ++y) {
 #pragma unroll
-                    for (int o = 1; o < 16; o *= 2) top[y] = fmaxf(top[y], __shfl_xor(top[y], o));
+                    for (int o = 1; o < TPR; o *= 2) top[y] = fmaxf(top[y], __shfl_xor(top[y], o));
                     int e;
                     __builtin_frexpf(top[y], &e);
                     e = top[y] > 0.f ? min(14 - e, 64) : 0;
@@ -851,41 +862,42 @@ struct SharedLora {
 #pragma unroll
             for (int y = 0; y < BATCH; ++y) {
                 const int m = mb + y * STEP;
-                VFrag<TI> f;
+                VFrag<TI, TERMS> f;
                 const float x[8] = {v[y][0], v[y][1], v[y][2], v[y][3], 0.f, 0.f, 0.f, 0.f};
                 f.set(x);
-                const int off = m * 128 + swz_chunk<8, true>(m, c4 / 8) * 16 + c4 % 8 * 2;
+                const int off = m * (CH * 2) + swz_chunk<CPR, true>(m, c4 / 8) * 16 + c4 % 8 * 2;
                 typedef int i32x2 __attribute__((ext_vector_type(2)));
-                *(i32x2*)(vh + off) = i32x2{f.f[0][0], f.f[0][1]};
-                *(i32x2*)(vl + off) = i32x2{f.f[1][0], f.f[1][1]};
+#pragma unroll
+                for (int t = 0; t < TERMS; ++t) *(i32x2*)(vt + t * V_BYTES + off) = i32x2{f.f[t][0], f.f[t][1]};
             }
         }
     }
 
-    __device__ static __forceinline__ void multiply(typename KT::Acc& acc, const char* vh, const char* vl, const char* u,
+    __device__ static __forceinline__ void multiply(typename KT::Acc& acc, const char* vt, const char* u,
                                                     uint64_t rows, int left, int wm, int wn, int lane)
     {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             if (g * 32 >= left) break;
-            i32x4 fh[TM], fl[TM];
+            i32x4 fv[TERMS][TM];
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
                 const bool own = rows >> (i * MI + lane % MI) & 1;
                 const i32x4 zero = {0, 0, 0, 0};
-                fh[i] = OV::template frag<MI>(vh, wm * WTM + i * MI, g * 32, lane);
-                fl[i] = OV::template frag<MI>(vl, wm * WTM + i * MI, g * 32, lane);
-                fh[i] = own ? fh[i] : zero;
-                fl[i] = own ? fl[i] : zero;
+#pragma unroll
+                for (int t = 0; t < TERMS; ++t) {
+                    fv[t][i] = OV::template frag<MI>(vt + t * V_BYTES, wm * WTM + i * MI, g * 32, lane);
+                    fv[t][i] = own ? fv[t][i] : zero;
+                }
             }
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 __builtin_amdgcn_sched_barrier(0);
                 const i32x4 f = OU::template frag<MI>(u, wn * WTN + j * MI, g * 32, lane);
 #pragma unroll
-                for (int i = 0; i < TM; ++i) mfma_step<TI, MI>(fh[i], f, acc[i][j]);
+                for (int t = 0; t < TERMS; ++t)
 #pragma unroll
-                for (int i = 0; i < TM; ++i) mfma_step<TI, MI>(fl[i], f, acc[i][j]);
+                    for (int i = 0; i < TM; ++i) mfma_step<TI, MI>(fv[t][i], f, acc[i][j]);
             }
         }
     }
@@ -907,8 +919,8 @@ gemm_lora_odd_kernel(Params p, Lora q)
     KT::zero(acc);
     T::mainloop(p, smem, m0, n0, acc, lane, wave);
     bare_barrier();       // no wave reads the tiles any more
-    lora_add<TI, false, 1, 16, KT::TM, KT::TN>(p, q, acc, m0 + wave / WN * KT::WTM, n0 + wave % WN * KT::WTN, lane,
-                                               (float*)smem + 128 * wave);
+    lora_add<TI, false, terms_of_v(TI, TO), 1, 16, KT::TM, KT::TN>(p, q, acc, m0 + wave / WN * KT::WTM, n0 + wave % WN * KT::WTN,
+                                                                   lane, (float*)smem + 128 * wave);
     store_tile<KT, false>(p, smem, m0, n0, acc, tid, lane, wave);
 }
 
@@ -935,8 +947,8 @@ gemm_lora_dma_kernel(Params p, Lora q)
     bool bad = false;
     if constexpr (NB > 0) {
         bare_barrier();   // no wave reads the ring any more
-        lora_add<TI, true, NB, MI, KT::TM, KT::TN>(p, q, acc, m0 + wave / WN * KT::WTM, n0 + wave % WN * KT::WTN, lane,
-                                                   (float*)smem + 128 * wave);
+        lora_add<TI, true, terms_of_v(TI, TO), NB, MI, KT::TM, KT::TN>(p, q, acc, m0 + wave / WN * KT::WTM,
+                                                                       n0 + wave % WN * KT::WTN, lane, (float*)smem + 128 * wave);
     } else {
         bad = SharedLora<KT, TI>::add(p, q, smem, acc, m0, n0, tid, lane, wave);
     }
@@ -966,8 +978,8 @@ gemm_lora_f32_kernel(Params p, Lora q)
     KT::mainloop(p, smem, oa, ob, m0, n0, 0, (p.K + BK - 1) / BK, acc, tid, lane, wave);
     const auto col = [&](int j) { return KT::UB::row(j, lane % 32); };
     const int rm0 = m0 + wave / WN * KT::WTM, cn0 = n0 + wave % WN * KT::WTN;
-    if (VEC && q.odd_up) lora_add<In::F32, false, 2, 32>(p, q, acc, rm0, cn0, lane, nullptr, 0, 1, col);
-    else lora_add<In::F32, VEC, 2, 32>(p, q, acc, rm0, cn0, lane, nullptr, 0, 1, col);
+    if (VEC && q.odd_up) lora_add<In::F32, false, 1, 2, 32>(p, q, acc, rm0, cn0, lane, nullptr, 0, 1, col);
+    else lora_add<In::F32, VEC, 1, 2, 32>(p, q, acc, rm0, cn0, lane, nullptr, 0, 1, col);
     KT::template store<false, false>(p, m0, n0, acc, lane, wave, smem);
 }
 
@@ -993,7 +1005,8 @@ gemm_lora_skinny_kernel(Params p, Lora q)
     typename T::Acc acc;
     T::zero(acc);
     if (wave >= NW)
-        lora_add<TI, VEC, NB, 16, MT, NT>(p, q, acc, m0, n0, lane, (float*)(smem + T::RING) + 128 * (wave - NW), wave - NW, NL);
+        lora_add<TI, VEC, terms_of_v(TI, TO), NB, 16, MT, NT>(p, q, acc, m0, n0, lane, (float*)(smem + T::RING) + 128 * (wave - NW),
+                                                              wave - NW, NL);
     else
         T::stream(p, smem, m0, n0, acc, lane, wave);
     T::template join<TO, NW + NL>(p, smem, m0, n0, acc, tid, lane, wave);

@@ -124,3 +124,22 @@ def test_an_infinity_counts_before_the_rounding(M, N, pad):
         want[50] = float("nan")
         got = x.c.float()
         assert ((got == want) | (got.isnan() & want.isnan())).all()
+
+
+@pytest.mark.parametrize("M,N,pad", KERNELS)
+def test_fp32_outputs_hold_all_bits_of_v(M, N, pad):
+    """bf16 inputs and an fp32 output: v reaches 2^22 as a sum of products of
+    8-bit integers, exact in fp32, and up picks its columns one by one."""
+    say(M, N, pad)
+    for R in (40, 100):
+        x = Case(M, N, 64, 3, R, "bf16_f32", ids="distinct" if M < 300 else "packed", kind="int5", pad=pad, mixed=False,
+                 scales=False)
+        gen = torch.Generator().manual_seed(M + R)
+        for t in (x.a, x.down):
+            t.copy_(torch.randint(-255, 256, t.shape, generator=gen).to(t.dtype))
+        x.b.zero_()
+        x.up.copy_((torch.arange(N)[:, None] % R == torch.arange(R)).to(x.up.dtype))
+        x.run()
+        torch.cuda.synchronize()
+        same(x)
+        assert x.c.abs().max() > 2 ** 17 and (M == 1 or (x.c.abs() % 2 == 1).any())

@@ -257,6 +257,9 @@ __device__ __forceinline__ i32x4 finite_part(i32x4 v)
 // terms are off by at most 2^-22 of it in fp16 and by 2^-16 in bf16, three in
 // bf16 by 2^-24.  (One alone would be off by 2^-8 there.)  bf16 takes the third
 // where the output is fp32 and would show it; a bf16 output is rounded to 2^-8.
+// fp16's smallest step is 2^-24, so whoever splits v scales its rows first: to
+// a largest value of 2^13 or more, which leaves half a step, 2^-38 of that
+// largest, for the values far below it.
 constexpr int terms_of_v(In ti, Out to)
 {
     return ti == In::F32 ? 1 : ti == In::BF16 && to == Out::F32 ? 3 : 2;

@@ -339,9 +339,13 @@ typedef struct {
 /*
  * The product above, rounded once.  a_major 'k', c_major 'n' (else
  * GEMM_ERR_BAD_MAJOR), b_major 'k' or 'n'.  v and all sums are fp32; v enters
- * the second product as two terms of the input type (off by at most 2^-22 of
- * itself for fp16, 2^-16 for bf16), or three for bf16 with an fp32 output
- * (2^-24).  Infinities and NaN in one slot reach only the rows that use it.
+ * the second product unsplit for fp32, as two terms of the input type for fp16
+ * and bf16 (v[m][r] off by at most 2^-22 of itself and 2^-16), or three for
+ * bf16 with an fp32 output (2^-24).  fp16 first scales a row of v by one power
+ * of two, so there it is off by 2^-38 of the row's largest |v| where that is
+ * more (by 2^-89 where even that is smaller).  Products of many rows split
+ * scales[i] * v instead of v: it must be in fp32's range.
+ * Infinities and NaN in one slot reach only the rows that use it.
  * lora NULL, adapters 0, rank 0 or K 0 is the plain product.
  *
  * workspace: at least gemm_lora_workspace_size() bytes of device memory,

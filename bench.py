@@ -124,7 +124,7 @@ HEADLINE = "fp32_8192"
 # Sources the dense GEMM kernels and their launch parameters are built from
 # (the probes, the allocation-free entry point's wrapper and the grouped and
 # adapter operators do not change them).
-_NOT_KERNEL_SOURCES = {"gemm_probe.hip", "gemm_noalloc.hip", "gemm_plan.hpp", "gemm_checks.hpp"}
+_NOT_KERNEL_SOURCES = {"gemm_probe.hip", "gemm_noalloc.hip", "gemm_plan.hpp", "gemm_checks.hpp", "gemm_tiles.hpp"}
 _NOT_KERNEL_PREFIXES = ("gemm_ragged", "gemm_lora")
 
 

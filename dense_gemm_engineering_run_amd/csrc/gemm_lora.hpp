@@ -39,8 +39,9 @@ struct Lora {
 
 // R rounded up to whole MFMA steps of any input type.
 constexpr int kRankStep = 32;
-// Rows of v one workgroup computes.
+// Rows of v one workgroup computes, and its threads (64 rows where tiled).
 constexpr int kShrinkRows = 16;
+constexpr int kShrinkThreads = 256;
 
 // The distinct adapters of up to 64 rows, one lane each.  A lane fetches its
 // own row's rank and scale, so that the walk over the adapters waits for no
@@ -1085,29 +1086,18 @@ inline ShrinkPlan shrink_plan(int64_t M, int64_t K, bool tiled, int pitch = 32)
 // both kernels together, and 1261 against 1333 at 4096 rows of rank 128.)
 inline bool shrink_tiled(int in_bytes, bool vec) { return in_bytes == 2 && vec; }
 
+inline LoraShape shape_of(const LoraCall& c, bool f32) { return {f32, c.vec, c.b_kmajor, c.p.M, c.p.N}; }
+
 template <class Kernel>
-hipError_t launch_lora(Kernel kernel, const LoraCall& c, int BM, int BN, int threads, hipStream_t s)
+hipError_t launch_lora(Kernel kernel, const LoraCall& c, const Tile& t, hipStream_t s)
 {
     Params p = c.p;
     Lora q = c.q;
-    p.tiles_m = (p.M + BM - 1) / BM;
-    p.tiles_n = (p.N + BN - 1) / BN;
+    p.tiles_m = (int)ceil_div(p.M, t.bm);
+    p.tiles_n = (int)ceil_div(p.N, t.bn);
     p.group_m = p.tiles_m < 8 ? p.tiles_m : 8;
     void* args[] = {&p, &q};
-    return hipLaunchKernel((const void*)kernel, dim3((unsigned)((int64_t)p.tiles_m * p.tiles_n)), dim3(threads), args, 0, s);
-}
-
-// The few-row kernel's grid: column tiles in chunks of 8, one per XCD.
-template <class Kernel>
-hipError_t launch_skinny(Kernel kernel, const LoraCall& c, int BM, int BN, int threads, hipStream_t s)
-{
-    Params p = c.p;
-    Lora q = c.q;
-    p.tiles_m = (p.M + BM - 1) / BM;
-    p.tiles_n = (p.N + BN - 1) / BN;
-    void* args[] = {&p, &q};
-    const int64_t grid = (int64_t)(p.tiles_n + 7) / 8 * 8 * p.tiles_m;
-    return hipLaunchKernel((const void*)kernel, dim3((unsigned)grid), dim3(threads), args, 0, s);
+    return hipLaunchKernel((const void*)kernel, dim3((unsigned)lora_grid(shape_of(c, false), t)), dim3(t.threads), args, 0, s);
 }
 
 template <In TI>
@@ -1119,101 +1109,73 @@ hipError_t launch_shrink(const LoraCall& c, hipStream_t s)
     const int rows = c.shrink_rows;
     const dim3 grid((unsigned)((p.M + rows - 1) / rows), (unsigned)q.splits, (unsigned)q.z);
     if constexpr (TI != In::F32)
-        if (rows == 64) return hipLaunchKernel((const void*)&lora_shrink_dma_kernel<TI>, grid, dim3(256), args, 0, s);
+        if (rows == 64) return hipLaunchKernel((const void*)&lora_shrink_dma_kernel<TI>, grid, dim3(kShrinkThreads), args, 0, s);
     const void* kernel = c.vec ? (const void*)&lora_shrink_kernel<TI, true> : (const void*)&lora_shrink_kernel<TI, false>;
-    return hipLaunchKernel(kernel, grid, dim3(256), args, 0, s);
+    return hipLaunchKernel(kernel, grid, dim3(kShrinkThreads), args, 0, s);
 }
 
 template <In TI, Out TO>
 struct LoraInst {
-    template <int BM, int BN, int BK, int WM, int WN, int ST, int NB, bool BKM>
+    template <LoraTile T, bool BKM, bool VEC>
+    static hipError_t stream(const LoraCall& c, hipStream_t s)
+    {
+        constexpr Tile t = tile_of(T);
+        return launch_lora(&gemm_lora_skinny_kernel<TI, TO, t.wm, t.wn, t.extra, t.stages, t.threads / 64 - t.extra, BKM, VEC>, c, t, s);
+    }
+    template <LoraTile T, bool BKM>
     static hipError_t dma(const LoraCall& c, hipStream_t s)
     {
-        return launch_lora(&gemm_lora_dma_kernel<TI, TO, BM, BN, BK, WM, WN, ST, NB, BKM>, c, BM, BN, WM * WN * 64, s);
+        constexpr Tile t = tile_of(T);
+        return launch_lora(&gemm_lora_dma_kernel<TI, TO, t.bm, t.bn, t.bk, t.wm, t.wn, t.stages, t.extra, BKM>, c, t, s);
     }
-    template <int BM, int BN, int BK, int WM, int WN, int DEPTH, bool BKM>
+    template <LoraTile T, bool BKM>
     static hipError_t odd(const LoraCall& c, hipStream_t s)
     {
-        return launch_lora(&gemm_lora_odd_kernel<TI, TO, BM, BN, BK, WM, WN, DEPTH, BKM>, c, BM, BN, WM * WN * 64, s);
+        constexpr Tile t = tile_of(T);
+        return launch_lora(&gemm_lora_odd_kernel<TI, TO, t.bm, t.bn, t.bk, t.wm, t.wn, t.stages, BKM>, c, t, s);
     }
-    template <int BM, int BN, int ST, bool BKM, bool VEC>
+    template <LoraTile T, bool BKM, bool VEC>
     static hipError_t f32(const LoraCall& c, hipStream_t s)
     {
-        return launch_lora(&gemm_lora_f32_kernel<BM, BN, ST, BKM, VEC>, c, BM, BN, 256, s);
+        constexpr Tile t = tile_of(T);
+        return launch_lora(&gemm_lora_f32_kernel<t.bm, t.bn, t.stages, BKM, VEC>, c, t, s);
     }
     template <bool BKM, bool VEC>
     static hipError_t product(const LoraCall& c, hipStream_t s)
     {
+        const LoraTile t = lora_tile(shape_of(c, TI == In::F32));
+        if constexpr (TI == In::F32 || (BKM && VEC)) {
+            if (t == LoraTile::Stream16x16) return stream<LoraTile::Stream16x16, BKM, VEC>(c, s);
+            if (t == LoraTile::Stream16x32) return stream<LoraTile::Stream16x32, BKM, VEC>(c, s);
+        }
         if constexpr (TI == In::F32) {
-            // Measured, N = K = 4096, us for both kernels (rows: one adapter
-            // each of 16 up to 64, packed above; B n-major in brackets):
-            //   rows rank  16x16 str.    16x32 str.    32x32 str.    64x64        64x128
-            //      1  16    24.2 [31.3]   26.2 [28.5]   31.6 [31.6]    94 [ 95]
-            //     16 128    47.1 [61.1]   54.3 [68.3]   65.6 [78.9]   146 [182]
-            //     32  16    40.2 [55.4]   31.9 [37.0]   39.6 [44.8]   107 [113]
-            //     64  16    65.1 [86.8]   48.8 [58.8]   40.6 [43.5]   108 [113]
-            //    128  16    96.2 [141]    69.4 [94.0]   56.6 [70.3]    96 [110]
-            //    256 128                               158  [224]     130 [146]     238 [238]
-            //   1024  16                               419  [429]     298 [303]     283 [284]
-            //   4096  16                              1344           1110          1065
-            auto tiles = [&](int bm, int bn) { return ((int64_t)c.p.M + bm - 1) / bm * ((c.p.N + bn - 1) / bn); };
-            if (c.p.M <= 16) return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 1, 8, 4, 4, BKM, VEC>, c, 16, 16, 768, s);
-            if (c.p.M <= 32) return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 2, 8, 3, 4, BKM, VEC>, c, 16, 32, 768, s);
-            if (tiles(64, 64) <= 192) return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 2, 2, 8, 2, 4, BKM, VEC>, c, 32, 32, 768, s);
+            if (t == LoraTile::Stream32x32) return stream<LoraTile::Stream32x32, BKM, VEC>(c, s);
             if constexpr (VEC) {
-                if (tiles(64, 128) >= 512) return f32<64, 128, 2, BKM, true>(c, s);
-                return f32<64, 64, 3, BKM, true>(c, s);
+                if (t == LoraTile::F32Rows64x128) return f32<LoraTile::F32Rows64x128, BKM, true>(c, s);
+                return f32<LoraTile::F32Rows64x64, BKM, true>(c, s);
             } else {
-                return f32<64, 64, 2, BKM, false>(c, s);
+                return f32<LoraTile::F32Odd64x64, BKM, false>(c, s);
             }
         } else if constexpr (!VEC) {
-            // Measured in bf16, N = 4096, K = 4095, us for both kernels (rows:
-            // one adapter each of 16 up to 64, packed above):
-            //   rows rank  32x32   64x64   128x128  256x128
-            //      1  16    29.4    41.5     71.4    104
-            //     64  16    38.3    58.2    105      154
-            //    128  64    45.2    54.4    100      127
-            //    256  64    77.7    55.6     98.0    143
-            //   1024  64   297     182      115      171
-            //   4096  64   971     517      383      315
-            // (Loads element by element: 123 at one row, 1853 at 4096.)
-            auto tiles = [&](int bm, int bn) { return ((int64_t)c.p.M + bm - 1) / bm * ((c.p.N + bn - 1) / bn); };
-            if (c.p.M <= 144) return odd<32, 32, 256, 2, 2, 2, BKM>(c, s);
-            if (tiles(64, 64) <= 512) return odd<64, 64, 128, 2, 4, 2, BKM>(c, s);
-            if (tiles(256, 128) >= 256) return odd<256, 128, 64, 4, 2, 2, BKM>(c, s);
-            return odd<128, 128, 64, 4, 2, 2, BKM>(c, s);
-        } else {
-            // Measured in bf16, N = K = 4096, us for both kernels (rows: one
-            // adapter each up to 64, packed above; rank):
-            //   rows rank  16x16 str. 16x32 str. 32x16 str. 32x32   32x32 sh. 64x64 sh. 128x128 sh. 256x256 sh.
-            //      1  16   15.2                  17.3       19.4
-            //     16  16   20.2                  22.9       25.5
-            //     32  16   30.4       23.4       23.8       27.2
-            //     32 128              42.6       57.2
-            //     64  16   53.3       35.4       38.3       30.5    34.5      65.6
-            //    128  64                                    42.9    31.9      37.4      62.6        100
-            //    256  64                                    43.3    48.9      33.9      56.1        103
-            //    512  64                                                      49.5      55.0        103
-            //   1024  64                                                      86.4      59.5        102
-            //   2048  64                                                     151       109          107
-            //   8192  64                                                     482       367          234
-            // (str.: the streaming kernel for few rows, B k-major only; sh.:
-            // adapters through LDS for the whole workgroup, of eight waves from
-            // 64x64 on: 1024 rows 66.5 on four.)  64x64 tiles that the chip
-            // holds at once take 128 of k at a time in three stages (33.9 us at
-            // 256 rows, 36.6 with 64 in four; at 512 rows 56.9 and 49.5).
-            auto tiles = [&](int t) { return ((int64_t)c.p.M + t - 1) / t * ((c.p.N + t - 1) / t); };
-            if constexpr (BKM) {
-                if (c.p.M <= 16) return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 1, 8, 4, 4>, c, 16, 16, 768, s);
-                if (c.p.M <= 32) return launch_skinny(&gemm_lora_skinny_kernel<TI, TO, 1, 2, 8, 3, 4>, c, 16, 32, 768, s);
+            switch (t) {
+            case LoraTile::Odd32x32: return odd<LoraTile::Odd32x32, BKM>(c, s);
+            case LoraTile::Odd64x64: return odd<LoraTile::Odd64x64, BKM>(c, s);
+            case LoraTile::Odd128x128: return odd<LoraTile::Odd128x128, BKM>(c, s);
+            case LoraTile::Odd256x128: return odd<LoraTile::Odd256x128, BKM>(c, s);
+            default: return hipErrorInvalidValue;
             }
-            if (c.p.M <= 32) return dma<16, 32, 256, 1, 2, 4, 4, BKM>(c, s);
-            if (c.p.M <= 96) return dma<32, 32, 128, 2, 2, 4, 4, BKM>(c, s);
-            if (c.p.M <= 144) return dma<32, 32, 128, 2, 2, 4, 0, BKM>(c, s);
-            if (tiles(256) >= 100) return launch_lora(&gemm_lora_pp_kernel<TI, TO, BKM>, c, 256, 256, 512, s);
-            if (tiles(64) <= 256) return dma<64, 64, 128, 2, 4, 3, 0, BKM>(c, s);
-            if (tiles(64) <= 512) return dma<64, 64, 64, 2, 4, 4, 0, BKM>(c, s);
-            return dma<128, 128, 64, 2, 4, 4, 0, BKM>(c, s);
+        } else {
+            if constexpr (!BKM)
+                if (t == LoraTile::Few16x32) return dma<LoraTile::Few16x32, BKM>(c, s);
+            switch (t) {
+            case LoraTile::Few32x32: return dma<LoraTile::Few32x32, BKM>(c, s);
+            case LoraTile::Shared32x32: return dma<LoraTile::Shared32x32, BKM>(c, s);
+            case LoraTile::Shared64x64: return dma<LoraTile::Shared64x64, BKM>(c, s);
+            case LoraTile::Shared64x64Four: return dma<LoraTile::Shared64x64Four, BKM>(c, s);
+            case LoraTile::Shared128x128: return dma<LoraTile::Shared128x128, BKM>(c, s);
+            case LoraTile::PingPong: return launch_lora(&gemm_lora_pp_kernel<TI, TO, BKM>, c, tile_of(LoraTile::PingPong), s);
+            default: return hipErrorInvalidValue;
+            }
         }
     }
     static hipError_t launch(const LoraCall& c, hipStream_t s)

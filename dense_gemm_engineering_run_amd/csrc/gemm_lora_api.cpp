@@ -116,8 +116,10 @@ int run(int64_t M, int64_t N, int64_t K, char a, char b, char c, int dtype, cons
     }
     q.b_kmajor = b == 'k';
     q.vec = vec;
-    // Workgroups of the smallest tile of any kernel here.
-    if ((M + 15) / 16 * ((N + 15) / 16) >= ((int64_t)1 << 31)) return GEMM_ERR_BAD_SHAPE;
+    const mg::LoraShape shape = mg::shape_of(q, es == 4);
+    const mg::Tile& tile = mg::kLoraTiles[(int)mg::lora_tile(shape)];
+    if (mg::lora_grid(shape, tile) > mg::kMaxGridThreads / tile.threads) return GEMM_ERR_BAD_SHAPE;
+    if (with && mg::ceil_div(M, q.shrink_rows) > mg::kMaxGridThreads / mg::kShrinkThreads) return GEMM_ERR_BAD_SHAPE;
     const int st = kLaunch[dtype](q, (hipStream_t)stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
     if (mg::log_enabled())
         std::fprintf(stderr, "mi355_gemm: lora %s M=%lld N=%lld K=%lld a=%c b=%c c=%c adapters=%lld rank=%lld %s\n",

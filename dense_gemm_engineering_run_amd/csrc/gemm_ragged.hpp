@@ -14,6 +14,7 @@
 #pragma once
 
 #include "gemm_f32dma.hpp"
+#include "gemm_tiles.hpp"
 
 namespace mg {
 
@@ -805,144 +806,82 @@ struct RaggedCall {
     bool vec;             // operands allow 16-byte loads
 };
 
-// The grid's upper bound: by rows, ceil(len_g / BM) tiles of BM rows summed
-// over the groups are at most (rows + groups * (BM - 1)) / BM.
+inline RaggedShape shape_of(const RaggedCall& c, bool f32)
+{
+    return {f32, c.by_rows, c.vec, c.b_kmajor, c.by_rows ? c.r.rows : c.p.M, c.p.N, c.r.groups};
+}
+
 template <By BY, class Kernel>
-hipError_t launch_ragged(Kernel kernel, const RaggedCall& c, int BM, int BN, int threads, hipStream_t s)
+hipError_t launch_ragged(Kernel kernel, const RaggedCall& c, const Tile& t, hipStream_t s)
 {
     Params p = c.p;
     Ragged r = c.r;
-    p.tiles_m = (p.M + BM - 1) / BM;
-    p.tiles_n = (p.N + BN - 1) / BN;
+    p.tiles_m = (int)ceil_div(p.M, t.bm);
+    p.tiles_n = (int)ceil_div(p.N, t.bn);
     // By k an XCD has 16 tiles of 4096 x 2048 outputs: 4 x 4 of them read fewer
     // rows of A and B than 8 x 2 (8192 k in 16 groups into fp32 187 us against
     // 192, in 32 groups 270 against 288).
     const int high = BY == By::K ? 4 : 8;
     p.group_m = p.tiles_m < high ? p.tiles_m : high;
-    dim3 grid;
-    if (BY == By::K) {
-        grid = dim3((unsigned)(p.tiles_m * p.tiles_n), (unsigned)r.groups);
-    } else {
-        int64_t t = ((int64_t)r.rows + (int64_t)r.groups * (BM - 1)) / BM;
-        if (t > r.rows) t = r.rows;
-        grid = dim3((unsigned)(t * p.tiles_n));
-    }
+    const dim3 grid((unsigned)ragged_grid(shape_of(c, false), t), BY == By::K ? (unsigned)r.groups : 1u);
     void* args[] = {&p, &r};
-    return hipLaunchKernel((const void*)kernel, grid, dim3(threads), args, 0, s);
+    return hipLaunchKernel((const void*)kernel, grid, dim3(t.threads), args, 0, s);
 }
 
 template <In TI, Out TO>
 struct RaggedInst {
-    template <int BM, int BN, int BK, int WM, int WN, int DEPTH, bool AK, bool BKM, By BY, bool EPI>
+    template <RaggedTile T, bool AK, bool BKM, By BY, bool EPI>
     static hipError_t odd(const RaggedCall& c, hipStream_t s)
     {
-        return launch_ragged<BY>(&gemm_ragged_odd_kernel<TI, TO, BM, BN, BK, WM, WN, DEPTH, AK, BKM, BY, EPI>, c, BM, BN, WM * WN * 64, s);
+        constexpr Tile t = tile_of(T);
+        return launch_ragged<BY>(&gemm_ragged_odd_kernel<TI, TO, t.bm, t.bn, t.bk, t.wm, t.wn, t.stages, AK, BKM, BY, EPI>, c, t, s);
     }
-    // Operands that are not 16-byte aligned, eight waves a tile.  Measured in
-    // bf16, B k-major (n-major in brackets where it differs), us, in brackets
-    // behind the 128x128 tile: on four waves:
-    //   rows/group  groups  N x K         32x64   64x128       128x128           256x128
-    //       2         8     4095 x 4095    54.8    70.6         72.7 ( 90.4)      98.3
-    //      16        64     1023 x 2047    72.0    67.4 [58.4]  72.0 ( 99.7)     107
-    //      50         2     4095 x 1023    10.9    17.0         20.2 ( 26.7)      28.4
-    //      64        32     2047 x 2047   117      97.5 [86.8] 110   (149)       116
-    //     128        32     2047 x 2047   189     142          116   (160)       168
-    //     512        16     4095 x 2047   635     397          298   (446) [278] 345 [350]
-    // Loads element by element took 181, 190, -, -, -, 1657 us.
-    template <bool BKM>
-    static hipError_t odd_rows(const RaggedCall& c, hipStream_t s)
-    {
-        const int64_t groups = c.r.groups, avg = (c.r.rows + groups - 1) / groups;
-        if (avg <= 8 || groups * ((avg + 31) / 32) * ((c.p.N + 63) / 64) <= 320)
-            return odd<32, 64, 128, 2, 4, 2, true, BKM, By::Rows, false>(c, s);
-        if (avg <= 80) return odd<64, 128, 64, 2, 4, 2, true, BKM, By::Rows, false>(c, s);
-        return odd<128, 128, 64, 2, 4, 2, true, BKM, By::Rows, false>(c, s);
-    }
-    // bf16 -> fp32, us: 8192 k in 16 groups of 4095 x 2047 402 (on 64x64 tiles
-    // 561); 4096 k in 4 groups of 1023 x 1023, 256 tiles, 30.0 (38.2 on 64x64
-    // with 128 k at a time); 8192 k in 8 groups of 511 x 511, 128 tiles, 34.6
-    // (26.7); in 4 groups of 255 x 255 47.1 (29.8).
-    template <bool EPI>
-    static hipError_t odd_k(const RaggedCall& c, hipStream_t s)
-    {
-        const int64_t tiles = ((int64_t)c.p.M + 127) / 128 * ((c.p.N + 127) / 128) * c.r.groups;
-        if (tiles <= 128) return odd<64, 64, 128, 2, 4, 2, false, false, By::K, EPI>(c, s);
-        return odd<128, 128, 64, 4, 2, 2, false, false, By::K, EPI>(c, s);
-    }
-    template <int BM, int BN, int BK, int WM, int WN, int MI, int ST, bool AK, bool BKM, By BY, bool EPI>
+    template <RaggedTile T, bool AK, bool BKM, By BY, bool EPI>
     static hipError_t dma(const RaggedCall& c, hipStream_t s)
     {
-        return launch_ragged<BY>(&gemm_ragged_dma_kernel<TI, TO, BM, BN, BK, WM, WN, MI, ST, AK, BKM, BY, EPI>, c, BM, BN, WM * WN * 64, s);
+        constexpr Tile t = tile_of(T);
+        return launch_ragged<BY>(&gemm_ragged_dma_kernel<TI, TO, t.bm, t.bn, t.bk, t.wm, t.wn, t.mi, t.stages, AK, BKM, BY, EPI>, c, t, s);
     }
     template <bool AK, bool BKM, By BY, bool EPI>
     static hipError_t pp(const RaggedCall& c, hipStream_t s)
     {
-        return launch_ragged<BY>(&gemm_ragged_pp_kernel<TI, TO, 256, 256, 64, 4, 2, 16, AK, BKM, BY, EPI>, c, 256, 256, 512, s);
+        constexpr Tile t = tile_of(RaggedTile::PingPong);
+        return launch_ragged<BY>(&gemm_ragged_pp_kernel<TI, TO, t.bm, t.bn, t.bk, t.wm, t.wn, t.mi, AK, BKM, BY, EPI>, c, t, s);
     }
-    // By rows: the tile height follows the rows a group has on average (the
-    // host knows no more), then how many tiles that makes.  Measured in bf16,
-    // B k-major (n-major in brackets where it differs), us:
-    //   rows/group  groups  N x K       16-row 32     64     128x128 128x256 256x256
-    //       1         8     4096 x 4096   39.7  38.6 [44.9] 42.0 [36.7] 41.6  61.7  75
-    //      16         8     4096 x 4096   55.9  53.2 [62.8] 61.8 [47.5] 62.5  74.1  75
-    //      16        64     2048 x 1024   60.3  56.9   51.5   61.1   59.0   85
-    //      64         8     4096 x 4096  100    77.4   67.3   90.4   78.7   88.9
-    //     128         8     4096 x 4096  168   118     95.6   89.0   80.2   89.2
-    //     128        32     2048 x 4096                155    143    153    194
-    //     256         8     4096 x 4096               132    121    126     90.9
-    //     256         8     2048 x 1024                21.1   25.7   20.2   23.5
-    //    1024         8     4096 x 2048               206    190    175    140
-    //    4096         8     4096 x 4096                      1270   1150    847
-    // (128x256 on eight waves of 16x16 MFMAs; on four of 32x32: 82.8 and 160 at
-    // 128 rows.)  Too few tiles of 128x256: 128x128, from 192 rows on in two
-    // stages, two workgroups a CU (22.9 us at 256 rows in 8 groups of 2048 x
-    // 1024, 24.6 in four stages).
-    // Products too small to fill the chip with those take the tile that spreads
-    // them further: 1 group of 48 rows of 1024 x 4096 14.6 on 32x64 (25.8 on
-    // 64x128), 4 groups of 128 20.2 (34.3 on 128x128), 4 groups of 300 28.0 on
-    // 128x64 (37.1 on 128x128).
     template <bool BKM>
     static hipError_t rows(const RaggedCall& c, hipStream_t s)
     {
-        const int64_t groups = c.r.groups, avg = (c.r.rows + groups - 1) / groups;
-        auto tiles = [&](int bm, int bn) { return groups * ((avg + bm - 1) / bm) * ((c.p.N + bn - 1) / bn); };
-        if (tiles(32, 64) <= 320) return dma<32, 64, 128, 1, 4, 16, 3, true, BKM, By::Rows, false>(c, s);
-        if (avg > 80 && tiles(128, 64) <= 192) return dma<128, 64, 64, 2, 2, 16, 4, true, BKM, By::Rows, false>(c, s);
-        if (avg <= 24) {
-            if constexpr (BKM) return dma<32, 64, 128, 1, 4, 16, 3, true, BKM, By::Rows, false>(c, s);
-            else return dma<64, 128, 64, 2, 2, 16, 3, true, BKM, By::Rows, false>(c, s);
+        switch (ragged_tile(shape_of(c, false))) {
+        case RaggedTile::Rows32x64: return dma<RaggedTile::Rows32x64, true, BKM, By::Rows, false>(c, s);
+        case RaggedTile::Rows64x128: return dma<RaggedTile::Rows64x128, true, BKM, By::Rows, false>(c, s);
+        case RaggedTile::Rows128x64: return dma<RaggedTile::Rows128x64, true, BKM, By::Rows, false>(c, s);
+        case RaggedTile::Rows128x128: return dma<RaggedTile::Rows128x128, true, BKM, By::Rows, false>(c, s);
+        case RaggedTile::Rows128x128Two: return dma<RaggedTile::Rows128x128Two, true, BKM, By::Rows, false>(c, s);
+        case RaggedTile::Rows128x256: return dma<RaggedTile::Rows128x256, true, BKM, By::Rows, false>(c, s);
+        case RaggedTile::PingPong: return pp<true, BKM, By::Rows, false>(c, s);
+        case RaggedTile::Odd32x64: return odd<RaggedTile::Odd32x64, true, BKM, By::Rows, false>(c, s);
+        case RaggedTile::Odd64x128: return odd<RaggedTile::Odd64x128, true, BKM, By::Rows, false>(c, s);
+        case RaggedTile::Odd128x128: return odd<RaggedTile::Odd128x128, true, BKM, By::Rows, false>(c, s);
+        default: return hipErrorInvalidValue;
         }
-        if (avg <= 80) return dma<64, 128, 64, 2, 2, 16, 3, true, BKM, By::Rows, false>(c, s);
-        if (avg >= 192 && tiles(256, 256) >= 100) return pp<true, BKM, By::Rows, false>(c, s);
-        if (tiles(128, 256) >= 100) return dma<128, 256, 64, 2, 4, 16, 3, true, BKM, By::Rows, false>(c, s);
-        if (avg < 192) return dma<128, 128, 64, 2, 2, 16, 4, true, BKM, By::Rows, false>(c, s);
-        return dma<128, 128, 64, 2, 2, 32, 2, true, BKM, By::Rows, false>(c, s);
     }
-    // By k: 256x256 tiles from three quarters of a CU's share of them up (bf16 ->
-    // fp32, 8 groups: 4096 x 2048 of 8192 k 161 us against 197 on 128x128; 4
-    // groups of 2048 x 2048 of 4096 k, 256 tiles, 43.2 against 48.1), then
-    // 128x128 in two stages, two workgroups a CU (8 groups of 1024 x 1024, 128
-    // tiles of 256x256: 36.4 against 47.1), up to one a CU in four (4 groups of
-    // 1024 x 1024: 19.5 against 24.4), and 64x64 where even those leave CUs idle
-    // (8 groups of 512 x 512 of 8192 k: 19.9 against 22.1; in 4 groups of 256 x
-    // 256 19.7 against 29.3).
     template <bool EPI>
     static hipError_t by_k(const RaggedCall& c, hipStream_t s)
     {
-        auto tiles = [&](int t) { return ((int64_t)c.p.M + t - 1) / t * ((c.p.N + t - 1) / t) * c.r.groups; };
-        if (tiles(256) >= 192) return pp<false, false, By::K, EPI>(c, s);
-        if (tiles(128) > 256) return dma<128, 128, 64, 2, 2, 32, 2, false, false, By::K, EPI>(c, s);
-        if (tiles(128) >= 192) return dma<128, 128, 64, 2, 4, 16, 4, false, false, By::K, EPI>(c, s);
-        return dma<64, 64, 64, 2, 2, 32, 4, false, false, By::K, EPI>(c, s);
+        switch (ragged_tile(shape_of(c, false))) {
+        case RaggedTile::K64x64: return dma<RaggedTile::K64x64, false, false, By::K, EPI>(c, s);
+        case RaggedTile::K128x128: return dma<RaggedTile::K128x128, false, false, By::K, EPI>(c, s);
+        case RaggedTile::K128x128Two: return dma<RaggedTile::K128x128Two, false, false, By::K, EPI>(c, s);
+        case RaggedTile::PingPong: return pp<false, false, By::K, EPI>(c, s);
+        case RaggedTile::OddK64x64: return odd<RaggedTile::OddK64x64, false, false, By::K, EPI>(c, s);
+        case RaggedTile::OddK128x128: return odd<RaggedTile::OddK128x128, false, false, By::K, EPI>(c, s);
+        default: return hipErrorInvalidValue;
+        }
     }
     static hipError_t launch(const RaggedCall& c, hipStream_t s)
     {
-        if (c.by_rows) {
-            if (c.vec) return c.b_kmajor ? rows<true>(c, s) : rows<false>(c, s);
-            return c.b_kmajor ? odd_rows<true>(c, s) : odd_rows<false>(c, s);
-        }
-        if (c.vec) return c.p.epi ? by_k<true>(c, s) : by_k<false>(c, s);
-        return c.p.epi ? odd_k<true>(c, s) : odd_k<false>(c, s);
+        if (c.by_rows) return c.b_kmajor ? rows<true>(c, s) : rows<false>(c, s);
+        return c.p.epi ? by_k<true>(c, s) : by_k<false>(c, s);
     }
 };
 

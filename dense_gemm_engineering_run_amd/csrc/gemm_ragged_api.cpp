@@ -82,9 +82,9 @@ int run(bool by_rows, int64_t M, int64_t N, int64_t K, char a, char b, char c, i
     q.by_rows = by_rows;
     q.b_kmajor = b == 'k';
     q.vec = vec;
-    // Tiles in the grid, counted for the smallest tile of any kernel here.
-    const int64_t tn = (p.N + 15) / 16, tm = by_rows ? ((int64_t)M + groups * 15) / 16 : (p.M + 15) / 16;
-    if (tm * tn >= ((int64_t)1 << 31)) return GEMM_ERR_BAD_SHAPE;
+    const mg::RaggedShape shape = mg::shape_of(q, es == 4);
+    const mg::Tile& tile = mg::kRaggedTiles[(int)mg::ragged_tile(shape)];
+    if (mg::ragged_grid(shape, tile) > mg::kMaxGridThreads / tile.threads) return GEMM_ERR_BAD_SHAPE;
     const int st = kLaunch[dtype](q, (hipStream_t)stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
     if (mg::log_enabled())
         std::fprintf(stderr, "mi355_gemm: %s %s M=%lld N=%lld K=%lld a=%c b=%c c=%c groups=%lld %s\n",

@@ -295,9 +295,11 @@ int gemm_run_config(int64_t M, int64_t N, int64_t K, char a_major, char b_major,
  * Sizes, alignment (operands that are not 16-byte aligned run other kernels;
  * C's own alignment only decides the width of its stores), the checks and
  * their order, asynchrony and errors are those of gemm_run; ends must be
- * 4-byte aligned and not overlap C.  groups <= 65535; groups == 0
- * launches nothing.  No workspace; results are deterministic.  The tile
- * config is the library's choice (gemm_last_config does not record it).
+ * 4-byte aligned and not overlap C.  groups <= 65535, and the most tiles that
+ * any ends could need have to fit a launch (2^32 threads along an axis; else
+ * GEMM_ERR_BAD_SHAPE, after the overlap check); groups == 0 launches nothing.
+ * No workspace; results are deterministic.  The tile config is the library's
+ * choice (gemm_last_config does not record it).
  */
 int gemm_run_grouped(int64_t M, int64_t N, int64_t K, char a_major, char b_major, char c_major,
                      int dtype, const void* A, const void* B, void* C,

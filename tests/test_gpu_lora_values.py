@@ -7,14 +7,14 @@ the definition has one, of its sign, and NaN only where it has that.
 import pytest
 import torch
 
+from row_kernel_cases import LORA_VALUES
 from test_gpu_lora import TYPES, Case, say
 
 pytestmark = pytest.mark.gpu
 
 # Rows, columns and padding (1: operands that are not 16-byte aligned): every
 # kernel of the product.
-KERNELS = [(1, 72, 0), (24, 72, 0), (48, 136, 0)] + [(M, N, 1) for M, N in ((1, 72), (300, 520), (515, 2056), (1500, 1504), (4008, 2600))]
-KERNELS += [(140, 136, 0), (300, 520, 0), (515, 2056, 0), (1500, 1504, 0), (2312, 2568, 0)]
+KERNELS = [(M, N, pad) for (_, pad), sizes in LORA_VALUES.items() for M, N in sizes]
 
 
 def definition(x):

@@ -89,6 +89,20 @@ struct RaggedShape {
 // them further: 1 group of 48 rows of 1024 x 4096 14.6 on 32x64 (25.8 on
 // 64x128), 4 groups of 128 20.2 (34.3 on 128x128), 4 groups of 300 28.0 on
 // 128x64 (37.1 on 128x128).
+// At the limits (K = 2048 unless given; the tile above a limit second):
+//   320 tiles of 32x64: 5 groups of 32 rows, N = 4096, 18.4 and 17.2 (4 groups
+//     13.8 and 16.8); 5 of 64, N = 2048, 14.0 and 16.3; 2 of 128 rows, N = 2560,
+//     13.4 and 15.5 on 128x64.
+//   192 tiles of 128x64: 4 groups of 128 rows, N = 3008, 16.3 and 21.8 on
+//     128x128; 4 of 256, N = 1536, 16.3 and 21.2.
+//   24 rows: 16 groups, N = 2048, 23.8 and 24.5; 8 of 4096 x 4096 55.4 and 65.9
+//     (32 rows 57.0 and 66.1); n-major 26.1 and 23.3 at 16.
+//   80 rows: 16 groups, N = 2048, 30.1 and 26.2 (64 rows 25.3 and 25.8).
+//   192 rows: 16 groups, N = 2048, 37.4 on 128x256 and 45.2 on 256x256 (224
+//     rows 40.9 and 47.0); 100 tiles of 256x256: 6 groups of 256 rows, N = 4096,
+//     32.4 and 39.4 (128 tiles 40.7 and 46.8).
+//   100 tiles of 128x256: 7 groups of 128 rows, N = 3500, 23.7 on 128x128 and
+//     31.2; 9 of 256, N = 1536, 28.4 and 29.6.
 //
 // Unaligned 16-bit operands, eight waves a tile.  Measured in bf16, B k-major
 // (n-major in brackets where it differs), us, in brackets behind the 128x128
@@ -101,6 +115,9 @@ struct RaggedShape {
 //     128        32     2047 x 2047   189     142          116   (160)       168
 //     512        16     4095 x 2047   635     397          298   (446) [278] 345 [350]
 // Loads element by element took 181, 190, -, -, -, 1657 us.
+// At the limits (K = 2048): 8 rows in 16 groups, N = 2048, 26.8 and 34.4; 320
+// tiles, 5 groups of 40, N = 2048, 24.0 and 29.1; 80 rows in 16 groups 52.5 and
+// 40.9 (64 rows 39.1 and 40.5).
 //
 // fp32, us (K = 1024; 64x64 in three stages, 64x128 in two, 128x128 in two):
 //           64 rows in  4 groups of 1024     24.2    41.9   66.9
@@ -116,6 +133,11 @@ struct RaggedShape {
 //       64 rows in  16 groups of 2048 x 1024                   69.3          68.9    62.9
 //      300 rows in   1 group  of 1024 x 4096                   40.8          39.8    83.6
 // (Four waves that share a row's k-tiles also round less than one.)
+// At the limits: 16 rows in 8 groups of 4096 x 4096 104 and 112 on 32x64 (20
+// rows 128 and 113); 48 rows in 16 groups of 2048 x 2048 101 on 32x64, 95 on
+// 32x32, 79 on 64x64; 192 tiles of 64x64, 12 groups of 64 rows of 1024 x 2048,
+// 36.8 and 45.1; 1024 tiles of 64x128, 16 groups of 256 rows of 2048 x 1024, 146
+// on 64x64 and 169 (18 groups 165 and 170).
 inline RaggedTile rows_tile(const RaggedShape& s)
 {
     const int64_t avg = ceil_div(s.M, s.groups);
@@ -156,6 +178,12 @@ inline RaggedTile rows_tile(const RaggedShape& s)
 //        16 groups of 512 x 512              28.1           43.4
 //         4 groups of 1024 x 1024            75.7           98.6
 //         4 groups of 4096 x 2048           550            503
+// At the limits (1024 k a group; the tile above a limit second): 192 tiles of
+// 256x256, 6 groups of 2048 x 1024, 36.8 on 128x128 and 37.7 (into bf16 35.4 and
+// 33.4); 256 tiles of 128x128, 4 groups of 1024 x 1024, 16.5 on eight waves and
+// 17.3 (5 groups 27.1 and 20.5); 192, 4 groups of 1024 x 768, 19.6 on 64x64 and
+// 15.5.  Unaligned, 8 groups of 512 x 512 21.9 and 21.5 (10 groups 29.7 and
+// 21.8).  fp32, 512 tiles, 8 groups of 1024 x 1024 of 512 k 75.6 and 69.9.
 inline RaggedTile k_tile(const RaggedShape& s)
 {
     auto tiles = [&](int t) { return ceil_div(s.M, t) * ceil_div(s.N, t) * s.groups; };
@@ -216,7 +244,9 @@ struct LoraShape {
 };
 
 // The limits stand between sizes that were measured on both sides, rows with an
-// adapter each up to 64 rows and packed prompts above.
+// adapter each up to 64 rows and packed prompts above, at N = 4096.  (Those by M
+// alone suit N up to that: 144 rows at N = 14336, K = 4096 take 97 us on 32x32
+// and 58 on 128x128.)
 //
 // fp32, N = K = 4096, us for both kernels (rows: one adapter each of 16 up to
 // 64, packed above; B n-major in brackets):
@@ -229,6 +259,9 @@ struct LoraShape {
 //    256 128                               158  [224]     130 [146]     238 [238]
 //   1024  16                               419  [429]     298 [303]     283 [284]
 //   4096  16                              1344           1110          1065
+// At the limits: 16 rows 27.1 and 29.9 (24 rows 35.2 and 30.9), 32 rows 30.5 and
+// 40.9 (48 rows 44.2 and 44.1), 192 tiles of 64x64 73.8 and 96.0 (256 tiles 92.0
+// and 96.5), 512 tiles of 64x128 296 and 275.
 //
 // Unaligned 16-bit operands, bf16, N = 4096, K = 4095, us for both kernels
 // (rows: one adapter each of 16 up to 64, packed above):
@@ -240,6 +273,9 @@ struct LoraShape {
 //   1024  64   297     182      115      171
 //   4096  64   971     517      383      315
 // (Loads element by element: 123 at one row, 1853 at 4096.)
+// At the limits: 128 rows 41.7 and 49.4, 144 rows 61.5 and 50.4; 512 tiles of
+// 64x64 78.8 and 89.7 (576 107 and 92); 256 tiles of 256x128 175 on 128x128 and
+// 149 (2304 rows 251 and 271).
 //
 // 16-bit, bf16, N = K = 4096, us for both kernels (rows: one adapter each up to
 // 64, packed above; rank):
@@ -260,6 +296,13 @@ struct LoraShape {
 // 66.5 on four.)  64x64 tiles that the chip holds at once take 128 of k at a
 // time in three stages (33.9 us at 256 rows, 36.6 with 64 in four; at 512 rows
 // 56.9 and 49.5).
+// At the limits (rank 16 up to 40 rows, 64 above): 16 rows 21.5 and 24.8 (20
+// rows 30.4 and 24.4); 32 rows 25.0 and 29.4 (40 rows 36.2 and 30.3), B n-major
+// 28.8 and 29.9 (44.8 and 30.7); 96 rows packed 28.0 on 32x32 and 27.8 shared,
+// an adapter each 43.1 and 53.9; 128 rows 27.7 and 30.8 on 64x64, 144 rows 40.5
+// and 32.2; 256 tiles of 64x64 30.6 and 34.9 (320 51.1 and 45.9), 512 45.5 and
+// 47.6 on 128x128 (576 66.1 and 49.5); 100 tiles of 256x256 (1664 rows are 112)
+// 94.0 on 128x128 and 95.4, 1792 rows 94.5 and 93.8.
 inline LoraTile lora_tile(const LoraShape& s)
 {
     auto tiles = [&](int bm, int bn) { return ceil_div(s.M, bm) * ceil_div(s.N, bn); };

@@ -359,7 +359,9 @@ typedef struct {
  * and the three arrays must not overlap C, nor the workspace any input
  * (GEMM_ERR_ALIAS).  Sizes, alignment (A, B or down not 16-byte
  * aligned: the kernels for that run), the checks and their order, asynchrony
- * and errors are otherwise those of gemm_run_ws; results are deterministic.
+ * and errors are otherwise those of gemm_run_ws, and sizes whose grid no launch
+ * can have (2^32 threads) are GEMM_ERR_BAD_SHAPE after the others; results are
+ * deterministic.
  */
 int gemm_run_lora(int64_t M, int64_t N, int64_t K, char a_major, char b_major, char c_major,
                   int dtype, const void* A, const void* B, void* C,

@@ -8,4 +8,5 @@ from ._binding import (Epilogue, GemmError, Lora, gemm, gemm_config_describe, ge
                        gemm_load_tuning, gemm_num_configs, gemm_run, gemm_run_batched, gemm_run_config,
                        gemm_run_ex, gemm_run_ws, gemm_select_config, gemm_status_str, gemm_tuning_size,
                        gemm_workspace_size, grouped_gemm, grouped_gemm_k, gemm_lora, gemm_lora_workspace_size,
-                       gemm_run_grouped, gemm_run_grouped_k, gemm_run_lora)
+                       gemm_run_grouped, gemm_run_grouped_k, gemm_run_lora, quantize_rows, dequantize_rows, gemm_i8,
+                       gemm_i8_grad, gemm_quantize_rows, gemm_dequantize_rows, gemm_run_i8, gemm_run_i8_grad)

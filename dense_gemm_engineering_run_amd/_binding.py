@@ -67,6 +67,10 @@ _LORA = struct.Struct("qqPPqqqqPPP")      # the same, packed in one step
 assert _LORA.size == ctypes.sizeof(Lora)
 
 
+_EPILOGUE = struct.Struct("ffPi4x")     # Epilogue, packed in one step
+assert _EPILOGUE.size == ctypes.sizeof(Epilogue)
+
+
 _RUN_ARGS = [_i64, _i64, _i64, _chr, _chr, _chr, _int, _vp, _vp, _vp, _i64, _i64, _i64, _vp]
 _lib.gemm_run.argtypes = _RUN_ARGS
 _lib.gemm_run.restype = _int
@@ -93,6 +97,14 @@ _lib.gemm_run_lora.argtypes = _RUN_ARGS[:-1] + [ctypes.c_char_p, _vp, ctypes.c_s
 _lib.gemm_run_lora.restype = _int
 _lib.gemm_lora_workspace_size.argtypes = [_i64, _i64, _i64, _int, _i64, ctypes.POINTER(ctypes.c_size_t)]
 _lib.gemm_lora_workspace_size.restype = _int
+_lib.gemm_quantize_rows.argtypes = [_i64, _i64, _int, _vp, _vp, _vp, _i64, _i64, _vp]
+_lib.gemm_quantize_rows.restype = _int
+_lib.gemm_dequantize_rows.argtypes = _lib.gemm_quantize_rows.argtypes
+_lib.gemm_dequantize_rows.restype = _int
+_lib.gemm_run_i8.argtypes = _RUN_ARGS[:-1] + [_vp, _vp, ctypes.c_char_p, _vp]          # gemm_epilogue_t's bytes
+_lib.gemm_run_i8.restype = _int
+_lib.gemm_run_i8_grad.argtypes = _RUN_ARGS[:-1] + [_vp, _int, _vp]
+_lib.gemm_run_i8_grad.restype = _int
 _lib.gemm_status_str.argtypes = [_int]
 _lib.gemm_status_str.restype = ctypes.c_char_p
 _lib.gemm_num_configs.argtypes = [_int]
@@ -117,6 +129,9 @@ _lib.gemm_probe_hbm_read.restype = _int
 # gemm_dtype_t
 DTYPE_F32, DTYPE_F16_F32, DTYPE_BF16_BF16, DTYPE_F16_F16, DTYPE_BF16_F32 = range(5)
 DTYPE_NAMES = ["f32", "f16_f32", "bf16_bf16", "f16_f16", "bf16_f32"]
+
+# gemm_type_t
+GEMM_TYPE_F32, GEMM_TYPE_F16, GEMM_TYPE_BF16 = range(3)
 
 # gemm_status_t (values as in include/mi355_gemm.h)
 GEMM_OK = 0
@@ -216,6 +231,29 @@ def gemm_lora_workspace_size(M, N, K, dtype, rank):
     if st != GEMM_OK:
         raise GemmError(st)
     return n.value
+
+
+def gemm_quantize_rows(M, K, type, X, Q, scales, ldx, ldq, stream=0):
+    """C ABI gemm_quantize_rows (device addresses). Returns the status."""
+    return _lib.gemm_quantize_rows(M, K, type, X, Q, scales, ldx, ldq, stream)
+
+
+def gemm_dequantize_rows(M, K, type, Q, scales, X, ldq, ldx, stream=0):
+    """C ABI gemm_dequantize_rows (device addresses). Returns the status."""
+    return _lib.gemm_dequantize_rows(M, K, type, Q, scales, X, ldq, ldx, stream)
+
+
+def gemm_run_i8(M, N, K, a_major, b_major, c_major, type, A, B, C, lda, ldb, ldc, scale_a=0, scale_b=0, epilogue=None,
+                stream=0):
+    """C ABI gemm_run_i8; `epilogue` is an Epilogue or None. Returns the status."""
+    return _lib.gemm_run_i8(M, N, K, _c(a_major), _c(b_major), _c(c_major), type, A, B, C, lda, ldb, ldc, scale_a, scale_b,
+                            bytes(epilogue) if epilogue is not None else None, stream)
+
+
+def gemm_run_i8_grad(M, N, K, a_major, b_major, c_major, dtype, A, Q, C, lda, ldq, ldc, scales, accumulate=0, stream=0):
+    """C ABI gemm_run_i8_grad. Returns the status."""
+    return _lib.gemm_run_i8_grad(M, N, K, _c(a_major), _c(b_major), _c(c_major), dtype, A, Q, C, lda, ldq, ldc, scales,
+                                 int(bool(accumulate)), stream)
 
 
 def gemm_workspace_size(M, N, K, a_major, b_major, c_major, dtype, config_id=-1):
@@ -464,6 +502,106 @@ def gemm_lora(a, b, c, down, up, ids, workspace, ranks=None, scales=None, stream
     _launch(_lib.gemm_run_lora, index, stream, M, N, K, b"k", bm, b"n", dtype_code(dtype, c.dtype), a.data_ptr(),
             b.data_ptr(), c.data_ptr(), lda, ldb, ldc, lora, workspace.data_ptr(),
             workspace.numel() * workspace.element_size())
+    return c
+
+
+_TYPE_CODES = {} if torch is None else {torch.float32: GEMM_TYPE_F32, torch.float16: GEMM_TYPE_F16,
+                                        torch.bfloat16: GEMM_TYPE_BF16}
+
+
+def _type_code(dtype, what):
+    try:
+        return _TYPE_CODES[dtype]
+    except KeyError:
+        raise ValueError(f"{what} must be float32, float16 or bfloat16, not {dtype}") from None
+
+
+def _float_vector(t, n, what):
+    if t.dtype is not torch.float32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous float32 vector of {n}")
+
+
+def _rows8(wide, q, scales, names):
+    """Checks of a matrix, its 8-bit form and its rows' scales: the GPU, M, K,
+    both leading dimensions and the wide type's code."""
+    index = _gpu_index(wide, q, scales)
+    shape = wide.shape
+    if len(shape) != 2 or q.shape != shape:
+        raise ValueError(f"shape mismatch: {names[0]} {tuple(shape)}, {names[1]} {tuple(q.shape)}")
+    if q.dtype is not torch.int8:
+        raise ValueError(f"{names[1]} must be int8, not {q.dtype}")
+    _float_vector(scales, shape[0], "scales")
+    ldw, ldq = _ld(shape, wide.stride(), 0, 1), _ld(shape, q.stride(), 0, 1)
+    if ldw is None or ldq is None:
+        raise ValueError(f"{names[0]} {wide.stride()} and {names[1]} {q.stride()} must be row-major")
+    return index, shape[0], shape[1], ldw, ldq, _type_code(wide.dtype, names[0])
+
+
+def quantize_rows(x, q, scales, stream=None):
+    """Rows of x (M, K) to 8-bit integers q (M, K) and a float32 scale each
+    (gemm_quantize_rows): scales = max |x| / 127 of a row, q = x / scales to the
+    nearest, ties to even.  x and q are row-major.  Returns q and scales."""
+    index, M, K, ldx, ldq, code = _rows8(x, q, scales, ("x", "q"))
+    _launch(_lib.gemm_quantize_rows, index, stream, M, K, code, x.data_ptr(), q.data_ptr(), scales.data_ptr(), ldx, ldq)
+    return q, scales
+
+
+def dequantize_rows(q, scales, x, stream=None):
+    """x = q * scales[:, None] in x's type (gemm_dequantize_rows); x and q are
+    (M, K), row-major.  Returns x."""
+    index, M, K, ldx, ldq, code = _rows8(x, q, scales, ("x", "q"))
+    _launch(_lib.gemm_dequantize_rows, index, stream, M, K, code, q.data_ptr(), scales.data_ptr(), x.data_ptr(), ldq, ldx)
+    return x
+
+
+def gemm_i8(a, b, scale_a, scale_b, c, bias=None, activation=GEMM_ACT_NONE, stream=None):
+    """C = act(scale_a[:, None] * scale_b * (A * B^T) + bias) (gemm_run_i8): a is
+    (M, K) and b (N, K), int8, c (M, N), all row-major; scale_a (M,), scale_b (N,)
+    and bias (N,) are float32 vectors or None; activation is a GEMM_ACT_*."""
+    index = _gpu_index(a, b, c)
+    sa, sb = a.shape, b.shape
+    if len(sa) != 2 or len(sb) != 2 or sb[1] != sa[1] or c.shape != (sa[0], sb[0]):
+        raise ValueError(f"shape mismatch: a {tuple(sa)}, b {tuple(sb)}, c {tuple(c.shape)}")
+    if a.dtype is not torch.int8 or b.dtype is not torch.int8:
+        raise ValueError(f"a and b must be int8, not {a.dtype} and {b.dtype}")
+    at = [0, 0, 0]
+    for i, (t, n, what) in enumerate(((scale_a, sa[0], "scale_a"), (scale_b, sb[0], "scale_b"), (bias, sb[0], "bias"))):
+        if t is not None:
+            _gpu_index(a, t)
+            _float_vector(t, n, what)
+            at[i] = t.data_ptr()
+    lda, ldb, ldc = _ld(sa, a.stride(), 0, 1), _ld(sb, b.stride(), 0, 1), _ld(c.shape, c.stride(), 0, 1)
+    if lda is None or ldb is None or ldc is None:
+        raise ValueError(f"a {a.stride()}, b {b.stride()} and c {c.stride()} must be row-major")
+    epilogue = None if bias is None and activation == GEMM_ACT_NONE else _EPILOGUE.pack(1.0, 0.0, at[2], activation)
+    _launch(_lib.gemm_run_i8, index, stream, sa[0], sb[0], sa[1], b"k", b"k", b"n", _type_code(c.dtype, "c"), a.data_ptr(),
+            b.data_ptr(), c.data_ptr(), lda, ldb, ldc, at[0], at[1], epilogue)
+    return c
+
+
+def gemm_i8_grad(a, q, scales, c, accumulate=False, stream=None):
+    """C[m][n] = sum over k of A[m][k] * scales[k] * Q[n][k], or that added to C
+    (gemm_run_i8_grad): a is (M, K) with M or K contiguous, q an int8 (N, K) with N
+    contiguous, scales a float32 (K,), c (M, N) row-major.  For a layer y =
+    x * w^T with xq, xs = quantize_rows(x, ...) and wq, ws = quantize_rows(w, ...):
+    gemm_i8_grad(dy.t(), xq.t(), xs, dw) and gemm_i8_grad(dy, wq.t(), ws, dx)."""
+    index = _gpu_index(a, q, scales, c)
+    sa, sq = a.shape, q.shape
+    if len(sa) != 2 or len(sq) != 2 or sq[1] != sa[1] or c.shape != (sa[0], sq[0]):
+        raise ValueError(f"shape mismatch: a {tuple(sa)}, q {tuple(sq)}, c {tuple(c.shape)}")
+    if q.dtype is not torch.int8:
+        raise ValueError(f"q must be int8, not {q.dtype}")
+    _float_vector(scales, sa[1], "scales")
+    ta = a.stride()
+    am, lda = b"k", _ld(sa, ta, 0, 1)
+    if lda is None:
+        am, lda = b"m", _ld(sa, ta, 1, 0)
+    ldq, ldc = _ld(sq, q.stride(), 1, 0), _ld(c.shape, c.stride(), 0, 1)
+    if lda is None or ldq is None or ldc is None:
+        raise ValueError(f"a {ta} must have one contiguous dimension, q {q.stride()} be the transposed view of a row-major "
+                         f"matrix, c {c.stride()} row-major")
+    _launch(_lib.gemm_run_i8_grad, index, stream, sa[0], sq[0], sa[1], am, b"n", b"n", dtype_code(a.dtype, c.dtype),
+            a.data_ptr(), q.data_ptr(), c.data_ptr(), lda, ldq, ldc, scales.data_ptr(), bool(accumulate))
     return c
 
 

@@ -194,6 +194,20 @@ struct DmaOperand {
             }
         }
     }
+
+    // The same for 8-bit values, `valid` of them left in a row.
+    template <int NT>
+    __device__ static __forceinline__ void zero_tail_bytes(char* t, int valid, int tid)
+    {
+        static_assert(KMAJ, "8-bit operands are k-contiguous");
+#pragma unroll 1
+        for (int idx = tid; idx < ROWS * CPR; idx += NT) {
+            const int row = idx / CPR, c = idx % CPR;
+            if (c < valid / 16) continue;
+            i32x4* q = (i32x4*)(t + row * RB + swz_chunk<CPR, true>(row, c) * 16);
+            *q = mask_bytes(*q, valid - c * 16);
+        }
+    }
 };
 
 // The pieces of the kernel: the main loop over a range of k-tiles of one C
@@ -272,7 +286,7 @@ struct Dma16 {
         const int wm = wave / WN, wn = wave % WN;
         const int nkt = (p.K + BK - 1) / BK;
         const int kvalid_last = p.K - (nkt - 1) * BK;
-        const bool ragged = kvalid_last != BK;
+        const bool ragged = kvalid_last != BK || (TI == In::I8 && p.k_odd);
         // Operand fields as locals (the DMA asm statements clobber memory).
         const char* const A = p.A;
         const char* const B = p.B;
@@ -310,8 +324,12 @@ struct Dma16 {
             char* sb = b_stage(smem, r);
             if (t == nkt - 1 && ragged && (AK || BKM)) {
                 bare_barrier();
-                oa.template zero_tail<NT>(sa, kvalid_last, tid);
-                ob.template zero_tail<NT>(sb, kvalid_last, tid);
+                if constexpr (TI == In::I8) {     // integers: one factor's zeros are enough
+                    oa.template zero_tail_bytes<NT>(sa, kvalid_last * 2 - p.k_odd, tid);
+                } else {
+                    oa.template zero_tail<NT>(sa, kvalid_last, tid);
+                    ob.template zero_tail<NT>(sb, kvalid_last, tid);
+                }
                 __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): the zeros are written
             }
             // A bare barrier: this wave's loads of tile t are complete (the vmcnt

@@ -1,0 +1,211 @@
+// gemm_i8.hpp -- products of 8-bit integers with a scale per row and column (gfx950).
+//
+//   C[m][n] = act(alpha * scale_a[m] scale_b[n] sum_k A[m][k] B[n][k] + beta * C_old[m][n] + bias[n])
+//
+// The sum is exact: 32-bit integers on the integer MFMAs, whose 16x16x64 and
+// 32x32x32 forms take 16 consecutive k of a row a lane, the byte layout of the
+// 16-bit forms.  So the tiles, rings and schedules of the 16-bit products
+// (gemm_dma.hpp, gemm_ragged.hpp) hold here as they are, on pairs of 8-bit
+// values (In::I8): Params::K, lda and ldb count pairs.  When the sums are
+// done they are scaled in their registers and leave by the 16-bit products'
+// stores.
+#pragma once
+
+#include "gemm_quant.hpp"
+#include "gemm_ragged.hpp"
+
+namespace mg {
+
+struct I8Scales {
+    const float* a;       // per row of C, or null: 1
+    const float* b;       // per column of C, or null: 1
+};
+
+// One output from its sum's bits: scaled in fp32 (the conversion and each
+// product round once), then the elementwise epilogue.
+template <Out TO>
+__device__ __forceinline__ float i8_value(const Params& p, int m, int n, float bits, float sa, float sb)
+{
+    const float v = settled((float)__float_as_int(bits) * sa * sb);
+    return p.epi && m < p.M && n < p.N ? epi_value<TO>(p, m, n, v) : v;
+}
+
+// The sums of an accumulator tile of KT (rows along its registers) to outputs.
+template <class KT>
+__device__ __forceinline__ void i8_finish(const Params& p, const I8Scales& s, int m0, int n0, typename KT::Acc& acc, int lane,
+                                          int wave)
+{
+    constexpr int WN = KT::TILE_N / KT::WTN;
+    const int wm = wave / WN, wn = wave % WN;
+    float sb[KT::TN];
+#pragma unroll
+    for (int j = 0; j < KT::TN; ++j) {
+        const int n = n0 + KT::col(wn, j, lane);
+        sb[j] = s.b && n < p.N ? s.b[n] : 1.f;
+    }
+#pragma unroll
+    for (int i = 0; i < KT::TM; ++i)
+#pragma unroll
+        for (int q = 0; q < KT::R; ++q) {
+            const int m = m0 + KT::row(wm, i, q, lane);
+            const float sa = s.a && m < p.M ? s.a[m] : 1.f;
+#pragma unroll
+            for (int j = 0; j < KT::TN; ++j)
+                acc[i][j][q] = i8_value<KT::OUT>(p, m, n0 + KT::col(wn, j, lane), acc[i][j][q], sa, sb[j]);
+        }
+}
+
+// ------------------------------------------------------------ operands at any byte
+
+// Rows that start at any byte: as OddRows and OddChunk, whose elements are two
+// bytes.  Words that hold an own byte are read, nothing else.
+struct ByteRows {
+    __amdgpu_buffer_rsrc_t r;
+
+    __device__ __forceinline__ ByteRows(const char* base, uint64_t bytes)
+        : r(make_rsrc(base - ((uint64_t)base & 3), bytes ? (bytes + ((uint64_t)base & 3) + 3) / 4 * 4 : 0))
+    {
+    }
+};
+
+// An operand's k-tiles of 2 * BK bytes a row, from memory through registers to
+// the LDS layout of DmaOperand.
+template <int ROWS, int BK, int NW, int DEPTH>
+struct ByteOperand {
+    using LDS = DmaOperand<ROWS, BK, NW, true, 16>;
+    int voff[LDS::IPW];
+    i32x4 words[DEPTH][LDS::IPW];
+    int last[DEPTH][LDS::IPW];
+
+    // ld in bytes.  (row0 is a multiple of 4 and k0 of 16, so every tile's
+    // first byte lies in its word as the base's.)
+    __device__ __forceinline__ void init(int wave, int lane, int64_t ld, const char* base)
+    {
+#pragma unroll
+        for (int j = 0; j < LDS::IPW; ++j) {
+            const int slot = (wave * LDS::IPW + j) * 64 + lane, row = slot / LDS::CPR;
+            voff[j] = (int)(row * ld) + swz_chunk<LDS::CPR, true>(row, slot % LDS::CPR) * 16 + (int)((uint64_t)base & 3);
+        }
+    }
+    __device__ __forceinline__ void load(int d, const char* base, uint64_t bytes, int64_t ld, int row0, int k0)
+    {
+        const int64_t origin = (int64_t)row0 * ld + k0;
+        const ByteRows s(base + origin, (uint64_t)origin < bytes ? bytes - (uint64_t)origin : 0);
+#pragma unroll
+        for (int j = 0; j < LDS::IPW; ++j) {
+            words[d][j] = buf_load16(s.r, voff[j] & ~3);
+            last[d][j] = __builtin_amdgcn_raw_buffer_load_b32(s.r, (voff[j] & ~3) + 16, 0, 0);
+        }
+    }
+    // ... of the tile at k0; bytes from K on as zeros.
+    __device__ __forceinline__ void store(int d, char* tile, int k0, int K, int wave, int lane) const
+    {
+#pragma unroll
+        for (int j = 0; j < LDS::IPW; ++j) {
+            const int slot = (wave * LDS::IPW + j) * 64 + lane;
+            const uint32_t sh = ((uint32_t)voff[j] & 3) * 8;
+            i32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = (int)__builtin_amdgcn_alignbit((uint32_t)(e < 3 ? words[d][j][e + 1] : last[d][j]),
+                                                      (uint32_t)words[d][j][e], sh);
+            if (k0 + 2 * BK > K)
+                v = mask_bytes(v, K - k0 - swz_chunk<LDS::CPR, true>(slot / LDS::CPR, slot % LDS::CPR) * 16);
+            *(i32x4*)(tile + slot * 16) = v;
+        }
+    }
+};
+
+// Operands at any byte (p.K, lda, ldb and the extents in bytes): LDS in two
+// stages, DEPTH tiles of loads in flight, one barrier a tile.
+template <Out TO, int BM, int BN, int BK, int WM, int WN, int DEPTH>
+__global__ void __launch_bounds__(WM * WN * 64)
+gemm_i8_odd_kernel(Params p, I8Scales sc)
+{
+    using KT = Dma16<In::I8, TO, BM, BN, BK, WM, WN, 16, 2, true, true>;
+    static_assert(DEPTH % 2 == 0, "a tile's stage is known at compile time");
+    __shared__ __attribute__((aligned(1024))) char smem[KT::SMEM];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tm, tn;
+    tile_coords(p, tm, tn);
+    tm = __builtin_amdgcn_readfirstlane(tm);
+    tn = __builtin_amdgcn_readfirstlane(tn);
+    const int m0 = tm * BM, n0 = tn * BN, wm = wave / WN, wn = wave % WN;
+    constexpr int KB = 2 * BK;
+    const int nkt = (p.K + KB - 1) / KB;
+    typename KT::Acc acc;
+    KT::zero(acc);
+    ByteOperand<BM, BK, KT::NW, DEPTH> oa;
+    ByteOperand<BN, BK, KT::NW, DEPTH> ob;
+    oa.init(wave, lane, p.lda, p.A);
+    ob.init(wave, lane, p.ldb, p.B);
+    auto load = [&](int t, int d) {               // past the end: empty extents
+        oa.load(d, p.A, t < nkt ? p.a_bytes : 0, p.lda, m0, t * KB);
+        ob.load(d, p.B, t < nkt ? p.b_bytes : 0, p.ldb, n0, t * KB);
+    };
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) load(d, d);
+    for (int t0 = 0; t0 < nkt; t0 += DEPTH) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            const int t = t0 + d;
+            if (t >= nkt) break;
+            char* const sa = smem + d % 2 * KT::STAGE;
+            char* const sb = sa + KT::OA::BYTES;
+            oa.store(d, sa, t * KB, p.K, wave, lane);
+            ob.store(d, sb, t * KB, p.K, wave, lane);
+            load(t + DEPTH, d);
+            // The other stage is written after the next barrier, when every
+            // wave has read it.
+            __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0)
+            bare_barrier();
+#pragma unroll
+            for (int g = 0; g < KT::NG; ++g) {
+                i32x4 fa[KT::TM], fb[KT::TN];
+#pragma unroll
+                for (int i = 0; i < KT::TM; ++i) fa[i] = KT::OA::template frag<16>(sa, wm * KT::WTM + i * 16, g * 32, lane);
+#pragma unroll
+                for (int j = 0; j < KT::TN; ++j) fb[j] = KT::OB::template frag<16>(sb, wn * KT::WTN + j * 16, g * 32, lane);
+#pragma unroll
+                for (int i = 0; i < KT::TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < KT::TN; ++j) mfma_step<In::I8, 16>(fa[i], fb[j], acc[i][j]);
+            }
+        }
+    }
+    i8_finish<KT>(p, sc, m0, n0, acc, lane, wave);
+    store_tile<KT, false>(p, smem, m0, n0, acc, tid, lane, wave);
+}
+
+// ------------------------------------------------------------------ launchers
+
+// What the host asks of an output type's launchers (gemm_i8_<type>.hip).
+struct I8Call {
+    Params p;             // sizes and leading dimensions of A and B in bytes
+    I8Scales s;
+    bool vec;             // operands allow 16-byte loads
+};
+
+template <Out TO>
+struct I8Inst {
+    template <class Kernel>
+    static hipError_t run(Kernel kernel, Params p, const I8Call& c, int bm, int bn, int threads, hipStream_t s)
+    {
+        I8Scales sc = c.s;
+        p.tiles_m = (int)ceil_div(p.M, bm);
+        p.tiles_n = (int)ceil_div(p.N, bn);
+        p.group_m = p.tiles_m < 8 ? p.tiles_m : 8;
+        void* args[] = {&p, &sc};
+        return hipLaunchKernel((const void*)kernel, dim3((unsigned)(p.tiles_m * p.tiles_n)), dim3(threads), args, 0, s);
+    }
+    static hipError_t launch(const I8Call& c, hipStream_t s)
+    {
+        return run(&gemm_i8_odd_kernel<TO, 128, 128, 64, 2, 4, 2>, c.p, c, 128, 128, 512, s);
+    }
+};
+
+hipError_t i8_f32(const I8Call& c, hipStream_t s);
+hipError_t i8_f16(const I8Call& c, hipStream_t s);
+hipError_t i8_bf16(const I8Call& c, hipStream_t s);
+
+}  // namespace mg

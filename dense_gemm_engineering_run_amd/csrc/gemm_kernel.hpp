@@ -61,10 +61,15 @@ namespace mg {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-enum class In : int { F32 = 0, F16 = 1, BF16 = 2 };
+// I8: 8-bit integers, k-contiguous.  The kernels that take them see pairs of
+// them as the 2-byte elements of a 16-bit operand (the layouts of the matrix
+// units agree byte for byte) and accumulate integers, whose bits stand in the
+// fp32 accumulator registers.
+enum class In : int { F32 = 0, F16 = 1, BF16 = 2, I8 = 3 };
 enum class Out : int { F32 = 0, F16 = 1, BF16 = 2 };
 
 // Kernel arguments, already canonicalised to C n-major.
@@ -97,6 +102,7 @@ struct Params {
     int strip0;           // strip kernel: first column (or row) of C that it computes
     int c_trans;          // C stored transposed: element (m, n) at n * ldc + m (no epilogue)
     int split;            // split-k configs: k-ranges per tile (partial tiles in sk_part)
+    int k_odd;            // 8-bit operands: the last of the K pairs holds one value
 };
 
 // Point A, B, C at this workgroup's batch entry.
@@ -188,6 +194,17 @@ __device__ __forceinline__ i32x4 mask_k(i32x4 v, int k0, int K)
             uint32_t m = (k0 + 2 * d < K ? 0x0000ffffu : 0u) | (k0 + 2 * d + 1 < K ? 0xffff0000u : 0u);
             v[d] = (int)((uint32_t)v[d] & m);
         }
+    }
+    return v;
+}
+
+// Masks the bytes from `valid` on (counted from the chunk's first) of a 16-byte chunk.
+__device__ __forceinline__ i32x4 mask_bytes(i32x4 v, int valid)
+{
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const int n = min(max(valid - 4 * d, 0), 4);
+        v[d] &= n == 4 ? -1 : (1 << (8 * n)) - 1;
     }
     return v;
 }
@@ -311,6 +328,8 @@ __device__ __forceinline__ void mfma_step(const i32x4& a, const i32x4& b, f32x16
     } else if constexpr (TI == In::F16) {
         acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
                                                      __builtin_bit_cast(f16x8, b), acc, 0, 0, 0);
+    } else if constexpr (TI == In::I8) {
+        acc = __builtin_bit_cast(f32x16, __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, __builtin_bit_cast(i32x16, acc), 0, 0, 0));
     } else {
         acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                       __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
@@ -328,6 +347,8 @@ __device__ __forceinline__ void mfma_step(const i32x4& a, const i32x4& b, f32x4&
     } else if constexpr (TI == In::F16) {
         acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
                                                      __builtin_bit_cast(f16x8, b), acc, 0, 0, 0);
+    } else if constexpr (TI == In::I8) {
+        acc = __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, __builtin_bit_cast(i32x4, acc), 0, 0, 0));
     } else {
         acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                       __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);

@@ -441,7 +441,7 @@ struct PingPong {
         // m-contiguous operand reads zeros there, so if both are it is a tile
         // like the others.)
         constexpr bool TAIL = AK || BKM;
-        const int nkt = TAIL ? p.K / BK : (p.K + BK - 1) / BK;
+        const int nkt = TAIL ? (TI == In::I8 ? p.K - p.k_odd : p.K) / BK : (p.K + BK - 1) / BK;
         // A wave loads one operand only; its per-lane offsets pass through an
         // empty asm so that each takes one register (the 64-bit product they
         // come from would keep two, and a spilled offset's reload waits for
@@ -545,8 +545,12 @@ struct PingPong {
             else issue_b(nkt, 0, p.b_bytes);
             wait_vmcnt<0>();
             bare_barrier();
-            LA::template zero_tail<NT>(KT::a_stage(smem, 0), left, tid);
-            LB::template zero_tail<NT>(KT::b_stage(smem, 0), left, tid);
+            if constexpr (TI == In::I8) {
+                LA::template zero_tail_bytes<NT>(KT::a_stage(smem, 0), left * 2 - p.k_odd, tid);
+            } else {
+                LA::template zero_tail<NT>(KT::a_stage(smem, 0), left, tid);
+                LB::template zero_tail<NT>(KT::b_stage(smem, 0), left, tid);
+            }
             __syncthreads();
 #pragma unroll 1
             for (int g = 0; g * KG < left; ++g) {    // rolled: the accumulators stay where they are
@@ -710,9 +714,10 @@ struct Skinny {
         for (int t = wave; t < nkt; t += NW) {
             wait_vmcnt<(ST - 1) * L>();
             char* s = ring + slot * STAGE;
-            if (t == nkt - 1 && left != BK) {
-                oa.template zero_tail<64>(s, left, lane);
-                if constexpr (BKM) ob.template zero_tail<64>(s + OA::BYTES, left, lane);
+            if (t == nkt - 1 && (left != BK || (TI == In::I8 && p.k_odd))) {
+                if constexpr (TI == In::I8) oa.template zero_tail_bytes<64>(s, left * 2 - p.k_odd, lane);
+                else oa.template zero_tail<64>(s, left, lane);
+                if constexpr (TI != In::I8 && BKM) ob.template zero_tail<64>(s + OA::BYTES, left, lane);
                 __builtin_amdgcn_s_waitcnt(0xc07f);
             }
             asm volatile("" ::: "memory");

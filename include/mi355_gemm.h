@@ -375,6 +375,92 @@ int gemm_run_lora(int64_t M, int64_t N, int64_t K, char a_major, char b_major, c
  */
 int gemm_lora_workspace_size(int64_t M, int64_t N, int64_t K, int dtype, int64_t rank, size_t* bytes);
 
+/*
+ * A linear layer in 8 bits.  A matrix is held as 8-bit integers with one fp32
+ * scale a row (a token of the activations, an output channel of the weights):
+ * row m stands for scales[m] * Q[m][k].  Rows are stored one by one with k
+ * contiguous (ldq elements apart).
+ */
+typedef enum {
+    GEMM_TYPE_F32 = 0,
+    GEMM_TYPE_F16 = 1,
+    GEMM_TYPE_BF16 = 2,
+    GEMM_NUM_TYPES = 3
+} gemm_type_t;
+
+/*
+ * Rows of X (M x K, row-major, a gemm_type_t) to 8 bits:
+ *     scales[m] = max_k |X[m][k]| / 127
+ *     Q[m][k]   = the integer nearest 127 X[m][k] / max_k |X[m][k]|, ties to even
+ * as if the quotient were exact; the scale is rounded once, to fp32 (where the
+ * maximum is below 2^-119, to an fp32 subnormal).  A row of zeros, or of no
+ * values (K == 0), has scale 0; a row that holds a NaN or an infinity has scale
+ * NaN and zeros in Q, which makes NaN of whatever it is used in.
+ *
+ * gemm_dequantize_rows: X[m][k] = scales[m] * Q[m][k], for any scales, formed in
+ * fp32 and rounded to X's type.
+ *
+ * Any alignment down to the elements' (16-byte rows of X and as many 8-bit
+ * values' alignment of Q are fastest); nothing but the rows' own elements is
+ * read or written.  What is written must not overlap what is read
+ * (GEMM_ERR_ALIAS).  An unknown type is GEMM_ERR_BAD_DTYPE; the checks, their
+ * order, asynchrony and errors are those of gemm_run, and sizes whose grid no
+ * launch can have (2^32 threads; 2^24 rows always fit) are GEMM_ERR_BAD_SHAPE
+ * after the others.
+ */
+int gemm_quantize_rows(int64_t M, int64_t K, int type, const void* X, int8_t* Q, float* scales,
+                       int64_t ldx, int64_t ldq, void* stream);
+int gemm_dequantize_rows(int64_t M, int64_t K, int type, const int8_t* Q, const float* scales, void* X,
+                         int64_t ldq, int64_t ldx, void* stream);
+
+/*
+ * The layer's output from 8-bit tokens A (M x K) and weights B (N x K):
+ *
+ *     C[m][n] = act(alpha * scale_a[m] scale_b[n] sum_k A[m][k] B[n][k] + beta * C_old[m][n] + bias[n])
+ *
+ * type is C's (a gemm_type_t).  a_major and b_major 'k', c_major 'n' (else
+ * GEMM_ERR_BAD_MAJOR).  The sum is exact (K <= 131071, where 32 bits hold any
+ * sum, -128 * -128 throughout included; else GEMM_ERR_BAD_SHAPE); it is
+ * rounded to fp32, times scale_a[m], times scale_b[n], each product rounded to
+ * fp32, then the epilogue as in gemm_run_ex.  scale_a, scale_b: device arrays
+ * of M and N fp32 values, NULL for ones; epilogue NULL: none.  K == 0 is a sum
+ * of 0.  Sizes, the checks and their order, asynchrony and errors are otherwise
+ * those of gemm_run_ex; operands that are not 16-byte aligned (any byte will
+ * do) run other kernels, and sizes whose grid no launch can have are
+ * GEMM_ERR_BAD_SHAPE.  No workspace; results do not depend on the kernel.
+ */
+int gemm_run_i8(int64_t M, int64_t N, int64_t K, char a_major, char b_major, char c_major, int type,
+                const int8_t* A, const int8_t* B, void* C, int64_t lda, int64_t ldb, int64_t ldc,
+                const float* scale_a, const float* scale_b, const gemm_epilogue_t* epilogue, void* stream);
+
+/*
+ * The layer's gradients from 8-bit checkpoints, whose scales lie along the
+ * summed index:
+ *
+ *     C[m][n] = sum_k A[m][k] * scales[k] * Q[n][k]          (+ C[m][n] when accumulate != 0)
+ *
+ * dtype is A's and C's type (a gemm_dtype_t).  Q is 8-bit, stored k by k
+ * (b_major 'n': Q[n][k] at Q + n + k*ldq), scales a device array of K fp32
+ * values; c_major 'n'; else GEMM_ERR_BAD_MAJOR.  The weights' gradient (out x
+ * in) sums over tokens: A the gradient of the outputs (tokens x out) read as
+ * a_major 'm', Q the layer's 8-bit inputs (tokens x in).  The inputs' gradient
+ * (tokens x in) sums over output channels: A the same gradient, a_major 'k', Q
+ * the 8-bit weights (out x in) with their scales.
+ *
+ * Sums are fp32.  Into 16-bit C, scales[k] * Q[n][k] enters rounded to A's
+ * type, as gemm_dequantize_rows gives it.  Into fp32 C, scales[k] * Q[n][k] (bf16
+ * A) or scales[k] * A[m][k] (fp16 and fp32 A), rounded to fp32, enters whole.
+ * An infinity or NaN in A or scales makes infinities or NaN of what it reaches
+ * (into fp32 C an infinity may come out as NaN).
+ * accumulate adds to C in fp32 before the rounding to C's type.  K == 0 writes
+ * zeros (accumulate: nothing).  Sizes, alignment, the checks and their order,
+ * asynchrony and errors are otherwise those of gemm_run.  No workspace; results
+ * are deterministic.
+ */
+int gemm_run_i8_grad(int64_t M, int64_t N, int64_t K, char a_major, char b_major, char c_major, int dtype,
+                     const void* A, const int8_t* Q, void* C, int64_t lda, int64_t ldq, int64_t ldc,
+                     const float* scales, int accumulate, void* stream);
+
 /* Static description of a status code; never NULL. */
 const char* gemm_status_str(int status);
 

@@ -11,6 +11,7 @@
 // stores.
 #pragma once
 
+#include "gemm_i8_tiles.hpp"
 #include "gemm_quant.hpp"
 #include "gemm_ragged.hpp"
 
@@ -53,6 +54,98 @@ __device__ __forceinline__ void i8_finish(const Params& p, const I8Scales& s, in
             for (int j = 0; j < KT::TN; ++j)
                 acc[i][j][q] = i8_value<KT::OUT>(p, m, n0 + KT::col(wn, j, lane), acc[i][j][q], sa, sb[j]);
         }
+}
+
+// ------------------------------------------------------------ 16-byte aligned operands
+
+// The ring of gemm_dma.hpp.
+template <Out TO, int BM, int BN, int BK, int WM, int WN, int MI, int STAGES>
+__global__ void __launch_bounds__(WM * WN * 64)
+gemm_i8_dma_kernel(Params p, I8Scales sc)
+{
+    using KT = Dma16<In::I8, TO, BM, BN, BK, WM, WN, MI, STAGES, true, true>;
+    __shared__ __attribute__((aligned(1024))) char smem[KT::SMEM];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tm, tn;
+    tile_coords(p, tm, tn);
+    const int m0 = __builtin_amdgcn_readfirstlane(tm) * BM, n0 = __builtin_amdgcn_readfirstlane(tn) * BN;
+    typename KT::OA oa;
+    typename KT::OB ob;
+    oa.init(wave, lane, p.lda);
+    ob.init(wave, lane, p.ldb);
+    typename KT::Acc acc;
+    KT::zero(acc);
+    KT::mainloop(p, smem, oa, ob, m0, n0, 0, (p.K + BK - 1) / BK, acc, tid, lane, wave);
+    i8_finish<KT>(p, sc, m0, n0, acc, lane, wave);
+    store_tile<KT, false>(p, smem, m0, n0, acc, tid, lane, wave);
+}
+
+// The ping-pong schedule (PingPong), whose accumulators run along C's rows.
+template <Out TO, int BM, int BN, int BK, int WM, int WN, int MI>
+__global__ void __launch_bounds__(WM * WN * 64)
+gemm_i8_pp_kernel(Params p, I8Scales sc)
+{
+    using PP = PingPong<In::I8, TO, BM, BN, BK, WM, WN, MI, true, true, true>;
+    using KT = typename PP::KT;
+    __shared__ __attribute__((aligned(1024))) char smem[KT::SMEM];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tm, tn;
+    tile_coords(p, tm, tn);
+    const int m0 = __builtin_amdgcn_readfirstlane(tm) * BM, n0 = __builtin_amdgcn_readfirstlane(tn) * BN;
+    typename KT::Acc acc;
+    KT::zero(acc);
+    PP::mainloop(p, smem, m0, n0, acc, tid, lane, wave);
+    const int mb = m0 + wave / WN * KT::WTM + lane % MI, nb = n0 + wave % WN * KT::WTN + lane / MI * 4;
+    float sa[KT::TM];
+#pragma unroll
+    for (int i = 0; i < KT::TM; ++i) sa[i] = sc.a && mb + i * MI < p.M ? sc.a[mb + i * MI] : 1.f;
+#pragma unroll
+    for (int j = 0; j < KT::TN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int n = nb + j * MI + e;
+            const float sb = sc.b && n < p.N ? sc.b[n] : 1.f;
+#pragma unroll
+            for (int i = 0; i < KT::TM; ++i) acc[i][j][e] = i8_value<TO>(p, mb + i * MI, n, acc[i][j][e], sa[i], sb);
+        }
+    PP::store(p, smem, m0, n0, acc, lane, wave);
+}
+
+// Few rows: Skinny's streams, whose waves take the k-tiles in turn; their
+// integer sums meet in LDS.
+template <Out TO, int MT, int NT, int NW, int ST>
+__global__ void __launch_bounds__(NW * 64)
+gemm_i8_stream_kernel(Params p, I8Scales sc)
+{
+    using T = Skinny<In::I8, MT, NT, NW, ST, true, true>;
+    static_assert(T::RING <= 160 * 1024 && NW * T::PART * 4 <= T::RING, "LDS budget");
+    __shared__ __attribute__((aligned(1024))) char smem[T::RING];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tm, tn;
+    tile_coords(p, tm, tn);
+    const int m0 = __builtin_amdgcn_readfirstlane(tm) * (MT * 16), n0 = __builtin_amdgcn_readfirstlane(tn) * (NT * 16);
+    typename T::Acc acc;
+    T::zero(acc);
+    T::stream(p, smem, m0, n0, acc, lane, wave);
+    __syncthreads();
+    int* const part = (int*)smem;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                part[wave * T::PART + (i * 16 + lane / 16 * 4 + e) * (NT * 16) + j * 16 + lane % 16] = __float_as_int(acc[i][j][e]);
+    __syncthreads();
+    for (int x = tid; x < T::PART; x += NW * 64) {
+        const int m = m0 + x / (NT * 16), n = n0 + x % (NT * 16);
+        if (m >= p.M || n >= p.N) continue;
+        int v = part[x];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) v += part[w * T::PART + x];
+        store_out<TO>(p.C, (int64_t)m * p.ldc + n,
+                      i8_value<TO>(p, m, n, __int_as_float(v), sc.a ? sc.a[m] : 1.f, sc.b ? sc.b[n] : 1.f));
+    }
 }
 
 // ------------------------------------------------------------ operands at any byte
@@ -186,21 +279,63 @@ struct I8Call {
     bool vec;             // operands allow 16-byte loads
 };
 
+inline I8Shape shape_of(const I8Call& c) { return {c.vec, c.p.M, c.p.N, c.p.K}; }
+
 template <Out TO>
 struct I8Inst {
     template <class Kernel>
-    static hipError_t run(Kernel kernel, Params p, const I8Call& c, int bm, int bn, int threads, hipStream_t s)
+    static hipError_t run(Kernel kernel, const I8Call& c, const Tile& t, hipStream_t s)
     {
+        Params p = c.p;
         I8Scales sc = c.s;
-        p.tiles_m = (int)ceil_div(p.M, bm);
-        p.tiles_n = (int)ceil_div(p.N, bn);
+        if (c.vec) {                  // pairs of values
+            p.k_odd = p.K & 1;
+            p.K = (p.K + 1) / 2;
+            p.lda /= 2;
+            p.ldb /= 2;
+        }
+        p.tiles_m = (int)ceil_div(p.M, t.bm);
+        p.tiles_n = (int)ceil_div(p.N, t.bn);
         p.group_m = p.tiles_m < 8 ? p.tiles_m : 8;
         void* args[] = {&p, &sc};
-        return hipLaunchKernel((const void*)kernel, dim3((unsigned)(p.tiles_m * p.tiles_n)), dim3(threads), args, 0, s);
+        return hipLaunchKernel((const void*)kernel, dim3((unsigned)i8_grid(shape_of(c), t)), dim3(t.threads), args, 0, s);
+    }
+    template <I8Tile T>
+    static hipError_t stream(const I8Call& c, hipStream_t s)
+    {
+        constexpr Tile t = tile_of(T);
+        return run(&gemm_i8_stream_kernel<TO, t.wm, t.wn, t.extra, t.stages>, c, t, s);
+    }
+    template <I8Tile T>
+    static hipError_t dma(const I8Call& c, hipStream_t s)
+    {
+        constexpr Tile t = tile_of(T);
+        return run(&gemm_i8_dma_kernel<TO, t.bm, t.bn, t.bk, t.wm, t.wn, t.mi, t.stages>, c, t, s);
+    }
+    template <I8Tile T>
+    static hipError_t odd(const I8Call& c, hipStream_t s)
+    {
+        constexpr Tile t = tile_of(T);
+        return run(&gemm_i8_odd_kernel<TO, t.bm, t.bn, t.bk, t.wm, t.wn, t.stages>, c, t, s);
     }
     static hipError_t launch(const I8Call& c, hipStream_t s)
     {
-        return run(&gemm_i8_odd_kernel<TO, 128, 128, 64, 2, 4, 2>, c.p, c, 128, 128, 512, s);
+        constexpr Tile pp = tile_of(I8Tile::PingPong);
+        switch (i8_tile(shape_of(c))) {
+        case I8Tile::Stream16x16: return stream<I8Tile::Stream16x16>(c, s);
+        case I8Tile::Stream16x32: return stream<I8Tile::Stream16x32>(c, s);
+        case I8Tile::Stream32x32: return stream<I8Tile::Stream32x32>(c, s);
+        case I8Tile::Dma32x64: return dma<I8Tile::Dma32x64>(c, s);
+        case I8Tile::Dma64x64: return dma<I8Tile::Dma64x64>(c, s);
+        case I8Tile::Dma64x128: return dma<I8Tile::Dma64x128>(c, s);
+        case I8Tile::Dma128x128: return dma<I8Tile::Dma128x128>(c, s);
+        case I8Tile::Dma128x256: return dma<I8Tile::Dma128x256>(c, s);
+        case I8Tile::PingPong: return run(&gemm_i8_pp_kernel<TO, pp.bm, pp.bn, pp.bk, pp.wm, pp.wn, pp.mi>, c, pp, s);
+        case I8Tile::Odd32x32: return odd<I8Tile::Odd32x32>(c, s);
+        case I8Tile::Odd64x64: return odd<I8Tile::Odd64x64>(c, s);
+        case I8Tile::Odd128x128: return odd<I8Tile::Odd128x128>(c, s);
+        default: return hipErrorInvalidValue;
+        }
     }
 };
 

@@ -91,7 +91,9 @@ int run(int64_t M, int64_t N, int64_t K, char a, char b, char c, int type, const
     }
     q.s = mg::I8Scales{scale_a, scale_b};
     q.vec = vec;
-    if (mg::ceil_div(M, 128) * mg::ceil_div(N, 128) > mg::kMaxGridThreads / 512) return GEMM_ERR_BAD_SHAPE;
+    const mg::I8Shape shape = mg::shape_of(q);
+    const mg::Tile& tile = mg::kI8Tiles[(int)mg::i8_tile(shape)];
+    if (mg::i8_grid(shape, tile) > mg::kMaxGridThreads / tile.threads) return GEMM_ERR_BAD_SHAPE;
     const int st = kLaunch[type](q, (hipStream_t)stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
     if (mg::log_enabled())
         std::fprintf(stderr, "mi355_gemm: i8 %s M=%lld N=%lld K=%lld %s\n", kTypeNames[type], (long long)M, (long long)N,
@@ -134,7 +136,9 @@ int run_grad(int64_t M, int64_t N, int64_t K, char a, char b, char c, int dtype,
     q.g.scales = scales;
     q.a_kmajor = a == 'k';
     q.vec = vec;
-    if (mg::ceil_div(M, 64) * mg::ceil_div(N, 64) > mg::kMaxGridThreads / 256) return GEMM_ERR_BAD_SHAPE;
+    const mg::GradShape shape = mg::shape_of(q, eo == 4, eo == 4 && dtype != GEMM_DTYPE_BF16_F32);
+    const mg::Tile& tile = mg::kGradTiles[(int)mg::grad_tile(shape)];
+    if (mg::grad_grid(shape, tile) > mg::kMaxGridThreads / tile.threads) return GEMM_ERR_BAD_SHAPE;
     const int st = kGradLaunch[dtype](q, (hipStream_t)stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
     if (mg::log_enabled())
         std::fprintf(stderr, "mi355_gemm: i8_grad %s M=%lld N=%lld K=%lld a=%c %s\n", mg::dtype_name(dtype), (long long)M,

@@ -1,0 +1,119 @@
+// gemm_i8_tiles.hpp -- which kernel a product of 8-bit values runs, and the size
+// of its grid (host only; no HIP).
+#pragma once
+
+#include "gemm_tiles.hpp"
+
+namespace mg {
+
+// bk counts pairs of 8-bit values.
+enum class I8Tile : int {
+    Stream16x16, Stream16x32, Stream32x32, Dma32x64, Dma64x64, Dma64x128, Dma128x128, Dma128x256, PingPong,
+    Odd32x32, Odd64x64, Odd128x128,
+    Count
+};
+constexpr Tile kI8Tiles[] = {
+    {"stream 16x16", 16, 16, 0, 1, 1, 16, 4, 8, 512},
+    {"stream 16x32", 16, 32, 0, 1, 2, 16, 3, 8, 512},
+    {"stream 32x32", 32, 32, 0, 2, 2, 16, 2, 8, 512},
+    {"32x64", 32, 64, 128, 1, 4, 16, 3, 0, 256},
+    {"64x64", 64, 64, 128, 2, 4, 16, 3, 0, 512},
+    {"64x128", 64, 128, 64, 2, 4, 16, 4, 0, 512},
+    {"128x128", 128, 128, 64, 2, 4, 16, 4, 0, 512},
+    {"128x256", 128, 256, 64, 2, 4, 16, 3, 0, 512},
+    {"ping-pong 256x256", 256, 256, 64, 4, 2, 16, 3, 0, 512},
+    {"unaligned 32x32", 32, 32, 128, 2, 2, 16, 2, 0, 256},
+    {"unaligned 64x64", 64, 64, 64, 2, 4, 16, 2, 0, 512},
+    {"unaligned 128x128", 128, 128, 64, 2, 4, 16, 2, 0, 512},
+};
+static_assert(sizeof(kI8Tiles) / sizeof(Tile) == (int)I8Tile::Count, "one entry a tile");
+constexpr Tile tile_of(I8Tile t) { return kI8Tiles[(int)t]; }
+
+struct I8Shape {
+    bool vec;             // A and B allow 16-byte loads
+    int64_t M, N, K;
+};
+
+// The smallest tile that makes no more than one for each of the 256 CUs, else
+// the largest.  us, bf16 outputs, N = K = 4096 unless given:
+//   rows               16x16  16x32  32x32  32x64  64x64  64x128 128x128 128x256 256x256
+//      1                 6.0    6.1    6.3    8.9   10.2
+//     16                 6.2    6.3    6.5    9.1
+//     32                        6.5    7.1    9.3   10.7
+//     64                               7.4    9.3   10.8   14.7
+//     64  N 8192 K 2048                9.9    7.1    7.9    9.8
+//    128                                     10.0   11.1   14.8   20.4
+//    256                                     13.8   12.5   15.6   20.7    31.0
+//   1000  N 1024 K 2048                       9.2    8.3   10.1   13.8    19.6    27.0
+//    512                                            23.7   18.4   22.9    32.0    45.3
+//   1024                                                   33.9   25.9    34.4    45.9
+//   2048                                                          47.3    39.6    48.0
+//   8192  K 1024                                                          56.0    53.4
+//   8192                                                                 147.7   125.3
+// (The first three stream: the waves share a tile's k.)
+// Unaligned: 32x32 / 64x64 / 128x128 took 14.2 / 25.7 / 35.4 for one row of 4095
+// x 4095, 10.9 / 15.3 / 23.8 for 300 of 1023 x 2047, - / 44.8 / 38.2 for 4095 of
+// 2049 x 1028.
+inline I8Tile i8_tile(const I8Shape& s)
+{
+    auto tiles = [&](int bm, int bn) { return ceil_div(s.M, bm) * ceil_div(s.N, bn); };
+    if (!s.vec) {
+        if (tiles(32, 32) <= 512) return I8Tile::Odd32x32;
+        return tiles(64, 64) <= 512 ? I8Tile::Odd64x64 : I8Tile::Odd128x128;
+    }
+    if (tiles(16, 16) <= 256) return I8Tile::Stream16x16;
+    if (tiles(16, 32) <= 256) return I8Tile::Stream16x32;
+    if (tiles(32, 32) <= 256) return I8Tile::Stream32x32;
+    if (tiles(32, 64) <= 256) return I8Tile::Dma32x64;
+    if (tiles(64, 64) <= 256) return I8Tile::Dma64x64;
+    if (tiles(64, 128) <= 256) return I8Tile::Dma64x128;
+    if (tiles(128, 128) <= 256) return I8Tile::Dma128x128;
+    return tiles(128, 256) <= 256 ? I8Tile::Dma128x256 : I8Tile::PingPong;
+}
+
+inline int64_t i8_grid(const I8Shape& s, const Tile& t) { return ceil_div(s.M, t.bm) * ceil_div(s.N, t.bn); }
+
+// ------------------------------------------------------------ gradients from 8-bit values
+
+// bk: k of a tile; stages: tiles of loads in flight (streaming: a wave's);
+// extra: waves that stream, else waves a SIMD that the registers leave room for.
+enum class GradTile : int {
+    Stream32x32, Stream32x64, T64x64, T64x128, T128x128Deep, T128x128, T256x256, Tall256x128, Wide128x256, Count
+};
+constexpr Tile kGradTiles[] = {
+    {"stream 32x32", 32, 32, 64, 1, 1, 16, 2, 8, 512},
+    {"stream 32x64", 32, 64, 32, 1, 1, 16, 2, 8, 512},
+    {"64x64", 64, 64, 128, 2, 4, 16, 2, 2, 512},
+    {"64x128", 64, 128, 64, 2, 4, 16, 2, 2, 512},
+    {"128x128, 64 deep", 128, 128, 64, 2, 4, 16, 2, 2, 512},
+    {"128x128", 128, 128, 32, 2, 4, 16, 2, 2, 512},
+    {"256x256", 256, 256, 32, 4, 2, 16, 2, 2, 512},
+    {"256x128", 256, 128, 64, 4, 4, 16, 1, 4, 1024},
+    {"128x256", 128, 256, 64, 4, 4, 16, 1, 4, 1024},
+};
+static_assert(sizeof(kGradTiles) / sizeof(Tile) == (int)GradTile::Count, "one entry a tile");
+constexpr Tile tile_of(GradTile t) { return kGradTiles[(int)t]; }
+
+struct GradShape {
+    bool vec;             // A and Q allow 16-byte loads
+    bool wide;            // fp32 C: three MFMAs a product
+    bool split_a;         // ... of A's terms (else of Q's)
+    int64_t M, N, K;
+};
+
+inline GradTile grad_tile(const GradShape& s)
+{
+    auto tiles = [&](int bm, int bn) { return ceil_div(s.M, bm) * ceil_div(s.N, bn); };
+    if (tiles(32, 32) <= 256) return GradTile::Stream32x32;
+    if (tiles(32, 64) <= 256) return GradTile::Stream32x64;
+    if (tiles(64, 64) <= 256) return GradTile::T64x64;
+    if (tiles(64, 128) <= 384) return GradTile::T64x128;
+    if (!s.vec) return GradTile::T128x128;
+    if (tiles(128, 128) <= 256) return GradTile::T128x128Deep;
+    if (s.wide) return tiles(256, 128) < 384 ? GradTile::T128x128 : s.split_a ? GradTile::Wide128x256 : GradTile::Tall256x128;
+    return tiles(256, 256) < 192 ? GradTile::T128x128 : GradTile::T256x256;
+}
+
+inline int64_t grad_grid(const GradShape& s, const Tile& t) { return ceil_div(s.M, t.bm) * ceil_div(s.N, t.bn); }
+
+}  // namespace mg

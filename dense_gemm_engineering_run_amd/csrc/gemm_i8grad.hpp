@@ -17,6 +17,7 @@
 //     fp32 ones.
 #pragma once
 
+#include "gemm_i8_tiles.hpp"
 #include "gemm_quant.hpp"
 #include "gemm_ragged.hpp"
 
@@ -40,13 +41,22 @@ struct GradTypes {
 template <In T>
 __device__ __forceinline__ void split8(float (&v)[8], i32x4 (&t)[1])
 {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-    for (int d = 0; d < 4; ++d) t[0][d] = (int)((uint32_t)round16<T>(v[2 * d]) | ((uint32_t)round16<T>(v[2 * d + 1]) << 16));
+    for (int d = 0; d < 4; ++d) {
+        const f32x2 x = {v[2 * d], v[2 * d + 1]};
+        if constexpr (T == In::F16) {
+            typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+            t[0][d] = __builtin_bit_cast(int, __builtin_convertvector(x, f16x2));
+        } else {
+            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+            t[0][d] = __builtin_bit_cast(int, __builtin_convertvector(x, bf16x2));
+        }
+    }
 }
 
 // The same in three bf16 terms by cutting off: 8 of the 24 bits each, nothing
-// is left.  An infinity stays one in the first term (NaN, whose cut-off bits
-// may be an infinity's, leaves NaN behind).
+// is left (of an infinity, NaN).
 template <In T>
 __device__ __forceinline__ void split8(float (&v)[8], i32x4 (&t)[3])
 {
@@ -61,17 +71,28 @@ __device__ __forceinline__ void split8(float (&v)[8], i32x4 (&t)[3])
             }
             t[s][d] = (int)__builtin_amdgcn_perm((uint32_t)__float_as_int(v[2 * d + 1]), (uint32_t)__float_as_int(v[2 * d]),
                                                  0x07060302u);
-            if (s < 2)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float& x = v[2 * d + e];
-                    const float f = __int_as_float(__float_as_int(x) & (int)0xffff0000);
-                    x = s == 0 && x == f ? 0.f : x - f;
-                }
+            if (s < 2) {
+                v[2 * d] -= __int_as_float(__float_as_int(v[2 * d]) & (int)0xffff0000);
+                v[2 * d + 1] -= __int_as_float(__float_as_int(v[2 * d + 1]) & (int)0xffff0000);
+            }
         }
 }
 
-// Eight bytes from any byte of a row: three words, shifted.
+// The resource of what is left of an operand from `origin` on, an element of
+// it; not live: of nothing.  Scalar throughout (64-bit comparisons are not).
+// ALIGN: from the word that holds the first byte to the end of the last one.
+template <bool ALIGN>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rest(const char* base, uint64_t bytes, int64_t origin, bool live)
+{
+    const uint64_t at = (uint64_t)base + (uint64_t)origin, lead = ALIGN ? at & 3 : 0;
+    uint64_t n = bytes - (uint64_t)origin + lead;
+    if (ALIGN) n = (n + 3) & ~(uint64_t)3;
+    const uint32_t lo = (uint32_t)(n >> 32) != 0 ? 0xffffffffu : (uint32_t)n;
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(at - lead), (short)0, live ? (int)lo : 0, kBufferFlags);
+}
+
+// Eight bytes of a row: from any byte (three words, shifted), or 8-byte aligned.
+template <bool VEC>
 struct ByteChunk8 {
     int w0, w1, w2;
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int off)     // off: from the first word
@@ -89,16 +110,37 @@ struct ByteChunk8 {
         hi = (int)__builtin_amdgcn_alignbit((uint32_t)w2, (uint32_t)w1, sh);
     }
 };
+template <>
+struct ByteChunk8<true> {
+    i32x2 w;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int off) { w = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0); }
+    __device__ __forceinline__ void get(int, int& lo, int& hi) const
+    {
+        lo = w[0];
+        hi = w[1];
+    }
+};
+// Sixteen bytes of 16-bit values likewise.
+template <bool VEC>
+struct HalfChunk : OddChunk {
+};
+template <>
+struct HalfChunk<true> {
+    i32x4 v;
+    __device__ __forceinline__ void load(const OddRows& s, int off) { v = buf_load16(s.r, off); }
+    __device__ __forceinline__ i32x4 get(int, int) const { return v; }
+};
 
-// One operand's k-tile in LDS: TERMS tiles in DmaOperand's layout.
+// The operands: k-tiles from memory to registers, D tiles ahead, and from there
+// to LDS as DmaOperand lays them out, a tile a term.
 
 // Q: k rows of ROWS bytes to [BK][ROWS] values, exact or times scales[k].
-template <In MT, int ROWS, int BK, int NW, int TERMS, bool SCALED>
+template <In MT, int ROWS, int BK, int NW, int TERMS, bool SCALED, bool VEC, int D>
 struct QOperand {
     using LDS = DmaOperand<ROWS, BK, NW, false, 16>;
     int voff[LDS::IPW];
-    ByteChunk8 q[LDS::IPW];
-    float s[LDS::IPW];
+    ByteChunk8<VEC> q[D][LDS::IPW];
+    float s[D][LDS::IPW];
 
     __device__ static __forceinline__ int slot(int wave, int lane, int j) { return (wave * LDS::IPW + j) * 64 + lane; }
     __device__ __forceinline__ void init(int wave, int lane, int64_t ld)
@@ -110,36 +152,36 @@ struct QOperand {
         }
     }
     // Rows from K on lie past the extent and read as zeros, scale included.
-    __device__ __forceinline__ void load(const GradParams& g, uint64_t bytes, int row0, int k0, int wave, int lane)
+    __device__ __forceinline__ void load(int d, const GradParams& g, int row0, int k0, int wave, int lane)
     {
+        const bool live = k0 < g.p.K;
         const int64_t origin = (int64_t)k0 * g.p.ldb + row0;
-        const char* const at = g.p.B + origin;
-        const int lead = (int)((uint64_t)at & 3);
-        const uint64_t rem = (uint64_t)origin < bytes ? bytes - (uint64_t)origin : 0;
-        const __amdgpu_buffer_rsrc_t r = make_rsrc(at - lead, rem ? (rem + lead + 3) / 4 * 4 : 0);
+        const int lead = VEC ? 0 : (int)((uint64_t)(g.p.B + origin) & 3);
+        const __amdgpu_buffer_rsrc_t r = rest<!VEC>(g.p.B, g.p.b_bytes, origin, live);
+        const __amdgpu_buffer_rsrc_t rs = rest<false>((const char*)g.scales, (uint64_t)g.p.K * 4, (int64_t)k0 * 4, live);
 #pragma unroll
         for (int j = 0; j < LDS::IPW; ++j) {
-            q[j].load(r, voff[j] + lead);
-            if constexpr (SCALED) {
-                const int k = k0 + slot(wave, lane, j) / LDS::RCH;
-                s[j] = k < g.p.K ? g.scales[k] : 0.f;
-            }
+            q[d][j].load(r, voff[j] + lead);
+            if constexpr (SCALED)
+                s[d][j] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, slot(wave, lane, j) / LDS::RCH * 4, 0, 0));
         }
     }
-    __device__ __forceinline__ void store(const GradParams& g, char* tile, int row0, int k0, int wave, int lane) const
+    __device__ __forceinline__ void store(int d, const GradParams& g, char* tile, int row0, int k0, int wave, int lane) const
     {
-        const int lead = (int)((uint64_t)(g.p.B + (int64_t)k0 * g.p.ldb + row0) & 3);
+        const int lead = VEC ? 0 : (int)((uint64_t)(g.p.B + (int64_t)k0 * g.p.ldb + row0) & 3);
 #pragma unroll
         for (int j = 0; j < LDS::IPW; ++j) {
             int w[2];
-            q[j].get(voff[j] + lead, w[0], w[1]);
-            // The words at the last row's end can hold bytes of what follows it: k from K on is zeros.
-            const bool live = k0 + slot(wave, lane, j) / LDS::RCH < g.p.K;
+            q[d][j].get(voff[j] + lead, w[0], w[1]);
+            if constexpr (!VEC) {
+                // The words at the last row's end can hold bytes of what follows it.
+                if (k0 + slot(wave, lane, j) / LDS::RCH >= g.p.K) w[0] = w[1] = 0;
+            }
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                v[e] = live ? byte_value(w[e / 4], e % 4) : 0.f;
-                if constexpr (SCALED) v[e] *= s[j];
+                v[e] = byte_value(w[e / 4], e % 4);
+                if constexpr (SCALED) v[e] *= s[d][j];
             }
             i32x4 t[TERMS];
             split8<MT>(v, t);
@@ -149,31 +191,17 @@ struct QOperand {
     }
 };
 
-// 16-bit A as it is.
-template <In TI, int ROWS, int BK, int NW, bool KMAJ, bool SPLIT>
+// A: 16-bit values as they are, or (SPLIT) fp16 and fp32 ones times scales[k] in
+// three bf16 terms.
+template <In TI, int ROWS, int BK, int NW, bool KMAJ, bool SPLIT, bool VEC, int D>
 struct AOperand {
-    OddOperand<ROWS, BK, NW, KMAJ, 1> o;
-    __device__ __forceinline__ void init(int wave, int lane, int64_t ld) { o.at.init(wave, lane, ld); }
-    __device__ __forceinline__ void load(const GradParams& g, uint64_t bytes, int row0, int k0, int, int)
-    {
-        o.load(0, g.p.A, bytes, g.p.lda, row0, k0);
-    }
-    __device__ __forceinline__ void store(const GradParams& g, char* tile, int k0, int wave, int lane) const
-    {
-        o.store(0, tile, g.p.A, k0, g.p.K, wave, lane);
-    }
-};
-
-// fp16 or fp32 A times scales[k], in three bf16 terms.
-template <In TI, int ROWS, int BK, int NW, bool KMAJ>
-struct AOperand<TI, ROWS, BK, NW, KMAJ, true> {
     using LDS = DmaOperand<ROWS, BK, NW, KMAJ, 16>;
     static constexpr bool WIDE = TI == In::F32;
-    static constexpr int ES = WIDE ? 4 : 2;
+    static constexpr int ES = WIDE ? 4 : 2, NS = !SPLIT ? 0 : KMAJ ? 8 : 1;
     int voff[LDS::IPW];
-    i32x4 wide[WIDE ? LDS::IPW : 1][2];
-    OddChunk half[WIDE ? 1 : LDS::IPW];
-    float s[LDS::IPW][KMAJ ? 8 : 1];
+    i32x4 wide[WIDE ? D : 1][WIDE ? LDS::IPW : 1][2];
+    HalfChunk<VEC> half[WIDE ? 1 : D][WIDE ? 1 : LDS::IPW];
+    float s[SPLIT ? D : 1][LDS::IPW][NS ? NS : 1];
 
     // k of a slot's first value within the tile.
     __device__ static __forceinline__ int k_of(int slot)
@@ -190,63 +218,89 @@ struct AOperand<TI, ROWS, BK, NW, KMAJ, true> {
             voff[j] = (int)((KMAJ ? slot / LDS::CPR : slot / LDS::RCH) * ld * ES) + o.voff[j] * (ES / 2);
         }
     }
-    __device__ __forceinline__ void load(const GradParams& g, uint64_t bytes, int row0, int k0, int wave, int lane)
+    __device__ __forceinline__ void load(int d, const GradParams& g, int row0, int k0, int wave, int lane)
     {
+        const bool live = k0 < g.p.K;
         const int64_t origin = (KMAJ ? (int64_t)row0 * g.p.lda + k0 : (int64_t)k0 * g.p.lda + row0) * ES;
-        const uint64_t rem = (uint64_t)origin < bytes ? bytes - (uint64_t)origin : 0;
-        const __amdgpu_buffer_rsrc_t r = make_rsrc(g.p.A + origin, rem);
-        const OddRows odd(g.p.A + origin, rem);
+        OddRows r;
+        r.r = rest<!VEC && !WIDE>(g.p.A, g.p.a_bytes, origin, live);
+        r.lead = (int)((uint64_t)g.p.A & 2);              // (every tile's first element lies in its word as A's)
+        const __amdgpu_buffer_rsrc_t rs = rest<false>((const char*)g.scales, (uint64_t)g.p.K * 4, (int64_t)k0 * 4, live);
 #pragma unroll
         for (int j = 0; j < LDS::IPW; ++j) {
             if constexpr (WIDE) {
-                wide[j][0] = buf_load16(r, voff[j]);
-                wide[j][1] = buf_load16(r, voff[j] + 16);
+                wide[d][j][0] = buf_load16(r.r, voff[j]);
+                wide[d][j][1] = buf_load16(r.r, voff[j] + 16);
             } else {
-                half[j].load(odd, voff[j]);
+                half[d][j].load(r, voff[j]);
             }
-            const int k = k0 + k_of((wave * LDS::IPW + j) * 64 + lane);
+            const int k = k_of((wave * LDS::IPW + j) * 64 + lane);
+            if constexpr (NS == 1) {
+                s[d][j][0] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, k * 4, 0, 0));
+            } else if constexpr (NS == 8) {       // (scales are 4-byte aligned: k is a multiple of 8)
 #pragma unroll
-            for (int e = 0; e < (KMAJ ? 8 : 1); ++e) s[j][e] = k + e < g.p.K ? g.scales[k + e] : 0.f;
+                for (int h = 0; h < 2; ++h) {
+                    const i32x4 v = buf_load16(rs, k * 4 + h * 16);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[d][j][h * 4 + e] = __int_as_float(v[e]);
+                }
+            }
         }
     }
-    __device__ __forceinline__ void store(const GradParams& g, char* tile, int k0, int wave, int lane) const
+    __device__ __forceinline__ void store(int d, const GradParams& g, char* tile, int k0, int wave, int lane) const
     {
-        const int lead = (int)((uint64_t)g.p.A & 2);      // (every tile's first element lies in its word as A's)
+        const int lead = (int)((uint64_t)g.p.A & 2);
+        // What lies past K may be anything, but for whole rows past the extent.
+        const bool part = (KMAJ || !VEC) && k0 + BK > g.p.K;
 #pragma unroll
         for (int j = 0; j < LDS::IPW; ++j) {
-            const int slot = (wave * LDS::IPW + j) * 64 + lane, k = k0 + k_of(slot);
-            float v[8];
-            if constexpr (WIDE) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = __int_as_float(wide[j][e / 4][e % 4]);
+            const int slot = (wave * LDS::IPW + j) * 64 + lane, left = g.p.K - k0 - k_of(slot);
+            if constexpr (!SPLIT) {
+                i32x4 v = half[d][j].get(lead, voff[j]);
+                if (part) {
+                    asm volatile("");
+                    if constexpr (KMAJ) v = mask_k<In::F16>(v, 0, left);
+                    else v = left > 0 ? v : i32x4{0, 0, 0, 0};
+                }
+                *(i32x4*)(tile + slot * 16) = v;
             } else {
-                QuantType<In::F16>::unpack(half[j].get(lead, voff[j]), v);
-            }
+                float v[8];
+                if constexpr (WIDE) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[e] *= s[j][KMAJ ? e : 0];
-                if (k + (KMAJ ? e : 0) >= g.p.K) v[e] = 0.f;       // past K may stand anything
-            }
-            i32x4 t[3];
-            split8<In::BF16>(v, t);
+                    for (int e = 0; e < 8; ++e) v[e] = __int_as_float(wide[d][j][e / 4][e % 4]);
+                } else {
+                    QuantType<In::F16>::unpack(half[d][j].get(lead, voff[j]), v);
+                }
 #pragma unroll
-            for (int x = 0; x < 3; ++x) *(i32x4*)(tile + x * LDS::BYTES + slot * 16) = t[x];
+                for (int e = 0; e < 8; ++e) v[e] *= s[d][j][KMAJ ? e : 0];
+                if (part) {
+                    asm volatile("");
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if ((KMAJ ? e : 0) >= left) v[e] = 0.f;
+                }
+                i32x4 t[3];
+                split8<In::BF16>(v, t);
+#pragma unroll
+                for (int x = 0; x < 3; ++x) *(i32x4*)(tile + x * LDS::BYTES + slot * 16) = t[x];
+            }
         }
     }
 };
 
-// Operands at any element (Q: any byte) through registers: LDS in two stages,
-// a tile of loads in flight, one barrier a tile.  EPI: added to C.
-template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, bool AK, bool EPI>
-__global__ void __launch_bounds__(WM * WN * 64)
-gemm_i8grad_odd_kernel(GradParams g)
+// LDS in two stages, D tiles of loads in flight; while a tile is multiplied the
+// next one is scaled, converted and written.  VEC: 16-byte aligned A, 8-byte
+// aligned Q; else any element and byte.  EPI: added to C.
+template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, int D, int OCC, bool AK, bool VEC, bool EPI>
+__global__ void __launch_bounds__(WM * WN * 64, OCC)
+gemm_i8grad_kernel(GradParams g)
 {
     using GT = GradTypes<TI, TO>;
     constexpr In MT = GT::MT;
     constexpr int TA = GT::TA, TQ = GT::TQ, NW = WM * WN;
     using KT = Dma16<MT, TO, BM, BN, BK, WM, WN, 16, 2, AK, false>;
-    using OA = AOperand<TI, BM, BK, NW, AK, GT::SPLIT_A>;
-    using OQ = QOperand<MT, BN, BK, NW, TQ, !GT::SPLIT_A>;
+    using OA = AOperand<TI, BM, BK, NW, AK, GT::SPLIT_A, VEC, D>;
+    using OQ = QOperand<MT, BN, BK, NW, TQ, !GT::SPLIT_A, VEC, D>;
     constexpr int STAGE = TA * KT::OA::BYTES + TQ * KT::OB::BYTES, SMEM = 2 * STAGE;
     static_assert(SMEM <= 160 * 1024 && SMEM >= KT::SMEM, "LDS budget");
     __shared__ __attribute__((aligned(1024))) char smem[SMEM];
@@ -263,44 +317,172 @@ gemm_i8grad_odd_kernel(GradParams g)
     OQ oq;
     oa.init(wave, lane, p.lda);
     oq.init(wave, lane, p.ldb);
-    auto load = [&](int t) {                      // past the end: empty extents
-        oa.load(g, t < nkt ? p.a_bytes : 0, m0, t * BK, wave, lane);
-        oq.load(g, t < nkt ? p.b_bytes : 0, n0, t * BK, wave, lane);
+    auto load = [&](int t, int d) {               // past the end: empty extents
+        oa.load(d, g, m0, t * BK, wave, lane);
+        oq.load(d, g, n0, t * BK, wave, lane);
     };
-    load(0);
-    for (int t = 0; t < nkt; ++t) {
-        char* const sa = smem + t % 2 * STAGE;
-        char* const sq = sa + TA * KT::OA::BYTES;
-        oa.store(g, sa, t * BK, wave, lane);
-        oq.store(g, sq, n0, t * BK, wave, lane);
-        load(t + 1);
-        // The other stage is written after the next barrier, when every wave
-        // has read it.
-        __builtin_amdgcn_s_waitcnt(0xc07f);       // lgkmcnt(0)
-        bare_barrier();
+    auto store = [&](int t, int d, char* sa) {
+        oa.store(d, g, sa, t * BK, wave, lane);
+        oq.store(d, g, sa + TA * KT::OA::BYTES, n0, t * BK, wave, lane);
+    };
 #pragma unroll
-        for (int x = 0; x < KT::NG; ++x) {
-            i32x4 fa[TA][KT::TM], fq[TQ][KT::TN];
+    for (int d = 0; d < D; ++d) load(d, d);
+    store(0, 0, smem);
+    load(D, 0);
+    __builtin_amdgcn_s_waitcnt(0xc07f);           // lgkmcnt(0)
+    bare_barrier();
+    // The loop twice: half the waves convert the next tile first and multiply
+    // then, the others (which share the SIMDs with them) the other way round.
+    auto loop = [&](auto early) {
+        for (int t0 = 0; t0 < nkt; t0 += D) {
 #pragma unroll
-            for (int s = 0; s < TA; ++s)
+            for (int d = 0; d < D; ++d) {
+                const int t = t0 + d;
+                if (t >= nkt) break;
+                const int stage = D == 1 ? t & 1 : d % 2;
+                const char* const sa = smem + stage * STAGE;
+                const char* const sq = sa + TA * KT::OA::BYTES;
+                // The next k-group's fragments ahead, where registers hold both.
+                constexpr bool AHEAD = KT::TM * KT::TN * 4 + 8 * (TA * KT::TM + TQ * KT::TN) <= 200;
+                constexpr int F = AHEAD ? 2 : 1;
+                i32x4 fa[F][TA][KT::TM], fq[F][TQ][KT::TN];
+                auto read = [&](int x) {
 #pragma unroll
-                for (int i = 0; i < KT::TM; ++i)
-                    fa[s][i] = KT::OA::template frag<16>(sa + s * KT::OA::BYTES, wm * KT::WTM + i * 16, x * 32, lane);
+                    for (int s = 0; s < TA; ++s)
 #pragma unroll
-            for (int s = 0; s < TQ; ++s)
+                        for (int i = 0; i < KT::TM; ++i)
+                            fa[x % F][s][i] = KT::OA::template frag<16>(sa + s * KT::OA::BYTES, wm * KT::WTM + i * 16, x * 32, lane);
 #pragma unroll
-                for (int j = 0; j < KT::TN; ++j)
-                    fq[s][j] = KT::OB::template frag<16>(sq + s * KT::OB::BYTES, wn * KT::WTN + j * 16, x * 32, lane);
-            // Small terms first.
+                    for (int s = 0; s < TQ; ++s)
 #pragma unroll
-            for (int s = TA * TQ - 1; s >= 0; --s)
+                        for (int j = 0; j < KT::TN; ++j)
+                            fq[x % F][s][j] = KT::OB::template frag<16>(sq + s * KT::OB::BYTES, wn * KT::WTN + j * 16, x * 32, lane);
+                };
+                // The other stage: every wave has read it before the last barrier.
+                auto next = [&]() {
+                    store(t + 1, (d + 1) % D, smem + (1 - stage) * STAGE);
+                    load(t + 1 + D, (d + 1) % D);
+                };
+                read(0);
+                if constexpr (early) {
+                    next();
+                    __builtin_amdgcn_sched_barrier(0);
+                }
 #pragma unroll
-                for (int i = 0; i < KT::TM; ++i)
+                for (int x = 0; x < KT::NG; ++x) {
+                    if (AHEAD && x + 1 < KT::NG) read(x + 1);
+                    // Small terms first.
 #pragma unroll
-                    for (int j = 0; j < KT::TN; ++j) mfma_step<MT, 16>(fa[s / TQ][i], fq[s % TQ][j], acc[i][j]);
+                    for (int s = TA * TQ - 1; s >= 0; --s)
+#pragma unroll
+                        for (int i = 0; i < KT::TM; ++i)
+#pragma unroll
+                            for (int j = 0; j < KT::TN; ++j) mfma_step<MT, 16>(fa[x % F][s / TQ][i], fq[x % F][s % TQ][j], acc[i][j]);
+                    if (!AHEAD && x + 1 < KT::NG) read(x + 1);
+                }
+                if constexpr (!early) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    next();
+                }
+                __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0)
+                bare_barrier();
+            }
+        }
+    };
+    if (wave < NW / 2) loop(std::true_type{});
+    else loop(std::false_type{});
+    store_tile<KT, EPI>(p, smem, m0, n0, acc, tid, lane, wave);
+}
+
+// Few tiles: NW waves take a tile's k-tiles in turn, each through LDS of its own
+// with nothing to wait for but itself, and their sums meet at the end, in wave
+// order.
+template <In TI, Out TO, int BM, int BN, int BK, int NW, int D, bool AK, bool VEC>
+__global__ void __launch_bounds__(NW * 64)
+gemm_i8grad_stream_kernel(GradParams g)
+{
+    using GT = GradTypes<TI, TO>;
+    constexpr In MT = GT::MT;
+    constexpr int TA = GT::TA, TQ = GT::TQ;
+    using KT = Dma16<MT, TO, BM, BN, BK, 1, 1, 16, 2, AK, false>;
+    using OA = AOperand<TI, BM, BK, 1, AK, GT::SPLIT_A, VEC, D>;
+    using OQ = QOperand<MT, BN, BK, 1, TQ, !GT::SPLIT_A, VEC, D>;
+    constexpr int STAGE = TA * KT::OA::BYTES + TQ * KT::OB::BYTES, PART = BM * BN;
+    constexpr int SMEM = NW * (STAGE > PART * 4 ? STAGE : PART * 4);
+    static_assert(SMEM <= 160 * 1024, "LDS budget");
+    __shared__ __attribute__((aligned(1024))) char smem[SMEM];
+    const Params& p = g.p;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tm, tn;
+    tile_coords(p, tm, tn);
+    const int m0 = __builtin_amdgcn_readfirstlane(tm) * BM, n0 = __builtin_amdgcn_readfirstlane(tn) * BN;
+    const int nkt = (p.K + BK - 1) / BK;
+    typename KT::Acc acc;
+    KT::zero(acc);
+    OA oa;
+    OQ oq;
+    oa.init(0, lane, p.lda);
+    oq.init(0, lane, p.ldb);
+    auto load = [&](int t, int d) {               // past the end: empty extents
+        oa.load(d, g, m0, t * BK, 0, lane);
+        oq.load(d, g, n0, t * BK, 0, lane);
+    };
+    char* const sa = smem + wave * STAGE;
+    char* const sq = sa + TA * KT::OA::BYTES;
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(wave + d * NW, d);
+    for (int t0 = wave; t0 < nkt; t0 += D * NW) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const int t = t0 + d * NW;
+            if (t >= nkt) break;
+            oa.store(d, g, sa, t * BK, 0, lane);
+            oq.store(d, g, sq, n0, t * BK, 0, lane);
+            load(t + D * NW, d);
+            __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): written
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int x = 0; x < KT::NG; ++x) {
+                i32x4 fa[TA][KT::TM], fq[TQ][KT::TN];
+#pragma unroll
+                for (int s = 0; s < TA; ++s)
+#pragma unroll
+                    for (int i = 0; i < KT::TM; ++i)
+                        fa[s][i] = KT::OA::template frag<16>(sa + s * KT::OA::BYTES, i * 16, x * 32, lane);
+#pragma unroll
+                for (int s = 0; s < TQ; ++s)
+#pragma unroll
+                    for (int j = 0; j < KT::TN; ++j)
+                        fq[s][j] = KT::OB::template frag<16>(sq + s * KT::OB::BYTES, j * 16, x * 32, lane);
+#pragma unroll
+                for (int s = TA * TQ - 1; s >= 0; --s)            // small terms first
+#pragma unroll
+                    for (int i = 0; i < KT::TM; ++i)
+#pragma unroll
+                        for (int j = 0; j < KT::TN; ++j) mfma_step<MT, 16>(fa[s / TQ][i], fq[s % TQ][j], acc[i][j]);
+            }
+            __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): read, the next tile may be written
+            asm volatile("" ::: "memory");
         }
     }
-    store_tile<KT, EPI>(p, smem, m0, n0, acc, tid, lane, wave);
+    __syncthreads();
+    float* const part = (float*)smem;
+#pragma unroll
+    for (int i = 0; i < KT::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < KT::TN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) part[wave * PART + KT::row(0, i, e, lane) * BN + KT::col(0, j, lane)] = acc[i][j][e];
+    __syncthreads();
+    for (int x = tid; x < PART; x += NW * 64) {
+        const int m = m0 + x / BN, n = n0 + x % BN;
+        if (m >= p.M || n >= p.N) continue;
+        float v = part[x];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) v += part[w * PART + x];
+        const int64_t at = (int64_t)m * p.ldc + n;
+        store_out<TO>(p.C, at, p.epi ? v + load_out<TO>(p.C, at) : v);
+    }
 }
 
 // ------------------------------------------------------------------ launchers
@@ -312,27 +494,60 @@ struct GradCall {
     bool vec;             // A and Q allow 16-byte loads
 };
 
+inline GradShape shape_of(const GradCall& c, bool wide, bool split_a) { return {c.vec, wide, split_a, c.g.p.M, c.g.p.N, c.g.p.K}; }
+
 template <In TI, Out TO>
 struct GradInst {
-    template <class Kernel>
-    static hipError_t run(Kernel kernel, GradParams g, int bm, int bn, int threads, hipStream_t s)
+    using GT = GradTypes<TI, TO>;
+    static constexpr bool WIDE = TO == Out::F32;
+    static hipError_t run(const void* kernel, const GradCall& c, const Tile& t, hipStream_t s)
     {
+        GradParams g = c.g;
         Params& p = g.p;
-        p.tiles_m = (int)ceil_div(p.M, bm);
-        p.tiles_n = (int)ceil_div(p.N, bn);
+        p.tiles_m = (int)ceil_div(p.M, t.bm);
+        p.tiles_n = (int)ceil_div(p.N, t.bn);
         p.group_m = p.tiles_m < 8 ? p.tiles_m : 8;
         void* args[] = {&g};
-        return hipLaunchKernel((const void*)kernel, dim3((unsigned)(p.tiles_m * p.tiles_n)), dim3(threads), args, 0, s);
+        return hipLaunchKernel(kernel, dim3((unsigned)grad_grid(shape_of(c, WIDE, GT::SPLIT_A), t)), dim3(t.threads), args, 0, s);
     }
-    template <bool AK, bool EPI>
+    template <GradTile T, bool AK, bool VEC>
+    static hipError_t stream(const GradCall& c, hipStream_t s)
+    {
+        constexpr Tile t = tile_of(T);
+        return run((const void*)&gemm_i8grad_stream_kernel<TI, TO, t.bm, t.bn, t.bk, t.extra, t.stages, AK, VEC>, c, t, s);
+    }
+    template <GradTile T, bool AK, bool VEC>
+    static hipError_t tile(const GradCall& c, hipStream_t s)
+    {
+        constexpr Tile t = tile_of(T);
+        return run(c.g.p.epi ? (const void*)&gemm_i8grad_kernel<TI, TO, t.bm, t.bn, t.bk, t.wm, t.wn, t.stages, t.extra, AK, VEC, true>
+                             : (const void*)&gemm_i8grad_kernel<TI, TO, t.bm, t.bn, t.bk, t.wm, t.wn, t.stages, t.extra, AK, VEC, false>,
+                   c, t, s);
+    }
+    template <bool AK, bool VEC>
     static hipError_t go(const GradCall& c, hipStream_t s)
     {
-        return run(&gemm_i8grad_odd_kernel<TI, TO, 64, 64, 32, 2, 2, AK, EPI>, c.g, 64, 64, 256, s);
+        const GradTile t = grad_tile(shape_of(c, WIDE, GT::SPLIT_A));
+        switch (t) {
+        case GradTile::Stream32x32: return stream<GradTile::Stream32x32, AK, VEC>(c, s);
+        case GradTile::Stream32x64: return stream<GradTile::Stream32x64, AK, VEC>(c, s);
+        case GradTile::T64x64: return tile<GradTile::T64x64, AK, VEC>(c, s);
+        case GradTile::T64x128: return tile<GradTile::T64x128, AK, VEC>(c, s);
+        case GradTile::T128x128: return tile<GradTile::T128x128, AK, VEC>(c, s);
+        default: break;
+        }
+        if constexpr (VEC) {
+            if (t == GradTile::T128x128Deep) return tile<GradTile::T128x128Deep, AK, true>(c, s);
+            if constexpr (!WIDE) return tile<GradTile::T256x256, AK, true>(c, s);
+            else if constexpr (GT::SPLIT_A) return tile<GradTile::Wide128x256, AK, true>(c, s);
+            else return tile<GradTile::Tall256x128, AK, true>(c, s);
+        }
+        return hipErrorInvalidValue;
     }
     static hipError_t launch(const GradCall& c, hipStream_t s)
     {
-        if (c.a_kmajor) return c.g.p.epi ? go<true, true>(c, s) : go<true, false>(c, s);
-        return c.g.p.epi ? go<false, true>(c, s) : go<false, false>(c, s);
+        if (c.a_kmajor) return c.vec ? go<true, true>(c, s) : go<true, false>(c, s);
+        return c.vec ? go<false, true>(c, s) : go<false, false>(c, s);
     }
 };
 

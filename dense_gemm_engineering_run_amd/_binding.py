@@ -505,6 +505,7 @@ def gemm_lora(a, b, c, down, up, ids, workspace, ranks=None, scales=None, stream
     return c
 
 
+_F32, _I8 = (None, None) if torch is None else (torch.float32, torch.int8)
 _TYPE_CODES = {} if torch is None else {torch.float32: GEMM_TYPE_F32, torch.float16: GEMM_TYPE_F16,
                                         torch.bfloat16: GEMM_TYPE_BF16}
 
@@ -516,41 +517,57 @@ def _type_code(dtype, what):
         raise ValueError(f"{what} must be float32, float16 or bfloat16, not {dtype}") from None
 
 
-def _float_vector(t, n, what):
-    if t.dtype is not torch.float32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+def _float_vector(t, index, n, what):
+    """The address of a contiguous float32 vector of n on GPU `index`."""
+    if t.dtype is not _F32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous float32 vector of {n}")
+    if t.get_device() != index:
+        raise ValueError(f"{what} must be on GPU {index}, not {t.device}")
+    return t.data_ptr()
+
+
+def _rows_ld(t, rows, cols):
+    """_ld of a matrix of known sizes, row-major."""
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        return None
+    if rows <= 1:
+        return max(16, -(-cols // 16) * 16)
+    return s0 if s0 >= max(1, cols) else None
 
 
 def _rows8(wide, q, scales, names):
     """Checks of a matrix, its 8-bit form and its rows' scales: the GPU, M, K,
-    both leading dimensions and the wide type's code."""
-    index = _gpu_index(wide, q, scales)
+    both leading dimensions, the wide type's code and the scales' address."""
+    index = wide.get_device()
+    if index < 0 or q.get_device() != index:
+        _gpu_index(wide, q)
     shape = wide.shape
     if len(shape) != 2 or q.shape != shape:
         raise ValueError(f"shape mismatch: {names[0]} {tuple(shape)}, {names[1]} {tuple(q.shape)}")
-    if q.dtype is not torch.int8:
+    if q.dtype is not _I8:
         raise ValueError(f"{names[1]} must be int8, not {q.dtype}")
-    _float_vector(scales, shape[0], "scales")
-    ldw, ldq = _ld(shape, wide.stride(), 0, 1), _ld(shape, q.stride(), 0, 1)
+    M, K = shape
+    ldw, ldq = _rows_ld(wide, M, K), _rows_ld(q, M, K)
     if ldw is None or ldq is None:
         raise ValueError(f"{names[0]} {wide.stride()} and {names[1]} {q.stride()} must be row-major")
-    return index, shape[0], shape[1], ldw, ldq, _type_code(wide.dtype, names[0])
+    return index, M, K, ldw, ldq, _type_code(wide.dtype, names[0]), _float_vector(scales, index, M, "scales")
 
 
 def quantize_rows(x, q, scales, stream=None):
     """Rows of x (M, K) to 8-bit integers q (M, K) and a float32 scale each
     (gemm_quantize_rows): scales = max |x| / 127 of a row, q = x / scales to the
     nearest, ties to even.  x and q are row-major.  Returns q and scales."""
-    index, M, K, ldx, ldq, code = _rows8(x, q, scales, ("x", "q"))
-    _launch(_lib.gemm_quantize_rows, index, stream, M, K, code, x.data_ptr(), q.data_ptr(), scales.data_ptr(), ldx, ldq)
+    index, M, K, ldx, ldq, code, at = _rows8(x, q, scales, ("x", "q"))
+    _launch(_lib.gemm_quantize_rows, index, stream, M, K, code, x.data_ptr(), q.data_ptr(), at, ldx, ldq)
     return q, scales
 
 
 def dequantize_rows(q, scales, x, stream=None):
     """x = q * scales[:, None] in x's type (gemm_dequantize_rows); x and q are
     (M, K), row-major.  Returns x."""
-    index, M, K, ldx, ldq, code = _rows8(x, q, scales, ("x", "q"))
-    _launch(_lib.gemm_dequantize_rows, index, stream, M, K, code, q.data_ptr(), scales.data_ptr(), x.data_ptr(), ldq, ldx)
+    index, M, K, ldx, ldq, code, at = _rows8(x, q, scales, ("x", "q"))
+    _launch(_lib.gemm_dequantize_rows, index, stream, M, K, code, q.data_ptr(), at, x.data_ptr(), ldq, ldx)
     return x
 
 
@@ -558,24 +575,25 @@ def gemm_i8(a, b, scale_a, scale_b, c, bias=None, activation=GEMM_ACT_NONE, stre
     """C = act(scale_a[:, None] * scale_b * (A * B^T) + bias) (gemm_run_i8): a is
     (M, K) and b (N, K), int8, c (M, N), all row-major; scale_a (M,), scale_b (N,)
     and bias (N,) are float32 vectors or None; activation is a GEMM_ACT_*."""
-    index = _gpu_index(a, b, c)
-    sa, sb = a.shape, b.shape
-    if len(sa) != 2 or len(sb) != 2 or sb[1] != sa[1] or c.shape != (sa[0], sb[0]):
-        raise ValueError(f"shape mismatch: a {tuple(sa)}, b {tuple(sb)}, c {tuple(c.shape)}")
-    if a.dtype is not torch.int8 or b.dtype is not torch.int8:
+    index = a.get_device()
+    if index < 0 or b.get_device() != index or c.get_device() != index:
+        _gpu_index(a, b, c)
+    sa, sb, sc = a.shape, b.shape, c.shape
+    if len(sa) != 2 or len(sb) != 2 or len(sc) != 2 or sb[1] != sa[1] or sc[0] != sa[0] or sc[1] != sb[0]:
+        raise ValueError(f"shape mismatch: a {tuple(sa)}, b {tuple(sb)}, c {tuple(sc)}")
+    if a.dtype is not _I8 or b.dtype is not _I8:
         raise ValueError(f"a and b must be int8, not {a.dtype} and {b.dtype}")
-    at = [0, 0, 0]
-    for i, (t, n, what) in enumerate(((scale_a, sa[0], "scale_a"), (scale_b, sb[0], "scale_b"), (bias, sb[0], "bias"))):
-        if t is not None:
-            _gpu_index(a, t)
-            _float_vector(t, n, what)
-            at[i] = t.data_ptr()
-    lda, ldb, ldc = _ld(sa, a.stride(), 0, 1), _ld(sb, b.stride(), 0, 1), _ld(c.shape, c.stride(), 0, 1)
+    (M, K), N = sa, sb[0]
+    scale_a = 0 if scale_a is None else _float_vector(scale_a, index, M, "scale_a")
+    scale_b = 0 if scale_b is None else _float_vector(scale_b, index, N, "scale_b")
+    epilogue = None
+    if bias is not None or activation != GEMM_ACT_NONE:
+        epilogue = _EPILOGUE.pack(1.0, 0.0, 0 if bias is None else _float_vector(bias, index, N, "bias"), activation)
+    lda, ldb, ldc = _rows_ld(a, M, K), _rows_ld(b, N, K), _rows_ld(c, M, N)
     if lda is None or ldb is None or ldc is None:
         raise ValueError(f"a {a.stride()}, b {b.stride()} and c {c.stride()} must be row-major")
-    epilogue = None if bias is None and activation == GEMM_ACT_NONE else _EPILOGUE.pack(1.0, 0.0, at[2], activation)
-    _launch(_lib.gemm_run_i8, index, stream, sa[0], sb[0], sa[1], b"k", b"k", b"n", _type_code(c.dtype, "c"), a.data_ptr(),
-            b.data_ptr(), c.data_ptr(), lda, ldb, ldc, at[0], at[1], epilogue)
+    _launch(_lib.gemm_run_i8, index, stream, M, N, K, b"k", b"k", b"n", _type_code(c.dtype, "c"), a.data_ptr(),
+            b.data_ptr(), c.data_ptr(), lda, ldb, ldc, scale_a, scale_b, epilogue)
     return c
 
 
@@ -585,23 +603,25 @@ def gemm_i8_grad(a, q, scales, c, accumulate=False, stream=None):
     contiguous, scales a float32 (K,), c (M, N) row-major.  For a layer y =
     x * w^T with xq, xs = quantize_rows(x, ...) and wq, ws = quantize_rows(w, ...):
     gemm_i8_grad(dy.t(), xq.t(), xs, dw) and gemm_i8_grad(dy, wq.t(), ws, dx)."""
-    index = _gpu_index(a, q, scales, c)
-    sa, sq = a.shape, q.shape
-    if len(sa) != 2 or len(sq) != 2 or sq[1] != sa[1] or c.shape != (sa[0], sq[0]):
-        raise ValueError(f"shape mismatch: a {tuple(sa)}, q {tuple(sq)}, c {tuple(c.shape)}")
-    if q.dtype is not torch.int8:
+    index = a.get_device()
+    if index < 0 or q.get_device() != index or c.get_device() != index:
+        _gpu_index(a, q, c)
+    sa, sq, sc = a.shape, q.shape, c.shape
+    if len(sa) != 2 or len(sq) != 2 or len(sc) != 2 or sq[1] != sa[1] or sc[0] != sa[0] or sc[1] != sq[0]:
+        raise ValueError(f"shape mismatch: a {tuple(sa)}, q {tuple(sq)}, c {tuple(sc)}")
+    if q.dtype is not _I8:
         raise ValueError(f"q must be int8, not {q.dtype}")
-    _float_vector(scales, sa[1], "scales")
-    ta = a.stride()
-    am, lda = b"k", _ld(sa, ta, 0, 1)
+    (M, K), N = sa, sq[0]
+    at = _float_vector(scales, index, K, "scales")
+    am, lda = b"k", _rows_ld(a, M, K)
     if lda is None:
-        am, lda = b"m", _ld(sa, ta, 1, 0)
-    ldq, ldc = _ld(sq, q.stride(), 1, 0), _ld(c.shape, c.stride(), 0, 1)
+        am, lda = b"m", _ld(sa, a.stride(), 1, 0)
+    ldq, ldc = _ld(sq, q.stride(), 1, 0), _rows_ld(c, M, N)
     if lda is None or ldq is None or ldc is None:
-        raise ValueError(f"a {ta} must have one contiguous dimension, q {q.stride()} be the transposed view of a row-major "
-                         f"matrix, c {c.stride()} row-major")
-    _launch(_lib.gemm_run_i8_grad, index, stream, sa[0], sq[0], sa[1], am, b"n", b"n", dtype_code(a.dtype, c.dtype),
-            a.data_ptr(), q.data_ptr(), c.data_ptr(), lda, ldq, ldc, scales.data_ptr(), bool(accumulate))
+        raise ValueError(f"a {a.stride()} must have one contiguous dimension, q {q.stride()} be the transposed view of a "
+                         f"row-major matrix, c {c.stride()} row-major")
+    _launch(_lib.gemm_run_i8_grad, index, stream, M, N, K, am, b"n", b"n", dtype_code(a.dtype, c.dtype), a.data_ptr(),
+            q.data_ptr(), c.data_ptr(), lda, ldq, ldc, at, bool(accumulate))
     return c
 
 

@@ -78,14 +78,15 @@ inline int64_t i8_grid(const I8Shape& s, const Tile& t) { return ceil_div(s.M, t
 // bk: k of a tile; stages: tiles of loads in flight (streaming: a wave's);
 // extra: waves that stream, else waves a SIMD that the registers leave room for.
 enum class GradTile : int {
-    Stream32x32, Stream32x64, T64x64, T64x128, T128x128Deep, T128x128, T256x256, Tall256x128, Wide128x256, Count
+    Stream32x32, Stream32x64, T64x64, T64x128, T64x128Two, T128x128Deep, T128x128, T256x256, Tall256x128, Wide128x256, Count
 };
 constexpr Tile kGradTiles[] = {
     {"stream 32x32", 32, 32, 64, 1, 1, 16, 2, 8, 512},
     {"stream 32x64", 32, 64, 32, 1, 1, 16, 2, 8, 512},
     {"64x64", 64, 64, 128, 2, 4, 16, 2, 2, 512},
     {"64x128", 64, 128, 64, 2, 4, 16, 2, 2, 512},
-    {"128x128, 64 deep", 128, 128, 64, 2, 4, 16, 2, 2, 512},
+    {"64x128, two a CU", 64, 128, 64, 2, 4, 16, 1, 4, 512},
+    {"128x128, 64 deep", 128, 128, 64, 4, 4, 16, 1, 4, 1024},
     {"128x128", 128, 128, 32, 2, 4, 16, 2, 2, 512},
     {"256x256", 256, 256, 32, 4, 2, 16, 2, 2, 512},
     {"256x128", 256, 128, 64, 4, 4, 16, 1, 4, 1024},
@@ -101,17 +102,39 @@ struct GradShape {
     int64_t M, N, K;
 };
 
+// The smallest tile that makes no more than one for each of the 256 CUs; past
+// that the largest that fills most of them.  us, bf16 into bf16 / bf16 into fp32
+// / fp32, A m-major (k-major is within a few percent):
+//   M x N, K              32x32 str.   32x64 str.    64x64        64x128       128x128, 64 deep
+//    512 x  256, 1000    6.7/8.3/9.1  7.7/10/9.6   9.1/13/16    12/21/19
+//     32 x 4096, 4096    13/17/19     15/26/22      25/42/50
+//   1024 x  512, 1024    9.6/14/16    7.9/11/10     9.2/14/16
+//   1024 x 1024, 4096    39/64/77     28/52/44      24/44/50     38/71/65       51/98/109
+//   2048 x 1024, 4096                               41/83/97     38/71/66       51/100/110
+//   2048 x 2048, 4096                               80/165/192   63/142/113     54/105/113
+//                        64x128       128x128       256x256 | 256x128 | 128x256 (16-bit C, Q's terms, A's terms)
+//   4096 x 2048, 1024    33/80/61     27/50/74      35/49/54
+//   3008 x 2000, 3008    67/158/126   68/123/197    89/113/118
+//   4096 x 4096, 2048    - / - /225   94/181/ -     69/176/179
+//   8192 x 2048, 1024    - / - /115   50/94/ -      38/98/94
+// Unaligned: 2049 x 1028, 4095 k takes 50/ - /145 on 64x128, 56/ - /100 on 128x128
+// 64 deep (153 tiles); 3000 x 2000, 3001 k 68/ - /127 on 64x128, 69/ - /197 on
+// 128x128, - / - /134 on 64x128 with two a CU (k-major - / - /129, 159 on 64x128).
 inline GradTile grad_tile(const GradShape& s)
 {
     auto tiles = [&](int bm, int bn) { return ceil_div(s.M, bm) * ceil_div(s.N, bn); };
     if (tiles(32, 32) <= 256) return GradTile::Stream32x32;
     if (tiles(32, 64) <= 256) return GradTile::Stream32x64;
     if (tiles(64, 64) <= 256) return GradTile::T64x64;
-    if (tiles(64, 128) <= 384) return GradTile::T64x128;
-    if (!s.vec) return GradTile::T128x128;
+    if (tiles(64, 128) <= 256) return GradTile::T64x128;
     if (tiles(128, 128) <= 256) return GradTile::T128x128Deep;
-    if (s.wide) return tiles(256, 128) < 384 ? GradTile::T128x128 : s.split_a ? GradTile::Wide128x256 : GradTile::Tall256x128;
-    return tiles(256, 256) < 192 ? GradTile::T128x128 : GradTile::T256x256;
+    if (s.split_a) {
+        if (!s.vec) return GradTile::T64x128Two;
+        return tiles(128, 256) >= 160 ? GradTile::Wide128x256 : GradTile::T64x128;
+    }
+    if (!s.vec) return GradTile::T128x128;
+    if (s.wide) return tiles(256, 128) >= 160 ? GradTile::Tall256x128 : GradTile::T128x128;
+    return tiles(256, 256) >= 160 ? GradTile::T256x256 : GradTile::T128x128;
 }
 
 inline int64_t grad_grid(const GradShape& s, const Tile& t) { return ceil_div(s.M, t.bm) * ceil_div(s.N, t.bn); }

@@ -533,14 +533,15 @@ struct GradInst {
         case GradTile::Stream32x64: return stream<GradTile::Stream32x64, AK, VEC>(c, s);
         case GradTile::T64x64: return tile<GradTile::T64x64, AK, VEC>(c, s);
         case GradTile::T64x128: return tile<GradTile::T64x128, AK, VEC>(c, s);
-        case GradTile::T128x128: return tile<GradTile::T128x128, AK, VEC>(c, s);
+        case GradTile::T128x128Deep: return tile<GradTile::T128x128Deep, AK, VEC>(c, s);
         default: break;
         }
-        if constexpr (VEC) {
-            if (t == GradTile::T128x128Deep) return tile<GradTile::T128x128Deep, AK, true>(c, s);
-            if constexpr (!WIDE) return tile<GradTile::T256x256, AK, true>(c, s);
-            else if constexpr (GT::SPLIT_A) return tile<GradTile::Wide128x256, AK, true>(c, s);
-            else return tile<GradTile::Tall256x128, AK, true>(c, s);
+        if constexpr (GT::SPLIT_A) {
+            if constexpr (!VEC) return tile<GradTile::T64x128Two, AK, false>(c, s);
+            else return tile<GradTile::Wide128x256, AK, true>(c, s);
+        } else {
+            if (t == GradTile::T128x128) return tile<GradTile::T128x128, AK, VEC>(c, s);
+            if constexpr (VEC) return tile<WIDE ? GradTile::Tall256x128 : GradTile::T256x256, AK, true>(c, s);
         }
         return hipErrorInvalidValue;
     }

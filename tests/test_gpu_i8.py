@@ -27,6 +27,7 @@ import pytest
 import torch
 
 import dense_gemm_engineering_run_amd as g
+import i8_kernel_cases as cases
 
 pytestmark = pytest.mark.gpu
 
@@ -49,9 +50,11 @@ def ints(shape, seed, lo=-128, hi=127):
 
 
 def place(t, pad=0, offset=0, fill=SENTINEL):
-    """The matrix t on the GPU with `pad` more elements a row, `offset` elements
-    behind an aligned address; everything around it holds `fill`."""
+    """The matrix t on the GPU with `pad` more elements a row (None: up to 32, as
+    many as make rows of 16-byte multiples), `offset` elements behind an aligned
+    address; everything around it holds `fill`."""
     rows, cols = t.shape
+    pad = 16 + -cols % 16 if pad is None else pad
     flat = torch.full((rows * (cols + pad) + offset + 16,), fill, dtype=t.dtype, device="cuda")
     v = flat[offset:offset + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
     v.copy_(t)
@@ -206,7 +209,7 @@ class Product:
         size = (127.0 * math.sqrt(max(K, 1))) ** -0.5
         self.sa = (torch.exp(randn((M,), seed + 3)) * size).cuda() if scaled else None
         self.sb = (torch.exp(randn((N,), seed + 4)) * size / 30).cuda() if scaled else None
-        self.c = place(randn((M, N), seed + 5).to(self.t), pad + c_pad, offset)
+        self.c = place(randn((M, N), seed + 5).to(self.t), pad if pad is None else pad + c_pad, offset)
 
     def sums(self):
         return self.a.double() @ self.b.double().t()
@@ -333,7 +336,7 @@ class Gradient:
         self.q = place(q.to(torch.int8), pad, offset).t()
         s = 2.0 ** ints((K,), seed + 3, -1, 1).float() if self.exact else torch.exp(randn((K,), seed + 3)) / 100
         self.s = s.cuda()
-        self.c = place(ints((M, N), seed + 4, -9, 9).to(self.tout), pad + c_pad, offset)
+        self.c = place(ints((M, N), seed + 4, -9, 9).to(self.tout), pad if pad is None else pad + c_pad, offset)
 
     def reference(self, accumulate):
         a, x = self.a.double(), (self.s.double()[:, None] * self.q.t().double())
@@ -419,6 +422,50 @@ def test_what_is_not_a_number_stays_where_it_belongs(dtype, a_major):
         y.s[K // 2] = float("nan")
         g.gemm_i8_grad(y.a, y.q, y.s, y.c)
         assert y.c.isnan().all()
+
+
+# ---------------------------------------------------------------- every kernel
+
+@pytest.mark.parametrize("dtype", WIDE)
+@pytest.mark.parametrize("name,M,N", cases.PRODUCTS + cases.PRODUCTS_UNALIGNED)
+def test_every_product_kernel(dtype, name, M, N):
+    aligned = not name.startswith("unaligned")
+    for i, K in enumerate((1, 16, 100, 128, 255, 256, 257, 1041)):       # K odd and even, k-tiles whole and not
+        say(name, M, N, K)
+        Product(M, N, K, dtype, *((None, 0) if aligned else (1, 3)), seed=i).run()
+    if aligned:
+        Product(M, N, 384, dtype, None).run_epilogue(0.5, 0.25, True, g.GEMM_ACT_GELU)
+        x = Product(M, N, 160, dtype, None)
+        x.c = place(x.c.cpu(), 1, 1)                                        # C at any element
+        x.run()
+    else:
+        Product(M, N, 384, dtype, 1, 3).run_epilogue(0.5, 0.25, True, g.GEMM_ACT_GELU)
+
+
+def _gradient_kernels():
+    out = []
+    for dtype in PAIRS:
+        tin, tout = PAIRS[dtype]
+        for aligned in (True, False):
+            for name, M, N in cases.gradients(tout == F32, tout == F32 and tin != BF16, aligned):
+                out.append(pytest.param(dtype, aligned, M, N, id=f"{dtype}-{name}-{'aligned' if aligned else 'not'}".replace(" ", "_")))
+    return out
+
+
+@pytest.mark.parametrize("dtype,aligned,M,N", _gradient_kernels())
+@pytest.mark.parametrize("a_major", "mk")
+def test_every_gradient_kernel(dtype, aligned, M, N, a_major):
+    for i, K in enumerate((1, 32, 64, 131, 256, 520)):
+        say(dtype, aligned, a_major, M, N, K)
+        at = (None, 0) if aligned else (1, 3)
+        Gradient(M, N, K, dtype, a_major, *at, seed=i).run(accumulate=i % 2 == 1)
+        if i in (3, 5):
+            Gradient(M, N, K, dtype, a_major, *at, "int", seed=i).run(accumulate=i == 3)
+    if aligned:
+        x = Gradient(M, N, 200, dtype, a_major, None)
+        x.c = place(x.c.cpu(), 1, 1)
+        x.run()
+        x.run(accumulate=True)
 
 
 # ---------------------------------------------------------------- together

@@ -19,15 +19,16 @@ hipError_t launch(Kernel kernel, int64_t groups, int threads, hipStream_t s, Qua
     return hipLaunchKernel((const void*)kernel, dim3((unsigned)groups), dim3(threads), args, 0, s);
 }
 
-// How a call runs: waves a row and chunks a lane (0 waves: element by element).
+// How a call runs: waves a row and chunks a lane (0 waves: rows longer than
+// registers hold).
 struct QuantPlan {
     int waves, chunks;
     int64_t groups;
 };
-QuantPlan plan(int64_t M, int64_t K, int es, bool vec)
+QuantPlan plan(int64_t M, int64_t K, int es)
 {
     const int64_t lane_chunks = mg::ceil_div(K * es, 16 * 64);      // by one wave
-    if (!vec || lane_chunks > 64) return {0, 0, M};
+    if (lane_chunks > 64) return {0, 0, M};
     if (M > 2048 && lane_chunks <= 8) return {1, lane_chunks <= 2 ? 2 : lane_chunks <= 4 ? 4 : 8, mg::ceil_div(M, 4)};
     const int64_t c = mg::ceil_div(lane_chunks, 4);
     return {4, c <= 2 ? 2 : c <= 4 ? 4 : c <= 8 ? 8 : 16, M};
@@ -45,7 +46,7 @@ hipError_t quantize(const Quant& p, const QuantPlan& q, hipStream_t s)
     case 404: return launch(&quantize_kernel<T, 4, 4>, q.groups, 256, s, p);
     case 408: return launch(&quantize_kernel<T, 4, 8>, q.groups, 256, s, p);
     case 416: return launch(&quantize_kernel<T, 4, 16>, q.groups, 256, s, p);
-    default: return launch(&mg::quantize_any_kernel<T>, q.groups, 256, s, p);
+    default: return launch(&mg::quantize_long_kernel<T>, q.groups, 256, s, p);
     }
 }
 
@@ -53,17 +54,16 @@ struct RestorePlan {
     int spans;
     int64_t groups;
 };
-RestorePlan restore_plan(int64_t M, int64_t K, int es, bool vec)
+RestorePlan restore_plan(int64_t M, int64_t K, int es)
 {
-    const int64_t spans = mg::ceil_div(K, vec ? 64 * 4 * (16 / es) : 64 * 16);
+    const int64_t spans = mg::ceil_div(K, 64 * mg::kRestoreSteps * (16 / es));
     return {(int)spans, mg::ceil_div(M * spans, 4)};
 }
 
 template <In T>
-hipError_t dequantize(const Quant& p, const RestorePlan& q, bool vec, hipStream_t s)
+hipError_t dequantize(const Quant& p, const RestorePlan& q, hipStream_t s)
 {
-    return vec ? launch(&mg::dequantize_kernel<T, true>, q.groups, 256, s, p, q.spans)
-               : launch(&mg::dequantize_kernel<T, false>, q.groups, 256, s, p, q.spans);
+    return launch(&mg::dequantize_kernel<T>, q.groups, 256, s, p, q.spans);
 }
 
 void log_call(const char* what, int64_t M, int64_t K, int type, int st)
@@ -90,23 +90,19 @@ int run(bool to8, int64_t M, int64_t K, int type, const void* X, void* Y, float*
     if (mg::overlap(X, nx, Y, ny) || mg::overlap(scales, ns, Y, ny) || (to8 && mg::overlap(scales, ns, X, nx)))
         return GEMM_ERR_ALIAS;
     const Quant p = {(const char*)X, (char*)Y, scales, M, ldx, ldy, (int)K};
-    // Chunks of 16 bytes of wide values beside as many 8-bit ones.
-    const Operand& wide = to8 ? ox : oy;
-    const Operand& narrow = to8 ? oy : ox;
-    const bool vec = wide.aligned(16) && ((uintptr_t)narrow.p | (uint64_t)narrow.ld) % (16 / es) == 0;
     hipError_t e;
     if (to8) {
-        const QuantPlan q = plan(M, K, es, vec);
+        const QuantPlan q = plan(M, K, es);
         if (q.groups > mg::kMaxGridThreads / mg::kQuantThreads) return GEMM_ERR_BAD_SHAPE;
         e = type == GEMM_TYPE_F32 ? quantize<In::F32>(p, q, (hipStream_t)stream)
             : type == GEMM_TYPE_F16 ? quantize<In::F16>(p, q, (hipStream_t)stream)
                                     : quantize<In::BF16>(p, q, (hipStream_t)stream);
     } else {
-        const RestorePlan q = restore_plan(M, K, es, vec);
+        const RestorePlan q = restore_plan(M, K, es);
         if (q.groups > mg::kMaxGridThreads / mg::kQuantThreads) return GEMM_ERR_BAD_SHAPE;
-        e = type == GEMM_TYPE_F32 ? dequantize<In::F32>(p, q, vec, (hipStream_t)stream)
-            : type == GEMM_TYPE_F16 ? dequantize<In::F16>(p, q, vec, (hipStream_t)stream)
-                                    : dequantize<In::BF16>(p, q, vec, (hipStream_t)stream);
+        e = type == GEMM_TYPE_F32 ? dequantize<In::F32>(p, q, (hipStream_t)stream)
+            : type == GEMM_TYPE_F16 ? dequantize<In::F16>(p, q, (hipStream_t)stream)
+                                    : dequantize<In::BF16>(p, q, (hipStream_t)stream);
     }
     const int st = e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
     log_call(to8 ? "quantize_rows" : "dequantize_rows", M, K, type, st);

@@ -7,8 +7,8 @@
 // is exact in fp32; one Newton step with its exact remainder gives the quotient
 // as fp32 rounds it, and no quotient of such numbers other than an exact half
 // comes closer than 2^-19 of itself to one, so rounding that to an integer is
-// right.  For fp32 x a quotient within 2^-14 of a half is computed again in
-// fp64, whose 53 bits separate any 31-bit numerator's quotient from a half.
+// right.  For fp32 x a quotient within 2^-14 of a half is compared with it by the
+// exact products 127 x and half * top, each as two fp32 numbers.
 //
 // Bound by memory: a row is read once, held in registers by the waves it is
 // given, and written once.
@@ -19,6 +19,12 @@
 namespace mg {
 
 typedef int i32x2 __attribute__((ext_vector_type(2)));
+
+// Vectors at any element: the hardware takes any alignment, and where rows are
+// 16-byte aligned the accesses are.
+typedef i32x4 i32x4_any __attribute__((aligned(2)));
+typedef i32x2 i32x2_any __attribute__((aligned(1)));
+typedef int int_any __attribute__((aligned(1)));
 
 struct Quant {
     const char* x;        // rows of x (quantising) or of q (restoring)
@@ -98,18 +104,33 @@ struct RowScale {
     }
 };
 
+// The value as it stands, rounded to fp32: the compiler may otherwise join the
+// product that it comes from with what follows, an addition or a conversion to
+// 16 bits, and round only there.
+__device__ __forceinline__ float settled(float v)
+{
+    asm("" : "+v"(v));
+    return v;
+}
+
 // One value's integer, in the low byte (the others hold anything).
 template <In T>
 __device__ __forceinline__ uint32_t quantize_one(float x, const RowScale& r)
 {
-    const float a = x * r.mul;
+    const float a = settled(x * r.mul);
     float t = a * r.inv;
     t = __builtin_fmaf(__builtin_fmaf(-t, r.top, a), r.inv, t);
     // Adding 3 * 2^22 rounds to an integer (to even), whose low bits are the sum's.
     float n = t + 12582912.f;
     if constexpr (T == In::F32) {
-        if (__builtin_fabsf(t - (n - 12582912.f)) > 0.5f - 0x1p-14f)
-            n = (float)__builtin_rint(127.0 * (double)x / (double)r.wide) + 12582912.f;
+        const float i = n - 12582912.f, f = t - i;
+        if (__builtin_fabsf(f) > 0.5f - 0x1p-14f) {
+            // 127 x against half * top, both as a product and its rounding's error.
+            const float s = __builtin_copysignf(1.f, f), half = i + 0.5f * s, p = settled(half * r.top);
+            const float d = ((a - p) + (__builtin_fmaf(x, r.mul, -a) - __builtin_fmaf(half, r.top, -p))) * s;
+            const bool odd = __float_as_int(n) & 1;
+            n = d > 0.f || (d == 0.f && odd) ? n + s : n;
+        }
     }
     return (uint32_t)__float_as_int(n);
 }
@@ -122,10 +143,11 @@ __device__ __forceinline__ int pack4(uint32_t a, uint32_t b, uint32_t c, uint32_
 }
 
 template <In T>
-__device__ __forceinline__ void quantize_chunk(const i32x4& v, const RowScale& r, char* dst)
+__device__ __forceinline__ void quantize_chunk(i32x4 v, const RowScale& r, char* dst)
 {
     using Q = QuantType<T>;
     float f[Q::E];
+    asm volatile("" : "+v"(v));       // (what follows stays here: every chunk's values at once would fill the registers)
     Q::unpack(v, f);
     uint32_t n[Q::E];
 #pragma unroll
@@ -133,8 +155,8 @@ __device__ __forceinline__ void quantize_chunk(const i32x4& v, const RowScale& r
     int w[Q::E / 4];
 #pragma unroll
     for (int d = 0; d < Q::E / 4; ++d) w[d] = r.live ? pack4(n[4 * d], n[4 * d + 1], n[4 * d + 2], n[4 * d + 3]) : 0;
-    if constexpr (Q::E == 4) *(int*)dst = w[0];
-    else *(i32x2*)dst = i32x2{w[0], w[1]};
+    if constexpr (Q::E == 4) *(int_any*)dst = w[0];
+    else *(i32x2_any*)dst = i32x2{w[0], w[1]};
 }
 
 // The largest of W waves' maxima.
@@ -154,6 +176,7 @@ __device__ __forceinline__ uint32_t join_top(uint32_t m, int wave)
 }
 
 constexpr int kQuantThreads = 256;
+constexpr int kRestoreSteps = 4;
 
 // W waves a row, which hold it in U chunks of 16 bytes a lane.
 template <In T, int W, int U>
@@ -167,47 +190,44 @@ quantize_kernel(Quant p)
     if (row >= p.M) return;
     const char* const x = p.x + row * p.ldx * Q::ES;
     char* const y = p.y + row * p.ldy;
-    i32x4 v[U];
+    i32x4 v[U], last = {0, 0, 0, 0};
     uint32_t m = 0;
+    if (p.K >= E) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int k = (u * LANES + lane) * E;
-        v[u] = i32x4{0, 0, 0, 0};
-        if (k + E <= p.K) {
-            v[u] = *(const i32x4*)(x + (int64_t)k * Q::ES);
-        } else if (k < p.K) {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (k + e < p.K) {
-                    if constexpr (Q::ES == 4) v[u][e] = ((const int*)x)[k + e];
-                    else v[u][e / 2] |= (int)((uint32_t)((const uint16_t*)x)[k + e] << (16 * (e & 1)));
-                }
+        for (int u = 0; u < U; ++u) {
+            // Past the end: the first chunk again (a branch a chunk would cost 150 registers).
+            const int k = (u * LANES + lane) * E, at = k + E <= p.K ? k : 0;
+            v[u] = *(const i32x4_any*)(x + (int64_t)at * Q::ES);
         }
-    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) m = Q::top(v[u], m);
+        for (int u = 0; u < U; ++u) m = Q::top(v[u], m);
+    }
+    // What is left of a chunk at the row's end, an element a lane.
+    const int end = p.K / E * E + lane;
+    if (end < p.K) {
+        if constexpr (Q::ES == 4) last[0] = ((const int*)x)[end];
+        else last[0] = ((const uint16_t*)x)[end];
+    }
+    m = Q::top(last, m);
     const RowScale r(join_top<W>(Q::wave_top(m), wave));
     if (lane == 0) p.scales[row] = r.scale;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int k = (u * LANES + lane) * E;
-        if (k + E <= p.K) {
-            quantize_chunk<T>(v[u], r, y + k);
-        } else if (k < p.K) {
-            float f[E];
-            Q::unpack(v[u], f);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (k + e < p.K) y[k + e] = r.live ? (char)quantize_one<T>(f[e], r) : 0;
-        }
+        if (k + E <= p.K) quantize_chunk<T>(v[u], r, y + k);
+    }
+    if (end < p.K) {
+        float f[E];
+        Q::unpack(last, f);
+        y[end] = r.live ? (char)quantize_one<T>(f[0], r) : 0;
     }
 }
 
-// Rows at any element, or longer than registers hold: a workgroup a row, read
-// twice (the second time mostly from L2), element by element.
+// Rows longer than registers hold: a workgroup a row, read twice (the second
+// time mostly from L2), element by element.
 template <In T>
 __global__ void __launch_bounds__(kQuantThreads)
-quantize_any_kernel(Quant p)
+quantize_long_kernel(Quant p)
 {
     using Q = QuantType<T>;
     const int tid = threadIdx.x;
@@ -234,15 +254,6 @@ quantize_any_kernel(Quant p)
 // The fp32 value of byte e of a word.
 __device__ __forceinline__ float byte_value(int w, int e) { return (float)((w << (24 - 8 * e)) >> 24); }
 
-// The value as it stands, rounded to fp32: the compiler may otherwise round the
-// product that it comes from anew, and not always the same way, where it is
-// converted to 16 bits.
-__device__ __forceinline__ float settled(float v)
-{
-    asm("" : "+v"(v));
-    return v;
-}
-
 template <In T>
 __device__ __forceinline__ uint16_t round16(float v)
 {
@@ -250,70 +261,57 @@ __device__ __forceinline__ uint16_t round16(float v)
     else return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
-// 16 bytes of restored values a lane and step; a workgroup covers DQ_SPAN
-// columns of a row (grid x: columns, y: rows in turn).
-template <In T, bool VEC>
+// A wave takes a span of a row, 16 bytes of restored values a lane and step.
+template <In T>
 __global__ void __launch_bounds__(kQuantThreads)
 dequantize_kernel(Quant p, int spans)
 {
     using Q = QuantType<T>;
-    constexpr int E = VEC ? Q::E : 1, LANES = 64;
+    constexpr int E = Q::E, LANES = 64, U = kRestoreSteps;
     const int lane = threadIdx.x & 63;
-    const int64_t w = (int64_t)blockIdx.x * (kQuantThreads / 64) + (threadIdx.x >> 6);   // wave: a row's span
+    const int64_t w = (int64_t)blockIdx.x * (kQuantThreads / 64) + (threadIdx.x >> 6);
     const int64_t row = w / spans;
     if (row >= p.M) return;
-    constexpr int U = VEC ? 4 : 16;
     const int k0 = (int)(w % spans) * (LANES * E * U) + lane * E;
     const char* const q = p.x + row * p.ldx;
     char* const y = p.y + row * p.ldy * Q::ES;
     const float s = p.scales[row];
-    if constexpr (VEC) {
-        int v[U][E / 4];
+    int v[U][E / 4];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = k0 + u * LANES * E;
-            if (k + E > p.K) continue;
-            if constexpr (E == 4) v[u][0] = *(const int*)(q + k);
-            else {
-                const i32x2 t = *(const i32x2*)(q + k);
-                v[u][0] = t[0];
-                v[u][1] = t[1];
-            }
+    for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * LANES * E;
+        if (k + E > p.K) continue;
+        if constexpr (E == 4) {
+            v[u][0] = *(const int_any*)(q + k);
+        } else {
+            const i32x2 t = *(const i32x2_any*)(q + k);
+            v[u][0] = t[0];
+            v[u][1] = t[1];
         }
+    }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = k0 + u * LANES * E;
-            if (k + E <= p.K) {
-                i32x4 o;
+    for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * LANES * E;
+        if (k + E <= p.K) {
+            i32x4 o;
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    if constexpr (E == 4) {
-                        o[d] = __float_as_int(byte_value(v[u][0], d) * s);
-                    } else {
-                        const uint32_t lo = round16<T>(settled(byte_value(v[u][d / 2], d % 2 * 2) * s));
-                        const uint32_t hi = round16<T>(settled(byte_value(v[u][d / 2], d % 2 * 2 + 1) * s));
-                        o[d] = (int)(lo | (hi << 16));
-                    }
+            for (int d = 0; d < 4; ++d) {
+                if constexpr (E == 4) {
+                    o[d] = __float_as_int(byte_value(v[u][0], d) * s);
+                } else {
+                    const uint32_t lo = round16<T>(settled(byte_value(v[u][d / 2], d % 2 * 2) * s));
+                    const uint32_t hi = round16<T>(settled(byte_value(v[u][d / 2], d % 2 * 2 + 1) * s));
+                    o[d] = (int)(lo | (hi << 16));
                 }
-                *(i32x4*)(y + (int64_t)k * Q::ES) = o;
-            } else {
-                for (int e = 0; e < E; ++e)
-                    if (k + e < p.K) {
-                        const float f = settled((float)(signed char)q[k + e] * s);
-                        if constexpr (Q::ES == 4) ((float*)y)[k + e] = f;
-                        else ((uint16_t*)y)[k + e] = round16<T>(f);
-                    }
             }
-        }
-    } else {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = k0 + u * LANES;
-            if (k < p.K) {
-                const float f = settled((float)(signed char)q[k] * s);
-                if constexpr (Q::ES == 4) ((float*)y)[k] = f;
-                else ((uint16_t*)y)[k] = round16<T>(f);
-            }
+            *(i32x4_any*)(y + (int64_t)k * Q::ES) = o;
+        } else {
+            for (int e = 0; e < E; ++e)
+                if (k + e < p.K) {
+                    const float f = settled((float)(signed char)q[k + e] * s);
+                    if constexpr (Q::ES == 4) ((float*)y)[k + e] = f;
+                    else ((uint16_t*)y)[k + e] = round16<T>(f);
+                }
         }
     }
 }

@@ -49,6 +49,40 @@ mg::Params params(int64_t M, int64_t N, int64_t K, const void* A, const void* B,
     return p;
 }
 
+// Launches a product, its thin last rows and columns (i8_edges) after the rest.
+hipError_t launch_parts(mg::I8Call q, int type, int eo, hipStream_t s)
+{
+    const mg::I8Edges edges = mg::i8_edges(mg::shape_of(q));
+    // The last `left` rows or columns, which q loses.
+    auto cut = [&](bool rows, int64_t left) {
+        mg::I8Call rest = q;
+        mg::Params& p = rest.p;
+        const int64_t at = (rows ? p.M : p.N) - left;
+        (rows ? q.p.M : q.p.N) = (int)at;
+        (rows ? p.M : p.N) = (int)left;
+        if (rows) {
+            p.A += at * p.lda;
+            p.a_bytes -= (uint64_t)(at * p.lda);
+            if (rest.s.a) rest.s.a += at;
+        } else {
+            p.B += at * p.ldb;
+            p.b_bytes -= (uint64_t)(at * p.ldb);
+            if (rest.s.b) rest.s.b += at;
+            if (p.bias) p.bias += at;
+        }
+        p.C += (rows ? at * p.ldc : at) * eo;
+        p.c_vec = p.c_vec && (uintptr_t)p.C % 16 == 0;
+        return rest;
+    };
+    mg::I8Call parts[2];
+    int n = 0;
+    if (edges.rows) parts[n++] = cut(true, edges.rows);
+    if (edges.cols) parts[n++] = cut(false, edges.cols);
+    hipError_t e = kLaunch[type](q, s);
+    for (int i = 0; i < n && e == hipSuccess; ++i) e = kLaunch[type](parts[i], s);
+    return e;
+}
+
 int run(int64_t M, int64_t N, int64_t K, char a, char b, char c, int type, const int8_t* A, const int8_t* B, void* C,
         int64_t lda, int64_t ldb, int64_t ldc, const float* scale_a, const float* scale_b, const gemm_epilogue_t* epi,
         void* stream)
@@ -94,7 +128,8 @@ int run(int64_t M, int64_t N, int64_t K, char a, char b, char c, int type, const
     const mg::I8Shape shape = mg::shape_of(q);
     const mg::Tile& tile = mg::kI8Tiles[(int)mg::i8_tile(shape)];
     if (mg::i8_grid(shape, tile) > mg::kMaxGridThreads / tile.threads) return GEMM_ERR_BAD_SHAPE;
-    const int st = kLaunch[type](q, (hipStream_t)stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
+    hipError_t e = launch_parts(q, type, eo, (hipStream_t)stream);
+    const int st = e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
     if (mg::log_enabled())
         std::fprintf(stderr, "mi355_gemm: i8 %s M=%lld N=%lld K=%lld %s\n", kTypeNames[type], (long long)M, (long long)N,
                      (long long)K, gemm_status_str(st));

@@ -2,6 +2,8 @@
 // of its grid (host only; no HIP).
 #pragma once
 
+#include <initializer_list>
+
 #include "gemm_tiles.hpp"
 
 namespace mg {
@@ -72,6 +74,38 @@ inline I8Tile i8_tile(const I8Shape& s)
 }
 
 inline int64_t i8_grid(const I8Shape& s, const Tile& t) { return ceil_div(s.M, t.bm) * ceil_div(s.N, t.bn); }
+
+// C's last columns and rows, up to 16 past a multiple of 128, can go to calls of
+// their own behind the rest: where that saves the CUs a round of tiles, or lets a
+// smaller tile do, and what it saves is more than such a call's 5 to 12 us (20 *
+// 2^20 of a tile's products; the unaligned 128x128 tile runs twice a CU).
+// us, in brackets without: 8193 x 4096 x 4096 133 (159); 2049 rows of it 45.5
+// (51.2); 4100 x 4104 x 2048 54 (66); 4095 x 2049 x 1028 into fp32 28.1 (34.9);
+// unaligned 38.0 (41.1), 2048 x 4100 x 4096 83 (97).
+inline int64_t i8_cost(const I8Shape& s)
+{
+    const Tile& t = kI8Tiles[(int)i8_tile(s)];
+    const int64_t a_cu = !s.vec && t.bm == 128 ? 2 : 1;
+    return ceil_div(i8_grid(s, t), 256 * a_cu) * a_cu * t.bm * t.bn * s.K;
+}
+struct I8Edges {
+    int64_t rows, cols;
+};
+inline I8Edges i8_edges(const I8Shape& s)
+{
+    const int64_t call = 20 << 20;
+    const int64_t m = s.M > 128 && s.M % 128 <= 16 ? s.M % 128 : 0, n = s.N > 128 && s.N % 128 <= 16 ? s.N % 128 : 0;
+    I8Edges best = {0, 0};
+    int64_t least = i8_cost(s);
+    for (const I8Edges e : {I8Edges{0, n}, I8Edges{m, 0}, I8Edges{m, n}}) {
+        const int64_t cost = i8_cost({s.vec, s.M - e.rows, s.N - e.cols, s.K}) + call * ((e.rows != 0) + (e.cols != 0));
+        if (cost < least) {
+            least = cost;
+            best = e;
+        }
+    }
+    return best;
+}
 
 // ------------------------------------------------------------ gradients from 8-bit values
 

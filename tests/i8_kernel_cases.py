@@ -22,3 +22,8 @@ def gradients(wide, split_a, aligned):
     else:
         more = [("128x128", 2304, 1950), ("256x128", 2600, 1950) if wide else ("256x256", 3300, 3100)]
     return _GRADIENTS + more
+
+
+# aligned, M, N, K; rows and columns at the end that a call of their own computes
+EDGES = [(True, 2049, 4100, 2048, 1, 4), (True, 2053, 4096, 2048, 5, 0), (True, 2048, 4112, 2047, 0, 16),
+         (False, 2050, 4100, 1501, 2, 4), (False, 2048, 4100, 1501, 0, 4), (True, 2060, 4110, 1041, 0, 0)]

@@ -442,6 +442,15 @@ def test_every_product_kernel(dtype, name, M, N):
         Product(M, N, 384, dtype, 1, 3).run_epilogue(0.5, 0.25, True, g.GEMM_ACT_GELU)
 
 
+@pytest.mark.parametrize("dtype", WIDE)
+@pytest.mark.parametrize("aligned,M,N,K,rows,cols", cases.EDGES)
+def test_thin_edges(dtype, aligned, M, N, K, rows, cols):
+    at = (None, 0) if aligned else (1, 3)
+    Product(M, N, K, dtype, *at).run()
+    Product(M, N, K, dtype, *at, scaled=False, lo=-1).run()
+    Product(M, N, K, dtype, *at).run_epilogue(0.5, 0.25, True, g.GEMM_ACT_GELU)
+
+
 def _gradient_kernels():
     out = []
     for dtype in PAIRS:

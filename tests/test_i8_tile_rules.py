@@ -25,6 +25,11 @@ int main(int argc, char**)
     while (std::scanf("%15s %d %d %d %lld %lld %lld", kind, &vec, &wide, &split, &M, &N, &K) == 7) {
         const mg::I8Shape s = {!!vec, M, N, K};
         const mg::GradShape g = {!!vec, !!wide, !!split, M, N, K};
+        if (!std::strcmp(kind, "edges")) {
+            const mg::I8Edges e = mg::i8_edges(s);
+            std::printf("%d %d\n", (int)e.rows, (int)e.cols);
+            continue;
+        }
         const mg::Tile& t = std::strcmp(kind, "i8") ? mg::kGradTiles[(int)mg::grad_tile(g)] : mg::kI8Tiles[(int)mg::i8_tile(s)];
         std::printf("%s\n", t.name);
     }
@@ -72,3 +77,16 @@ def test_no_size_runs_out_of_rules(ask):
              for wide, split in ((False, False), (True, False), (True, True)) for M in sizes for N in sizes]
     known = {n.split(" ", 1)[1] for n in ask()}
     assert set(ask(lines)) <= known
+
+
+def test_the_tests_of_thin_edges_have_them(ask):
+    got = ask([("edges", aligned, False, False, M, N, K) for aligned, M, N, K, _, _ in cases.EDGES])
+    assert got == [f"{rows} {cols}" for _, _, _, _, rows, cols in cases.EDGES]
+
+
+def test_edges_are_never_the_whole(ask):
+    sizes = [1, 16, 100, 128, 129, 144, 257, 1000, 4097, 30000]
+    lines = [("edges", vec, False, False, M, N, K) for vec in (False, True) for M in sizes for N in sizes for K in (0, 1, 4096, 131071)]
+    for (_, _, _, _, M, N, _), line in zip(lines, ask(lines)):
+        rows, cols = map(int, line.split())
+        assert 0 <= rows <= 16 and 0 <= cols <= 16 and rows < M and cols < N

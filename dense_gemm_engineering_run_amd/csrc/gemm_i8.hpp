@@ -111,8 +111,33 @@ gemm_i8_pp_kernel(Params p, I8Scales sc)
     PP::store(p, smem, m0, n0, acc, lane, wave);
 }
 
-// Few rows: Skinny's streams, whose waves take the k-tiles in turn; their
-// integer sums meet in LDS.
+// Waves that hold sums of the same BM x BN tile, each over its own k: the sums of
+// all of them, finished and stored.
+template <Out TO, int BM, int BN, int NW>
+__device__ __forceinline__ void i8_join(const Params& p, const I8Scales& sc, int* part, int m0, int n0,
+                                        const f32x4 (&acc)[BM / 16][BN / 16], int tid, int lane, int wave)
+{
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < BM / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < BN / 16; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                part[wave * BM * BN + (i * 16 + lane / 16 * 4 + e) * BN + j * 16 + lane % 16] = __float_as_int(acc[i][j][e]);
+    __syncthreads();
+    for (int x = tid; x < BM * BN; x += NW * 64) {
+        const int m = m0 + x / BN, n = n0 + x % BN;
+        if (m >= p.M || n >= p.N) continue;
+        int v = part[x];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) v += part[w * BM * BN + x];
+        store_out<TO>(p.C, (int64_t)m * p.ldc + n,
+                      i8_value<TO>(p, m, n, __int_as_float(v), sc.a ? sc.a[m] : 1.f, sc.b ? sc.b[n] : 1.f));
+    }
+}
+
+// Few rows: Skinny's streams, whose waves take the k-tiles in turn.
 template <Out TO, int MT, int NT, int NW, int ST>
 __global__ void __launch_bounds__(NW * 64)
 gemm_i8_stream_kernel(Params p, I8Scales sc)
@@ -127,25 +152,7 @@ gemm_i8_stream_kernel(Params p, I8Scales sc)
     typename T::Acc acc;
     T::zero(acc);
     T::stream(p, smem, m0, n0, acc, lane, wave);
-    __syncthreads();
-    int* const part = (int*)smem;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                part[wave * T::PART + (i * 16 + lane / 16 * 4 + e) * (NT * 16) + j * 16 + lane % 16] = __float_as_int(acc[i][j][e]);
-    __syncthreads();
-    for (int x = tid; x < T::PART; x += NW * 64) {
-        const int m = m0 + x / (NT * 16), n = n0 + x % (NT * 16);
-        if (m >= p.M || n >= p.N) continue;
-        int v = part[x];
-#pragma unroll
-        for (int w = 1; w < NW; ++w) v += part[w * T::PART + x];
-        store_out<TO>(p.C, (int64_t)m * p.ldc + n,
-                      i8_value<TO>(p, m, n, __int_as_float(v), sc.a ? sc.a[m] : 1.f, sc.b ? sc.b[n] : 1.f));
-    }
+    i8_join<TO, T::PART / (NT * 16), NT * 16, NW>(p, sc, (int*)smem, m0, n0, acc, tid, lane, wave);
 }
 
 // ------------------------------------------------------------ operands at any byte
@@ -270,6 +277,65 @@ gemm_i8_odd_kernel(Params p, I8Scales sc)
     store_tile<KT, false>(p, smem, m0, n0, acc, tid, lane, wave);
 }
 
+// Few of their tiles: the waves take the k-tiles in turn, each through LDS of its
+// own with nothing to wait for but itself.
+template <Out TO, int BM, int BN, int NW, int D>
+__global__ void __launch_bounds__(NW * 64)
+gemm_i8_odd_stream_kernel(Params p, I8Scales sc)
+{
+    constexpr int BK = 64, KB = 2 * BK;
+    using KT = Dma16<In::I8, TO, BM, BN, BK, 1, 1, 16, 2, true, true>;
+    constexpr int STAGE = KT::STAGE, PART = BM * BN * 4, SMEM = NW * (STAGE > PART ? STAGE : PART);
+    static_assert(SMEM <= 160 * 1024, "LDS budget");
+    __shared__ __attribute__((aligned(1024))) char smem[SMEM];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tm, tn;
+    tile_coords(p, tm, tn);
+    const int m0 = __builtin_amdgcn_readfirstlane(tm) * BM, n0 = __builtin_amdgcn_readfirstlane(tn) * BN;
+    const int nkt = (p.K + KB - 1) / KB;
+    typename KT::Acc acc;
+    KT::zero(acc);
+    ByteOperand<BM, BK, 1, D> oa;
+    ByteOperand<BN, BK, 1, D> ob;
+    oa.init(0, lane, p.lda, p.A);
+    ob.init(0, lane, p.ldb, p.B);
+    auto load = [&](int t, int d) {               // past the end: empty extents
+        oa.load(d, p.A, t < nkt ? p.a_bytes : 0, p.lda, m0, t * KB);
+        ob.load(d, p.B, t < nkt ? p.b_bytes : 0, p.ldb, n0, t * KB);
+    };
+    char* const sa = smem + wave * STAGE;
+    char* const sb = sa + KT::OA::BYTES;
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(wave + d * NW, d);
+    for (int t0 = wave; t0 < nkt; t0 += D * NW) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const int t = t0 + d * NW;
+            if (t >= nkt) break;
+            oa.store(d, sa, t * KB, p.K, 0, lane);
+            ob.store(d, sb, t * KB, p.K, 0, lane);
+            load(t + D * NW, d);
+            __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): written
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int g = 0; g < KT::NG; ++g) {
+                i32x4 fa[KT::TM], fb[KT::TN];
+#pragma unroll
+                for (int i = 0; i < KT::TM; ++i) fa[i] = KT::OA::template frag<16>(sa, i * 16, g * 32, lane);
+#pragma unroll
+                for (int j = 0; j < KT::TN; ++j) fb[j] = KT::OB::template frag<16>(sb, j * 16, g * 32, lane);
+#pragma unroll
+                for (int i = 0; i < KT::TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < KT::TN; ++j) mfma_step<In::I8, 16>(fa[i], fb[j], acc[i][j]);
+            }
+            __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): read, the next tile may be written
+            asm volatile("" ::: "memory");
+        }
+    }
+    i8_join<TO, BM, BN, NW>(p, sc, (int*)smem, m0, n0, acc, tid, lane, wave);
+}
+
 // ------------------------------------------------------------------ launchers
 
 // What the host asks of an output type's launchers (gemm_i8_<type>.hip).
@@ -318,6 +384,12 @@ struct I8Inst {
         constexpr Tile t = tile_of(T);
         return run(&gemm_i8_odd_kernel<TO, t.bm, t.bn, t.bk, t.wm, t.wn, t.stages>, c, t, s);
     }
+    template <I8Tile T>
+    static hipError_t odd_stream(const I8Call& c, hipStream_t s)
+    {
+        constexpr Tile t = tile_of(T);
+        return run(&gemm_i8_odd_stream_kernel<TO, t.bm, t.bn, t.extra, t.stages>, c, t, s);
+    }
     static hipError_t launch(const I8Call& c, hipStream_t s)
     {
         constexpr Tile pp = tile_of(I8Tile::PingPong);
@@ -331,6 +403,8 @@ struct I8Inst {
         case I8Tile::Dma128x128: return dma<I8Tile::Dma128x128>(c, s);
         case I8Tile::Dma128x256: return dma<I8Tile::Dma128x256>(c, s);
         case I8Tile::PingPong: return run(&gemm_i8_pp_kernel<TO, pp.bm, pp.bn, pp.bk, pp.wm, pp.wn, pp.mi>, c, pp, s);
+        case I8Tile::OddStream16x16: return odd_stream<I8Tile::OddStream16x16>(c, s);
+        case I8Tile::OddStream32x32: return odd_stream<I8Tile::OddStream32x32>(c, s);
         case I8Tile::Odd32x32: return odd<I8Tile::Odd32x32>(c, s);
         case I8Tile::Odd64x64: return odd<I8Tile::Odd64x64>(c, s);
         case I8Tile::Odd128x128: return odd<I8Tile::Odd128x128>(c, s);

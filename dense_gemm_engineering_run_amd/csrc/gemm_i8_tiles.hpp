@@ -11,7 +11,7 @@ namespace mg {
 // bk counts pairs of 8-bit values.
 enum class I8Tile : int {
     Stream16x16, Stream16x32, Stream32x32, Dma32x64, Dma64x64, Dma64x128, Dma128x128, Dma128x256, PingPong,
-    Odd32x32, Odd64x64, Odd128x128,
+    OddStream16x16, OddStream32x32, Odd32x32, Odd64x64, Odd128x128,
     Count
 };
 constexpr Tile kI8Tiles[] = {
@@ -24,6 +24,8 @@ constexpr Tile kI8Tiles[] = {
     {"128x128", 128, 128, 64, 2, 4, 16, 4, 0, 512},
     {"128x256", 128, 256, 64, 2, 4, 16, 3, 0, 512},
     {"ping-pong 256x256", 256, 256, 64, 4, 2, 16, 3, 0, 512},
+    {"unaligned stream 16x16", 16, 16, 0, 1, 1, 16, 4, 8, 512},
+    {"unaligned stream 32x32", 32, 32, 0, 1, 1, 16, 2, 8, 512},
     {"unaligned 32x32", 32, 32, 128, 2, 2, 16, 2, 0, 256},
     {"unaligned 64x64", 64, 64, 64, 2, 4, 16, 2, 0, 512},
     {"unaligned 128x128", 128, 128, 64, 2, 4, 16, 2, 0, 512},
@@ -53,13 +55,19 @@ struct I8Shape {
 //   8192  K 1024                                                          56.0    53.4
 //   8192                                                                 147.7   125.3
 // (The first three stream: the waves share a tile's k.)
-// Unaligned: 32x32 / 64x64 / 128x128 took 14.2 / 25.7 / 35.4 for one row of 4095
-// x 4095, 10.9 / 15.3 / 23.8 for 300 of 1023 x 2047, - / 44.8 / 38.2 for 4095 of
-// 2049 x 1028.
+// Unaligned, us:              16x16 str. 32x32 str.  32x32   64x64  128x128
+//      1 of 4095 x 4095           8.1      10.1       14.4    26.1    35.4
+//     40 of 4095 x 4095          16.6      11.2       14.8    26.3
+//    300 of 1023 x 2047          19.5      14.5       10.6    15.2    23.8
+//   1500 of 1025 x 4095                               50.7    39.3    42.0
+//   4095 of 2049 x 1028                                       44.8    38.2
+//   3000 of 4095 x 2047                              156      87.0    54.5
 inline I8Tile i8_tile(const I8Shape& s)
 {
     auto tiles = [&](int bm, int bn) { return ceil_div(s.M, bm) * ceil_div(s.N, bn); };
     if (!s.vec) {
+        if (tiles(16, 16) <= 256) return I8Tile::OddStream16x16;
+        if (tiles(32, 32) <= 256) return I8Tile::OddStream32x32;
         if (tiles(32, 32) <= 512) return I8Tile::Odd32x32;
         return tiles(64, 64) <= 512 ? I8Tile::Odd64x64 : I8Tile::Odd128x128;
     }
@@ -81,7 +89,7 @@ inline int64_t i8_grid(const I8Shape& s, const Tile& t) { return ceil_div(s.M, t
 // 2^20 of a tile's products; the unaligned 128x128 tile runs twice a CU).
 // us, in brackets without: 8193 x 4096 x 4096 133 (159); 2049 rows of it 45.5
 // (51.2); 4100 x 4104 x 2048 54 (66); 4095 x 2049 x 1028 into fp32 28.1 (34.9);
-// unaligned 38.0 (41.1), 2048 x 4100 x 4096 83 (97).
+// unaligned 35.0 (41.1), 2048 x 4100 x 4096 83 (97).
 inline int64_t i8_cost(const I8Shape& s)
 {
     const Tile& t = kI8Tiles[(int)i8_tile(s)];

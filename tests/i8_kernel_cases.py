@@ -7,7 +7,8 @@ PRODUCTS = [
     ("32x64", 40, 8000), ("64x64", 60, 16000), ("64x128", 500, 4000), ("128x128", 1000, 4000), ("128x256", 2000, 4000),
     ("ping-pong 256x256", 2050, 4100),
 ]
-PRODUCTS_UNALIGNED = [("unaligned 32x32", 100, 300), ("unaligned 64x64", 1000, 1000), ("unaligned 128x128", 1500, 2100)]
+PRODUCTS_UNALIGNED = [("unaligned stream 16x16", 40, 300), ("unaligned stream 32x32", 100, 1000), ("unaligned 32x32", 300, 1000),
+                      ("unaligned 64x64", 1000, 1000), ("unaligned 128x128", 1500, 2100)]
 
 _GRADIENTS = [("stream 32x32", 100, 200), ("stream 32x64", 500, 600), ("64x64", 1000, 1000), ("64x128", 1000, 2000),
               ("128x128, 64 deep", 2000, 2000)]

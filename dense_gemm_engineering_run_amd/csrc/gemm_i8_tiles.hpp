@@ -123,7 +123,7 @@ enum class GradTile : int {
     Stream32x32, Stream32x64, T64x64, T64x128, T64x128Two, T128x128Deep, T128x128, T256x256, Tall256x128, Wide128x256, Count
 };
 constexpr Tile kGradTiles[] = {
-    {"stream 32x32", 32, 32, 64, 1, 1, 16, 2, 8, 512},
+    {"stream 32x32", 32, 32, 64, 1, 1, 16, 1, 8, 512},
     {"stream 32x64", 32, 64, 32, 1, 1, 16, 2, 8, 512},
     {"64x64", 64, 64, 128, 2, 4, 16, 2, 2, 512},
     {"64x128", 64, 128, 64, 2, 4, 16, 2, 2, 512},
@@ -148,8 +148,8 @@ struct GradShape {
 // that the largest that fills most of them.  us, bf16 into bf16 / bf16 into fp32
 // / fp32, A m-major (k-major is within a few percent):
 //   M x N, K              32x32 str.   32x64 str.    64x64        64x128       128x128, 64 deep
-//    512 x  256, 1000    6.7/8.3/9.1  7.7/10/9.6   9.1/13/16    12/21/19
-//     32 x 4096, 4096    13/17/19     15/26/22      25/42/50
+//    512 x  256, 1000    6.1/7.2/7.7  7.7/10/9.6   9.1/13/16    12/21/19
+//     32 x 4096, 4096    12/16/18     15/26/22      25/42/50
 //   1024 x  512, 1024    9.6/14/16    7.9/11/10     9.2/14/16
 //   1024 x 1024, 4096    39/64/77     28/52/44      24/44/50     38/71/65       51/98/109
 //   2048 x 1024, 4096                               41/83/97     38/71/66       51/100/110

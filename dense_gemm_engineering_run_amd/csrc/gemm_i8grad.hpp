@@ -191,6 +191,28 @@ struct QOperand {
     }
 };
 
+// Physical 16-byte chunk of chunk c of a k-contiguous row in LDS.  As swz_chunk,
+// but for rows of 4 chunks, where a read's lanes go by fours of rows in the order
+// 0 3 1 2 with the next chunk in the latter two: XOR with 0 3 2 1 keeps those on
+// different banks too (swz_chunk's 0 1 2 3 cost 6 % of the cycles of the
+// k-major 256x256 tile).
+template <int CPR>
+__device__ __forceinline__ int grad_chunk(int row, int c)
+{
+    if constexpr (CPR == 4) return c ^ (-(row / 4) & 3);
+    else return swz_chunk<CPR, true>(row, c);
+}
+template <class LDS, bool KMAJ>
+__device__ __forceinline__ i32x4 a_frag(const char* t, int rbase, int kb, int lane)
+{
+    if constexpr (KMAJ) {
+        const int row = rbase + lane % 16;
+        return *(const i32x4*)(t + row * LDS::RB + grad_chunk<LDS::CPR>(row, kb / 8 + lane / 16) * 16);
+    } else {
+        return LDS::template frag<16>(t, rbase, kb, lane);
+    }
+}
+
 // A: 16-bit values as they are, or (SPLIT) fp16 and fp32 ones times scales[k] in
 // three bf16 terms.
 template <In TI, int ROWS, int BK, int NW, bool KMAJ, bool SPLIT, bool VEC, int D>
@@ -206,16 +228,15 @@ struct AOperand {
     // k of a slot's first value within the tile.
     __device__ static __forceinline__ int k_of(int slot)
     {
-        return KMAJ ? swz_chunk<LDS::CPR, true>(slot / LDS::CPR, slot % LDS::CPR) * 8 : slot / LDS::RCH;
+        return KMAJ ? grad_chunk<LDS::CPR>(slot / LDS::CPR, slot % LDS::CPR) * 8 : slot / LDS::RCH;
     }
     __device__ __forceinline__ void init(int wave, int lane, int64_t ld)
     {
-        LDS o;
-        o.init(wave, lane, 0);
 #pragma unroll
         for (int j = 0; j < LDS::IPW; ++j) {
-            const int slot = (wave * LDS::IPW + j) * 64 + lane;
-            voff[j] = (int)((KMAJ ? slot / LDS::CPR : slot / LDS::RCH) * ld * ES) + o.voff[j] * (ES / 2);
+            const int slot = (wave * LDS::IPW + j) * 64 + lane, k = slot / LDS::RCH;
+            voff[j] = KMAJ ? (int)(slot / LDS::CPR * ld * ES) + k_of(slot) * ES
+                           : (int)(k * ld * ES) + (slot % LDS::RCH ^ LDS::mkey(k)) * 8 * ES;
         }
     }
     __device__ __forceinline__ void load(int d, const GradParams& g, int row0, int k0, int wave, int lane)
@@ -351,7 +372,7 @@ gemm_i8grad_kernel(GradParams g)
                     for (int s = 0; s < TA; ++s)
 #pragma unroll
                         for (int i = 0; i < KT::TM; ++i)
-                            fa[x % F][s][i] = KT::OA::template frag<16>(sa + s * KT::OA::BYTES, wm * KT::WTM + i * 16, x * 32, lane);
+                            fa[x % F][s][i] = a_frag<typename KT::OA, AK>(sa + s * KT::OA::BYTES, wm * KT::WTM + i * 16, x * 32, lane);
 #pragma unroll
                     for (int s = 0; s < TQ; ++s)
 #pragma unroll
@@ -448,7 +469,7 @@ gemm_i8grad_stream_kernel(GradParams g)
                 for (int s = 0; s < TA; ++s)
 #pragma unroll
                     for (int i = 0; i < KT::TM; ++i)
-                        fa[s][i] = KT::OA::template frag<16>(sa + s * KT::OA::BYTES, i * 16, x * 32, lane);
+                        fa[s][i] = a_frag<typename KT::OA, AK>(sa + s * KT::OA::BYTES, i * 16, x * 32, lane);
 #pragma unroll
                 for (int s = 0; s < TQ; ++s)
 #pragma unroll

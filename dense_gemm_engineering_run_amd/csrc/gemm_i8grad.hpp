@@ -78,18 +78,35 @@ __device__ __forceinline__ void split8(float (&v)[8], i32x4 (&t)[3])
         }
 }
 
-// The resource of what is left of an operand from `origin` on, an element of
-// it; not live: of nothing.  Scalar throughout (64-bit comparisons are not).
-// ALIGN: from the word that holds the first byte to the end of the last one.
+// An operand from one k-tile to the next: its resource begins at the tile and
+// ends with the operand.  Scalar throughout (64-bit comparisons are not, and
+// forming the resources anew from the tile's index took 150 cycles a tile).
+// ALIGN: from the word that holds the first byte to the end of the last one;
+// steps are multiples of 4 bytes.
 template <bool ALIGN>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rest(const char* base, uint64_t bytes, int64_t origin, bool live)
-{
-    const uint64_t at = (uint64_t)base + (uint64_t)origin, lead = ALIGN ? at & 3 : 0;
-    uint64_t n = bytes - (uint64_t)origin + lead;
-    if (ALIGN) n = (n + 3) & ~(uint64_t)3;
-    const uint32_t lo = (uint32_t)(n >> 32) != 0 ? 0xffffffffu : (uint32_t)n;
-    return __builtin_amdgcn_make_buffer_rsrc((void*)(at - lead), (short)0, live ? (int)lo : 0, kBufferFlags);
-}
+struct Walk {
+    uint64_t at, left;
+    int64_t step;
+    __device__ __forceinline__ void init(const char* base, uint64_t bytes, int64_t origin, int64_t step_)
+    {
+        const uint64_t first = (uint64_t)base + (uint64_t)origin, lead = ALIGN ? first & 3 : 0;
+        at = first - lead;
+        left = bytes - (uint64_t)origin + lead;
+        if (ALIGN) left = (left + 3) & ~(uint64_t)3;
+        step = step_;
+    }
+    // Not live: nothing is left.
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t next(bool live)
+    {
+        uint32_t high = (uint32_t)(left >> 32);
+        asm("" : "+s"(high));                     // (the compiler would make it one 64-bit comparison again)
+        const uint32_t n = high != 0 ? 0xffffffffu : (uint32_t)left;
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)at, (short)0, live ? (int)n : 0, kBufferFlags);
+        at += (uint64_t)step;
+        left -= (uint64_t)step;
+        return r;
+    }
+};
 
 // Eight bytes of a row: from any byte (three words, shifted), or 8-byte aligned.
 template <bool VEC>
@@ -134,59 +151,72 @@ struct HalfChunk<true> {
 // The operands: k-tiles from memory to registers, D tiles ahead, and from there
 // to LDS as DmaOperand lays them out, a tile a term.
 
-// Q: k rows of ROWS bytes to [BK][ROWS] values, exact or times scales[k].
+// Q: k rows of ROWS bytes to [BK][ROWS] values, exact or times scales[k].  A lane
+// loads what makes one 16-byte chunk of values, or two, side by side (their XOR
+// keys are even).
 template <In MT, int ROWS, int BK, int NW, int TERMS, bool SCALED, bool VEC, int D>
 struct QOperand {
     using LDS = DmaOperand<ROWS, BK, NW, false, 16>;
-    int voff[LDS::IPW];
+    static constexpr bool PAIR = VEC && LDS::IPW % 2 == 0;
+    static constexpr int W = PAIR ? 2 : 1, UNITS = LDS::IPW / W, PER_ROW = LDS::RCH / W;
+    int voff[UNITS];
     ByteChunk8<VEC> q[D][LDS::IPW];
-    float s[D][LDS::IPW];
+    float s[D][UNITS];
+    Walk<!VEC> walk;
+    Walk<false> walk_s;
 
-    __device__ static __forceinline__ int slot(int wave, int lane, int j) { return (wave * LDS::IPW + j) * 64 + lane; }
-    __device__ __forceinline__ void init(int wave, int lane, int64_t ld)
+    __device__ static __forceinline__ int unit(int wave, int lane, int j) { return (wave * UNITS + j) * 64 + lane; }
+    // From the tile at k0 on, `every` tiles at a time.
+    __device__ __forceinline__ void init(int wave, int lane, const GradParams& g, int row0, int k0, int every)
     {
-#pragma unroll
-        for (int j = 0; j < LDS::IPW; ++j) {
-            const int k = slot(wave, lane, j) / LDS::RCH, phys = slot(wave, lane, j) % LDS::RCH;
-            voff[j] = (int)(k * ld) + (phys ^ LDS::mkey(k)) * 8;
-        }
-    }
-    // Rows from K on lie past the extent and read as zeros, scale included.
-    __device__ __forceinline__ void load(int d, const GradParams& g, int row0, int k0, int wave, int lane)
-    {
-        const bool live = k0 < g.p.K;
         const int64_t origin = (int64_t)k0 * g.p.ldb + row0;
         const int lead = VEC ? 0 : (int)((uint64_t)(g.p.B + origin) & 3);
-        const __amdgpu_buffer_rsrc_t r = rest<!VEC>(g.p.B, g.p.b_bytes, origin, live);
-        const __amdgpu_buffer_rsrc_t rs = rest<false>((const char*)g.scales, (uint64_t)g.p.K * 4, (int64_t)k0 * 4, live);
 #pragma unroll
-        for (int j = 0; j < LDS::IPW; ++j) {
-            q[d][j].load(r, voff[j] + lead);
+        for (int j = 0; j < UNITS; ++j) {
+            const int k = unit(wave, lane, j) / PER_ROW, phys = unit(wave, lane, j) % PER_ROW;
+            voff[j] = (int)(k * g.p.ldb) + (phys * W ^ LDS::mkey(k)) * 8 + lead;
+        }
+        walk.init(g.p.B, g.p.b_bytes, origin, (int64_t)every * BK * g.p.ldb);
+        walk_s.init((const char*)g.scales, (uint64_t)g.p.K * 4, (int64_t)k0 * 4, (int64_t)every * BK * 4);
+    }
+    // Rows from K on lie past the extent and read as zeros, scale included.
+    __device__ __forceinline__ void load(int d, bool live, int wave, int lane)
+    {
+        const __amdgpu_buffer_rsrc_t r = walk.next(live), rs = walk_s.next(live);
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            if constexpr (PAIR) {
+                const i32x4 v = buf_load16(r, voff[j]);
+                q[d][2 * j].w = i32x2{v[0], v[1]};
+                q[d][2 * j + 1].w = i32x2{v[2], v[3]};
+            } else {
+                q[d][j].load(r, voff[j]);
+            }
             if constexpr (SCALED)
-                s[d][j] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, slot(wave, lane, j) / LDS::RCH * 4, 0, 0));
+                s[d][j] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, unit(wave, lane, j) / PER_ROW * 4, 0, 0));
         }
     }
-    __device__ __forceinline__ void store(int d, const GradParams& g, char* tile, int row0, int k0, int wave, int lane) const
+    __device__ __forceinline__ void store(int d, const GradParams& g, char* tile, int k0, int wave, int lane) const
     {
-        const int lead = VEC ? 0 : (int)((uint64_t)(g.p.B + (int64_t)k0 * g.p.ldb + row0) & 3);
 #pragma unroll
         for (int j = 0; j < LDS::IPW; ++j) {
+            const int u = j / W, chunk = unit(wave, lane, u) * W + j % W;
             int w[2];
-            q[d][j].get(voff[j] + lead, w[0], w[1]);
+            q[d][j].get(voff[u], w[0], w[1]);
             if constexpr (!VEC) {
                 // The words at the last row's end can hold bytes of what follows it.
-                if (k0 + slot(wave, lane, j) / LDS::RCH >= g.p.K) w[0] = w[1] = 0;
+                if (k0 + chunk / LDS::RCH >= g.p.K) w[0] = w[1] = 0;
             }
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 v[e] = byte_value(w[e / 4], e % 4);
-                if constexpr (SCALED) v[e] *= s[d][j];
+                if constexpr (SCALED) v[e] *= s[d][u];
             }
             i32x4 t[TERMS];
             split8<MT>(v, t);
 #pragma unroll
-            for (int x = 0; x < TERMS; ++x) *(i32x4*)(tile + x * LDS::BYTES + slot(wave, lane, j) * 16) = t[x];
+            for (int x = 0; x < TERMS; ++x) *(i32x4*)(tile + x * LDS::BYTES + chunk * 16) = t[x];
         }
     }
 };
@@ -224,29 +254,34 @@ struct AOperand {
     i32x4 wide[WIDE ? D : 1][WIDE ? LDS::IPW : 1][2];
     HalfChunk<VEC> half[WIDE ? 1 : D][WIDE ? 1 : LDS::IPW];
     float s[SPLIT ? D : 1][LDS::IPW][NS ? NS : 1];
+    Walk<!VEC && !WIDE> walk;
+    Walk<false> walk_s;
 
     // k of a slot's first value within the tile.
     __device__ static __forceinline__ int k_of(int slot)
     {
         return KMAJ ? grad_chunk<LDS::CPR>(slot / LDS::CPR, slot % LDS::CPR) * 8 : slot / LDS::RCH;
     }
-    __device__ __forceinline__ void init(int wave, int lane, int64_t ld)
+    // From the tile at k0 on, `every` tiles at a time.
+    __device__ __forceinline__ void init(int wave, int lane, const GradParams& g, int row0, int k0, int every)
     {
+        const int64_t ld = g.p.lda;
 #pragma unroll
         for (int j = 0; j < LDS::IPW; ++j) {
             const int slot = (wave * LDS::IPW + j) * 64 + lane, k = slot / LDS::RCH;
             voff[j] = KMAJ ? (int)(slot / LDS::CPR * ld * ES) + k_of(slot) * ES
                            : (int)(k * ld * ES) + (slot % LDS::RCH ^ LDS::mkey(k)) * 8 * ES;
         }
+        walk.init(g.p.A, g.p.a_bytes, (KMAJ ? (int64_t)row0 * ld + k0 : (int64_t)k0 * ld + row0) * ES,
+                  (int64_t)every * BK * (KMAJ ? 1 : ld) * ES);
+        walk_s.init((const char*)g.scales, (uint64_t)g.p.K * 4, (int64_t)k0 * 4, (int64_t)every * BK * 4);
     }
-    __device__ __forceinline__ void load(int d, const GradParams& g, int row0, int k0, int wave, int lane)
+    __device__ __forceinline__ void load(int d, const GradParams& g, bool live, int wave, int lane)
     {
-        const bool live = k0 < g.p.K;
-        const int64_t origin = (KMAJ ? (int64_t)row0 * g.p.lda + k0 : (int64_t)k0 * g.p.lda + row0) * ES;
         OddRows r;
-        r.r = rest<!VEC && !WIDE>(g.p.A, g.p.a_bytes, origin, live);
+        r.r = walk.next(live);
         r.lead = (int)((uint64_t)g.p.A & 2);              // (every tile's first element lies in its word as A's)
-        const __amdgpu_buffer_rsrc_t rs = rest<false>((const char*)g.scales, (uint64_t)g.p.K * 4, (int64_t)k0 * 4, live);
+        const __amdgpu_buffer_rsrc_t rs = walk_s.next(live);
 #pragma unroll
         for (int j = 0; j < LDS::IPW; ++j) {
             if constexpr (WIDE) {
@@ -336,15 +371,15 @@ gemm_i8grad_kernel(GradParams g)
     KT::zero(acc);
     OA oa;
     OQ oq;
-    oa.init(wave, lane, p.lda);
-    oq.init(wave, lane, p.ldb);
-    auto load = [&](int t, int d) {               // past the end: empty extents
-        oa.load(d, g, m0, t * BK, wave, lane);
-        oq.load(d, g, n0, t * BK, wave, lane);
+    oa.init(wave, lane, g, m0, 0, 1);
+    oq.init(wave, lane, g, n0, 0, 1);
+    auto load = [&](int t, int d) {               // tile by tile; past the end: empty extents
+        oa.load(d, g, t < nkt, wave, lane);
+        oq.load(d, t < nkt, wave, lane);
     };
     auto store = [&](int t, int d, char* sa) {
         oa.store(d, g, sa, t * BK, wave, lane);
-        oq.store(d, g, sa + TA * KT::OA::BYTES, n0, t * BK, wave, lane);
+        oq.store(d, g, sa + TA * KT::OA::BYTES, t * BK, wave, lane);
     };
 #pragma unroll
     for (int d = 0; d < D; ++d) load(d, d);
@@ -442,11 +477,11 @@ gemm_i8grad_stream_kernel(GradParams g)
     KT::zero(acc);
     OA oa;
     OQ oq;
-    oa.init(0, lane, p.lda);
-    oq.init(0, lane, p.ldb);
-    auto load = [&](int t, int d) {               // past the end: empty extents
-        oa.load(d, g, m0, t * BK, 0, lane);
-        oq.load(d, g, n0, t * BK, 0, lane);
+    oa.init(0, lane, g, m0, wave * BK, NW);
+    oq.init(0, lane, g, n0, wave * BK, NW);
+    auto load = [&](int t, int d) {               // tile by tile; past the end: empty extents
+        oa.load(d, g, t < nkt, 0, lane);
+        oq.load(d, t < nkt, 0, lane);
     };
     char* const sa = smem + wave * STAGE;
     char* const sq = sa + TA * KT::OA::BYTES;
@@ -458,7 +493,7 @@ gemm_i8grad_stream_kernel(GradParams g)
             const int t = t0 + d * NW;
             if (t >= nkt) break;
             oa.store(d, g, sa, t * BK, 0, lane);
-            oq.store(d, g, sq, n0, t * BK, 0, lane);
+            oq.store(d, g, sq, t * BK, 0, lane);
             load(t + D * NW, d);
             __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): written
             asm volatile("" ::: "memory");

@@ -200,9 +200,17 @@ struct QOperand {
     {
 #pragma unroll
         for (int j = 0; j < LDS::IPW; ++j) {
-            const int u = j / W, chunk = unit(wave, lane, u) * W + j % W;
+            // Of a pair, lanes 4 to 7 of 8 write the second first: 8 lanes' writes then
+            // lie on different banks of the 128 bytes that a cycle writes.
+            const int u = j / W, swap = PAIR && (lane & 4) ? 1 : 0, chunk = unit(wave, lane, u) * W + (j % W ^ swap);
             int w[2];
-            q[d][j].get(voff[u], w[0], w[1]);
+            if constexpr (PAIR) {
+                const i32x2 first = q[d][j].w, other = q[d][j ^ 1].w;
+                w[0] = swap ? other[0] : first[0];
+                w[1] = swap ? other[1] : first[1];
+            } else {
+                q[d][j].get(voff[u], w[0], w[1]);
+            }
             if constexpr (!VEC) {
                 // The words at the last row's end can hold bytes of what follows it.
                 if (k0 + chunk / LDS::RCH >= g.p.K) w[0] = w[1] = 0;

@@ -39,7 +39,7 @@ struct I8Shape {
 };
 
 // The smallest tile that makes no more than one for each of the 256 CUs, else
-// the largest.  us, bf16 outputs, N = K = 4096 unless given:
+// the largest, or one as narrow as C.  us, bf16 outputs, N = K = 4096 unless given:
 //   rows               16x16  16x32  32x32  32x64  64x64  64x128 128x128 128x256 256x256
 //      1                 6.0    6.1    6.3    8.9   10.2
 //     16                 6.2    6.3    6.5    9.1
@@ -54,6 +54,9 @@ struct I8Shape {
 //   2048                                                          47.3    39.6    48.0
 //   8192  K 1024                                                          56.0    53.4
 //   8192                                                                 147.7   125.3
+//      1  N 131072      138    109    121    102    114    112     123     128     147
+//     64  N 65536 K 2048                       41     37     30      33      30      40
+//  65536  N 64 K 2048                          40     38     42      36      46      41
 // (The first three stream: the waves share a tile's k.)
 // Unaligned, us:              16x16 str. 32x32 str.  32x32   64x64  128x128
 //      1 of 4095 x 4095           8.1      10.1       14.4    26.1    35.4
@@ -74,11 +77,11 @@ inline I8Tile i8_tile(const I8Shape& s)
     if (tiles(16, 16) <= 256) return I8Tile::Stream16x16;
     if (tiles(16, 32) <= 256) return I8Tile::Stream16x32;
     if (tiles(32, 32) <= 256) return I8Tile::Stream32x32;
-    if (tiles(32, 64) <= 256) return I8Tile::Dma32x64;
+    if (s.M <= 32 || tiles(32, 64) <= 256) return I8Tile::Dma32x64;
     if (tiles(64, 64) <= 256) return I8Tile::Dma64x64;
-    if (tiles(64, 128) <= 256) return I8Tile::Dma64x128;
-    if (tiles(128, 128) <= 256) return I8Tile::Dma128x128;
-    return tiles(128, 256) <= 256 ? I8Tile::Dma128x256 : I8Tile::PingPong;
+    if (s.M <= 64 || tiles(64, 128) <= 256) return I8Tile::Dma64x128;
+    if (s.N <= 128 || tiles(128, 128) <= 256) return I8Tile::Dma128x128;
+    return s.M <= 128 || tiles(128, 256) <= 256 ? I8Tile::Dma128x256 : I8Tile::PingPong;
 }
 
 inline int64_t i8_grid(const I8Shape& s, const Tile& t) { return ceil_div(s.M, t.bm) * ceil_div(s.N, t.bn); }
@@ -159,6 +162,8 @@ struct GradShape {
 //   3008 x 2000, 3008    67/158/126   68/123/197    89/113/118
 //   4096 x 4096, 2048    - / - /225   94/181/ -     69/176/179
 //   8192 x 2048, 1024    - / - /115   50/94/ -      38/98/94
+//  65536 x   64, 2048 (64x64: 62) 70/151/-  69/103/-       84/ - / -
+//  65536 x  128, 1024    40/84/ -     35/55/ -       44/ - / -
 // Unaligned: 2049 x 1028, 4095 k takes 50/ - /145 on 64x128, 56/ - /100 on 128x128
 // 64 deep (153 tiles); 3000 x 2000, 3001 k 68/ - /127 on 64x128, 69/ - /197 on
 // 128x128, - / - /134 on 64x128 with two a CU (k-major - / - /129, 159 on 64x128).
@@ -175,6 +180,8 @@ inline GradTile grad_tile(const GradShape& s)
         return tiles(128, 256) >= 160 ? GradTile::Wide128x256 : GradTile::T64x128;
     }
     if (!s.vec) return GradTile::T128x128;
+    const int64_t narrow = s.M < s.N ? s.M : s.N;
+    if (!s.wide && narrow <= 128) return narrow <= 64 ? GradTile::T64x64 : GradTile::T128x128;
     if (s.wide) return tiles(256, 128) >= 160 ? GradTile::Tall256x128 : GradTile::T128x128;
     return tiles(256, 256) >= 160 ? GradTile::T256x256 : GradTile::T128x128;
 }

@@ -6,6 +6,8 @@ PRODUCTS = [
     ("stream 16x16", 16, 250), ("stream 16x16", 1, 4000), ("stream 16x32", 5, 8000), ("stream 32x32", 30, 8000),
     ("32x64", 40, 8000), ("64x64", 60, 16000), ("64x128", 500, 4000), ("128x128", 1000, 4000), ("128x256", 2000, 4000),
     ("ping-pong 256x256", 2050, 4100),
+    # C narrower than the large tiles
+    ("32x64", 3, 40000), ("64x128", 50, 40000), ("128x128", 40000, 100), ("128x256", 100, 70000),
 ]
 PRODUCTS_UNALIGNED = [("unaligned stream 16x16", 40, 300), ("unaligned stream 32x32", 100, 1000), ("unaligned 32x32", 300, 1000),
                       ("unaligned 64x64", 1000, 1000), ("unaligned 128x128", 1500, 2100)]
@@ -20,8 +22,10 @@ def gradients(wide, split_a, aligned):
         more = [("64x128", 2304, 1950), ("128x256", 2600, 1950)] if aligned else [("64x128, two a CU", 2304, 1950)]
     elif not aligned:
         more = [("128x128", 2304, 1950)]
+    elif wide:
+        more = [("128x128", 2304, 1950), ("256x128", 2600, 1950)]
     else:
-        more = [("128x128", 2304, 1950), ("256x128", 2600, 1950) if wide else ("256x256", 3300, 3100)]
+        more = [("128x128", 2304, 1950), ("256x256", 3300, 3100), ("64x64", 40000, 40), ("128x128", 100, 50000)]
     return _GRADIENTS + more
 
 

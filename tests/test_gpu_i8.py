@@ -553,6 +553,39 @@ def test_captured_and_replayed(dtype, out):
             assert torch.equal(s[name], e[name]), (i, name)
 
 
+def test_offsets_past_32_bits():
+    """Rows far apart: 700 of them span 4.9 GB."""
+    ld, M, K, N = 7_000_000, 700, 130, 48
+    far = torch.empty(ld * M, dtype=torch.int8, device="cuda").as_strided((M, K), (ld, 1))
+    wide = torch.empty(ld * M // 2, dtype=BF16, device="cuda").as_strided((M, K), (ld // 2, 1))
+    x = randn((M, K), 1).to(BF16).cuda()
+    wide.copy_(x)
+    s = torch.empty(M, device="cuda")
+    g.quantize_rows(wide, far, s)
+    q, scales = quantized(x)
+    assert torch.equal(far, q) and torch.equal(s, scales)
+    wide.zero_()
+    g.dequantize_rows(far, s, wide)
+    assert torch.equal(wide, (q.float() * scales[:, None]).to(BF16))
+    w, ws = quantized(randn((N, K), 2).cuda())
+    c = torch.empty((M, N), device="cuda")
+    g.gemm_i8(far, w, s, ws, c)
+    assert torch.equal(c, (q.double() @ w.double().t()).float() * s[:, None] * ws)
+    dy = ints((M, N), 3, -3, 3).to(BF16).cuda()
+    near, away = torch.empty((N, K), device="cuda"), torch.empty((N, K), device="cuda")
+    g.gemm_i8_grad(dy.t(), q.t(), s, near)
+    g.gemm_i8_grad(dy.t(), far.t(), s, away)
+    assert torch.equal(near, away)
+    big = torch.empty(ld * M // 2, dtype=BF16, device="cuda").as_strided((M, N), (ld // 2, 1))
+    big.copy_(dy)
+    g.gemm_i8_grad(big.t(), q.t(), s, away)
+    assert torch.equal(near, away)
+    g.gemm_i8_grad(dy, w.t(), ws, wide)               # C far apart
+    dx = torch.empty((M, K), dtype=BF16, device="cuda")
+    g.gemm_i8_grad(dy, w.t(), ws, dx)
+    assert torch.equal(wide, dx)
+
+
 def test_on_another_stream():
     s, e = layer("bf16", "f32"), layer("bf16", "f32")
     e["step"]()

@@ -131,7 +131,7 @@ constexpr Tile kGradTiles[] = {
     {"64x64", 64, 64, 128, 2, 4, 16, 2, 2, 512},
     {"64x128", 64, 128, 64, 2, 4, 16, 2, 2, 512},
     {"64x128, two a CU", 64, 128, 64, 2, 4, 16, 1, 4, 512},
-    {"128x128, 64 deep", 128, 128, 64, 4, 4, 16, 1, 4, 1024},
+    {"128x128, deep", 128, 128, 64, 4, 4, 16, 1, 4, 1024},
     {"128x128", 128, 128, 32, 2, 4, 16, 2, 2, 512},
     {"256x256", 256, 256, 32, 4, 2, 16, 2, 2, 512},
     {"256x128", 256, 128, 64, 4, 4, 16, 1, 4, 1024},
@@ -139,11 +139,19 @@ constexpr Tile kGradTiles[] = {
 };
 static_assert(sizeof(kGradTiles) / sizeof(Tile) == (int)GradTile::Count, "one entry a tile");
 constexpr Tile tile_of(GradTile t) { return kGradTiles[(int)t]; }
-// The 64 deep tile where A is m-major and stands in three terms: a wave of 32x64
-// reads 10 fragments of LDS where two of 32x32 read 16, and eight convert as fast
-// as sixteen.  us, this | sixteen waves: 2048 x 1024, 4096 k of fp32 92 | 103, of
-// fp16 94 | 103; 2049 x 1028, 4095 k 96 | 102, 99 | 107; k-major A 97 | 91, 98 | 96.
-constexpr Tile kDeepTerms = {"128x128, 64 deep", 128, 128, 64, 4, 2, 16, 1, 2, 512};
+// The deep 128x128 tile of each kind of call.  Sixteen waves of 32x32 convert fast,
+// but read 16 fragments of LDS for the products of three terms where eight of 32x64
+// read 10, and with one term 64 k are little between two barriers.  us, this | as
+// in the table, m-major A (k-major):
+//   16-bit C   2048 x 2048, 4096 k 48 | 52 (47 | 49), 2049 x 1028, 4095 k 49 | 48 (46 | 46)
+//   Q's terms                      93 | 103 (94 | 100),                  94 | 96 (93 | 93)
+//   A's terms                     104 | 113,                             96 | 102
+constexpr Tile deep_tile(bool wide, bool split_a, bool a_kmajor)
+{
+    if (!wide) return {"", 128, 128, 128, 4, 4, 16, 1, 4, 1024};
+    if (!split_a) return {"", 128, 128, 64, 2, 4, 16, 1, 2, 512};
+    return a_kmajor ? kGradTiles[(int)GradTile::T128x128Deep] : Tile{"", 128, 128, 64, 4, 2, 16, 1, 2, 512};
+}
 
 struct GradShape {
     bool vec;             // A and Q allow 16-byte loads
@@ -155,12 +163,12 @@ struct GradShape {
 // The smallest tile that makes no more than one for each of the 256 CUs; past
 // that the largest that fills most of them.  us, bf16 into bf16 / bf16 into fp32
 // / fp32, A m-major (k-major is within a few percent):
-//   M x N, K              32x32 str.   32x64 str.    64x64        64x128       128x128, 64 deep
+//   M x N, K              32x32 str.   32x64 str.    64x64        64x128       128x128, deep
 //    512 x  256, 1000    6.1/7.2/7.7  7.7/10/9.6   9.1/13/16    12/21/19
 //     32 x 4096, 4096    12/16/18     15/26/22      25/42/50
 //   1024 x  512, 1024    9.6/14/16    7.9/11/10     9.2/14/16
-//   1024 x 1024, 4096    39/64/77     28/52/44      24/44/50     38/71/65       51/98/ -
-//   2048 x 1024, 4096                               41/83/97     38/71/66       51/100/92
+//   1024 x 1024, 4096    39/64/77     28/52/44      24/44/50     38/71/65       45/88/ -
+//   2048 x 1024, 4096                               41/83/97     38/71/66        - / - /92
 //   2048 x 2048, 4096                               80/165/192   63/142/113     54/105/113
 //                        64x128       128x128       256x256 | 256x128 | 128x256 (16-bit C, Q's terms, A's terms)
 //   4096 x 2048, 1024    33/80/61     27/50/74      35/49/54
@@ -169,8 +177,8 @@ struct GradShape {
 //   8192 x 2048, 1024    - / - /115   50/94/ -      38/98/94
 //  65536 x   64, 2048 (64x64: 62) 70/151/-  69/103/-       84/ - / -
 //  65536 x  128, 1024    40/84/ -     35/55/ -       44/ - / -
-// Unaligned: 2049 x 1028, 4095 k takes 50/ - /145 on 64x128, 56/ - /96 on 128x128
-// 64 deep (153 tiles); 3000 x 2000, 3001 k 68/ - /127 on 64x128, 69/ - /197 on
+// Unaligned: 2049 x 1028, 4095 k takes 61/141/136 on 64x128, 49/95/96 on 128x128,
+// deep (153 tiles); 3000 x 2000, 3001 k 68/ - /127 on 64x128, 69/ - /197 on
 // 128x128, - / - /134 on 64x128 with two a CU (k-major - / - /129, 159 on 64x128).
 inline GradTile grad_tile(const GradShape& s)
 {

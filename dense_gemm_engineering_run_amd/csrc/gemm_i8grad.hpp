@@ -583,7 +583,7 @@ struct GradInst {
     template <GradTile T, bool AK, bool VEC>
     static hipError_t tile(const GradCall& c, hipStream_t s)
     {
-        constexpr Tile t = T == GradTile::T128x128Deep && GT::SPLIT_A && !AK ? kDeepTerms : tile_of(T);
+        constexpr Tile t = T == GradTile::T128x128Deep ? deep_tile(WIDE, GT::SPLIT_A, AK) : tile_of(T);
         return run(c.g.p.epi ? (const void*)&gemm_i8grad_kernel<TI, TO, t.bm, t.bn, t.bk, t.wm, t.wn, t.stages, t.extra, AK, VEC, true>
                              : (const void*)&gemm_i8grad_kernel<TI, TO, t.bm, t.bn, t.bk, t.wm, t.wn, t.stages, t.extra, AK, VEC, false>,
                    c, t, s);

@@ -13,7 +13,7 @@ PRODUCTS_UNALIGNED = [("unaligned stream 16x16", 40, 300), ("unaligned stream 32
                       ("unaligned 64x64", 1000, 1000), ("unaligned 128x128", 1500, 2100)]
 
 _GRADIENTS = [("stream 32x32", 100, 200), ("stream 32x64", 500, 600), ("64x64", 1000, 1000), ("64x128", 1000, 2000),
-              ("128x128, 64 deep", 2000, 2000)]
+              ("128x128, deep", 2000, 2000)]
 
 
 def gradients(wide, split_a, aligned):

@@ -169,7 +169,7 @@ struct GradShape {
 //   1024 x  512, 1024    9.6/14/16    7.9/11/10     9.2/14/16
 //   1024 x 1024, 4096    39/64/77     28/52/44      24/44/50     38/71/65       45/88/ -
 //   2048 x 1024, 4096                               41/83/97     38/71/66        - / - /92
-//   2048 x 2048, 4096                               80/165/192   63/142/113     54/105/113
+//   2048 x 2048, 4096                               80/165/192   63/142/113     48/95/104
 //                        64x128       128x128       256x256 | 256x128 | 128x256 (16-bit C, Q's terms, A's terms)
 //   4096 x 2048, 1024    33/80/61     27/50/74      35/49/54
 //   3008 x 2000, 3008    67/158/126   68/123/197    89/113/118

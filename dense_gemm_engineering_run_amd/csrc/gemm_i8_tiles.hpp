@@ -11,7 +11,7 @@ namespace mg {
 // bk counts pairs of 8-bit values.
 enum class I8Tile : int {
     Stream16x16, Stream16x32, Stream32x32, Dma32x64, Dma64x64, Dma64x128, Dma128x128, Dma128x256, PingPong,
-    OddStream16x16, OddStream32x32, Odd32x32, Odd64x64, Odd128x128,
+    OddStream16x16, OddStream32x32, Odd32x32, Odd64x64, Odd128x128, Odd128x256,
     Count
 };
 constexpr Tile kI8Tiles[] = {
@@ -29,6 +29,7 @@ constexpr Tile kI8Tiles[] = {
     {"unaligned 32x32", 32, 32, 128, 2, 2, 16, 2, 0, 256},
     {"unaligned 64x64", 64, 64, 64, 2, 4, 16, 2, 0, 512},
     {"unaligned 128x128", 128, 128, 64, 2, 4, 16, 2, 0, 512},
+    {"unaligned 128x256", 128, 256, 64, 4, 4, 16, 2, 0, 1024},
 };
 static_assert(sizeof(kI8Tiles) / sizeof(Tile) == (int)I8Tile::Count, "one entry a tile");
 constexpr Tile tile_of(I8Tile t) { return kI8Tiles[(int)t]; }
@@ -58,13 +59,18 @@ struct I8Shape {
 //     64  N 65536 K 2048                       41     37     30      33      30      40
 //  65536  N 64 K 2048                          40     38     42      36      46      41
 // (The first three stream: the waves share a tile's k.)
-// Unaligned, us:              16x16 str. 32x32 str.  32x32   64x64  128x128
-//      1 of 4095 x 4095           8.1      10.1       14.4    26.1    35.4
-//     40 of 4095 x 4095          16.6      11.2       14.8    26.3
-//    300 of 1023 x 2047          19.5      14.5       10.6    15.2    23.8
-//   1500 of 1025 x 4095                               50.7    39.3    42.0
-//   4095 of 2049 x 1028                                       44.8    38.2
-//   3000 of 4095 x 2047                              156      87.0    54.5
+// Unaligned, us:              16x16 str. 32x32 str.  32x32   64x64  128x128  128x256
+//      1 of 4095 x 4095           7.8      10.1       14.4    26.1    35.4
+//     40 of 4095 x 4095          16.6       9.8       14.8    26.3
+//    300 of 1023 x 2047          19.5      14.5       10.1    15.2    23.8
+//   1500 of 1025 x 4095                               50.7    39.3    37.1     52.4
+//   4095 of 2048 x 1028                                       44.8    25.0     23.2
+//   2048 of 4096 x 4096                                               65.7     57.6
+//   3000 of 4095 x 2047                              156      87.0    53.8     60.2
+//   8192 of 4096 x 1024                                               71.4     73.1
+//   8192 of 4096 x 4096                                              241.4    215.1
+// (Two 128x128 tiles share a CU, and a last round of few of them is short; a
+// 128x256 tile has one for itself.)
 inline I8Tile i8_tile(const I8Shape& s)
 {
     auto tiles = [&](int bm, int bn) { return ceil_div(s.M, bm) * ceil_div(s.N, bn); };
@@ -72,7 +78,10 @@ inline I8Tile i8_tile(const I8Shape& s)
         if (tiles(16, 16) <= 256) return I8Tile::OddStream16x16;
         if (tiles(32, 32) <= 256) return I8Tile::OddStream32x32;
         if (tiles(32, 32) <= 512) return I8Tile::Odd32x32;
-        return tiles(64, 64) <= 512 ? I8Tile::Odd64x64 : I8Tile::Odd128x128;
+        if (tiles(64, 64) <= 512) return I8Tile::Odd64x64;
+        if (tiles(128, 128) <= 256) return I8Tile::Odd128x128;
+        const int64_t wide = tiles(128, 256);
+        return wide <= 256 || (s.K >= 2048 && (wide - 1) % 256 >= 160) ? I8Tile::Odd128x256 : I8Tile::Odd128x128;
     }
     if (tiles(16, 16) <= 256) return I8Tile::Stream16x16;
     if (tiles(16, 32) <= 256) return I8Tile::Stream16x32;
@@ -92,11 +101,11 @@ inline int64_t i8_grid(const I8Shape& s, const Tile& t) { return ceil_div(s.M, t
 // 2^20 of a tile's products; the unaligned 128x128 tile runs twice a CU).
 // us, in brackets without: 8193 x 4096 x 4096 133 (159); 2049 rows of it 45.5
 // (51.2); 4100 x 4104 x 2048 54 (66); 4095 x 2049 x 1028 into fp32 28.1 (34.9);
-// unaligned 35.0 (41.1), 2048 x 4100 x 4096 83 (97).
+// unaligned, on 128x128 tiles, 35.0 (41.1), 2048 x 4100 x 4096 83 (97).
 inline int64_t i8_cost(const I8Shape& s)
 {
     const Tile& t = kI8Tiles[(int)i8_tile(s)];
-    const int64_t a_cu = !s.vec && t.bm == 128 ? 2 : 1;
+    const int64_t a_cu = !s.vec && t.bm == 128 && t.bn == 128 ? 2 : 1;
     return ceil_div(i8_grid(s, t), 256 * a_cu) * a_cu * t.bm * t.bn * s.K;
 }
 struct I8Edges {

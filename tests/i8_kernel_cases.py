@@ -10,7 +10,8 @@ PRODUCTS = [
     ("32x64", 3, 40000), ("64x128", 50, 40000), ("128x128", 40000, 100), ("128x256", 100, 70000),
 ]
 PRODUCTS_UNALIGNED = [("unaligned stream 16x16", 40, 300), ("unaligned stream 32x32", 100, 1000), ("unaligned 32x32", 300, 1000),
-                      ("unaligned 64x64", 1000, 1000), ("unaligned 128x128", 1500, 2100)]
+                      ("unaligned 64x64", 1000, 1000), ("unaligned 128x128", 1500, 2100),
+                      ("unaligned 128x256", 2000, 4000)]
 
 _GRADIENTS = [("stream 32x32", 100, 200), ("stream 32x64", 500, 600), ("64x64", 1000, 1000), ("64x128", 1000, 2000),
               ("128x128, deep", 2000, 2000)]

@@ -142,7 +142,7 @@ constexpr Tile kGradTiles[] = {
     {"64x128, two a CU", 64, 128, 64, 2, 4, 16, 1, 4, 512},
     {"128x128, deep", 128, 128, 64, 4, 4, 16, 1, 4, 1024},
     {"128x128", 128, 128, 32, 2, 4, 16, 2, 2, 512},
-    {"256x256", 256, 256, 32, 4, 2, 16, 2, 2, 512},
+    {"256x256", 256, 256, 32, 4, 2, 16, 1, 2, 512},
     {"256x128", 256, 128, 64, 4, 4, 16, 1, 4, 1024},
     {"128x256", 128, 256, 64, 4, 4, 16, 1, 4, 1024},
 };
@@ -150,45 +150,73 @@ static_assert(sizeof(kGradTiles) / sizeof(Tile) == (int)GradTile::Count, "one en
 constexpr Tile tile_of(GradTile t) { return kGradTiles[(int)t]; }
 // The deep 128x128 tile of each kind of call.  Sixteen waves of 32x32 convert fast,
 // but read 16 fragments of LDS for the products of three terms where eight of 32x64
-// read 10, and with one term 64 k are little between two barriers.  us, this | as
-// in the table, m-major A (k-major):
-//   16-bit C   2048 x 2048, 4096 k 48 | 52 (47 | 49), 2049 x 1028, 4095 k 49 | 48 (46 | 46)
+// read 10.  us, this | as in the table, m-major A (k-major):
+//   16-bit C   2048 x 2048, 4096 k - | 77 (- | 78), 2049 x 1028, 4095 k - | 76 (- | 75)
+//     (on 4 x 2 waves 78 (87) and 84 (91), on 2 x 4 86 (90) and 90 (93))
 //   Q's terms                      93 | 103 (94 | 100),                  94 | 96 (93 | 93)
-//   A's terms                     104 | 113,                             96 | 102
+//   A's terms into fp32           104 | 113,                             96 | 102
 constexpr Tile deep_tile(bool wide, bool split_a, bool a_kmajor)
 {
-    if (!wide) return {"", 128, 128, 128, 4, 4, 16, 1, 4, 1024};
     if (!split_a) return {"", 128, 128, 64, 2, 4, 16, 1, 2, 512};
-    return a_kmajor ? kGradTiles[(int)GradTile::T128x128Deep] : Tile{"", 128, 128, 64, 4, 2, 16, 1, 2, 512};
+    return !wide || a_kmajor ? kGradTiles[(int)GradTile::T128x128Deep] : Tile{"", 128, 128, 64, 4, 2, 16, 1, 2, 512};
 }
 
 struct GradShape {
     bool vec;             // A and Q allow 16-byte loads
-    bool wide;            // fp32 C: three MFMAs a product
-    bool split_a;         // ... of A's terms (else of Q's)
+    bool wide;            // fp32 C: three MFMAs a product (else two)
+    bool split_a;         // the terms are A's (else Q's: bf16 into fp32)
     int64_t M, N, K;
+    bool a_kmajor;
 };
 
-// The smallest tile that makes no more than one for each of the 256 CUs; past
-// that the largest that fills most of them.  us, bf16 into bf16 / bf16 into fp32
-// / fp32, A m-major (k-major is within a few percent):
+// The smallest tile that makes no more than one for each of the 256 CUs; past that:
+//
+// 16-bit C: 128x256, where one for each CU does, else 256x256; as narrow as C.  us,
+// bf16 into bf16, A m-major (k-major; fp16 is within a few percent):
+//   M x N, K              32x32 str.   32x64 str.    64x64        64x128      128x128, deep
+//    512 x  256, 1000       7.6          8.6         12.7         14.9
+//     32 x 4096, 4096      16.9         19.7         38.2         48.8
+//   1024 x  512, 1024      12.9          8.9         13.0         15.3
+//   1024 x 1024, 4096      62           34           39           49           82 (2 x 4 waves)
+//   2048 x 1024, 4096                                77 (79)      50 (51)      69 (70)
+//   2048 x 2048, 4096                               157 (165)     87 (86)      77 (78)
+//                          64x128      128x128      128x256      256x256
+//   2304 x 1952,   64     10.7          9.3          9.5
+//   2304 x 1952,  256     16.4         15.8         15.0
+//   2304 x 1952, 2048     72           77           65          105
+//   3008 x 2000, 3008     95 (96)     101 (103)      87 (86)    141 (146)
+//   4096 x 2048, 1024     47 (46)      39 (42)       36 (36)     52 (54)
+//   3300 x 3104, 2048    137          126          132          108
+//   4096 x 4096, 2048    166 (165)    145 (151)     128 (127)   110 (115)
+//   8192 x 4096, 4096    636 (635)    561 (597)     492 (498)   420 (436)
+//  65536 x   64, 2048    101 (99)      87 (93)      144 (145)    -         64x64: 89 (94)
+//  65536 x  128, 1024     55 (53)      47 (50)       80 (76)     65 (68)
+//     64 x 65536, 2048    52 (49)      83 (78)       73 (65)     -
+//    128 x 65536, 1024    48 (47)      40 (42)       36 (36)     57 (54)
+// Unaligned        64x128     two a CU     128x128, deep   128x128
+//   2049 x 1028, 4095      86 (107)    91  (82)       76  (75)       109 (107)
+//   2304 x 1950, 2048      71  (85)    74  (71)       81  (81)        77 (106)
+//   3000 x 2000, 3001     106 (123)   110 (106)      116 (116)       111 (155)
+//   8192 x 4096, 4096     713 (846)   752 (719)      656 (665)       627 (840)
+//     64 x 65536, 2048     58  (62)    60  (55)       90  (83)        88 (110)
+//
+// fp32 C: the largest that fills most of the CUs.  us, bf16 into fp32 / fp32, A
+// m-major (k-major is within a few percent):
 //   M x N, K              32x32 str.   32x64 str.    64x64        64x128       128x128, deep
-//    512 x  256, 1000    6.1/7.2/7.7  7.7/10/9.6   9.1/13/16    12/21/19
-//     32 x 4096, 4096    12/16/18     15/26/22      25/42/50
-//   1024 x  512, 1024    9.6/14/16    7.9/11/10     9.2/14/16
-//   1024 x 1024, 4096    39/64/77     28/52/44      24/44/50     38/71/65       45/88/ -
-//   2048 x 1024, 4096                               41/83/97     38/71/66        - / - /92
-//   2048 x 2048, 4096                               80/165/192   63/142/113     48/95/104
-//                        64x128       128x128       256x256 | 256x128 | 128x256 (16-bit C, Q's terms, A's terms)
-//   4096 x 2048, 1024    33/80/61     27/50/74      35/49/54
-//   3008 x 2000, 3008    67/158/126   68/123/197    89/113/118
-//   4096 x 4096, 2048    - / - /225   94/181/ -     69/176/179
-//   8192 x 2048, 1024    - / - /115   50/94/ -      38/98/94
-//  65536 x   64, 2048 (64x64: 62) 70/151/-  69/103/-       84/ - / -
-//  65536 x  128, 1024    40/84/ -     35/55/ -       44/ - / -
-// Unaligned: 2049 x 1028, 4095 k takes 61/141/136 on 64x128, 49/95/96 on 128x128,
-// deep (153 tiles); 3000 x 2000, 3001 k 68/ - /127 on 64x128, 69/ - /197 on
-// 128x128, - / - /134 on 64x128 with two a CU (k-major - / - /129, 159 on 64x128).
+//    512 x  256, 1000      7.2/7.7       10/9.6      13/16         21/19
+//     32 x 4096, 4096       16/18        26/22       42/50
+//   1024 x  512, 1024       14/16        11/10       14/16
+//   1024 x 1024, 4096       64/77        52/44       44/50         71/65         88/ -
+//   2048 x 1024, 4096                                83/97         71/66         - /92
+//   2048 x 2048, 4096                               165/192       142/113        95/104
+//                          64x128      128x128      256x128 | 128x256 (Q's terms, A's terms)
+//   4096 x 2048, 1024       80/61        50/74       49/54
+//   3008 x 2000, 3008      158/126      123/197     113/118
+//   4096 x 4096, 2048       - /225      181/ -      176/179
+//   8192 x 2048, 1024       - /115       94/ -       98/94
+// Unaligned: 2049 x 1028, 4095 k takes 141/136 on 64x128, 95/96 on 128x128, deep (153
+// tiles); 3000 x 2000, 3001 k - /127 on 64x128, - /197 on 128x128, - /134 on 64x128
+// with two a CU (k-major - /129, 159 on 64x128).
 inline GradTile grad_tile(const GradShape& s)
 {
     auto tiles = [&](int bm, int bn) { return ceil_div(s.M, bm) * ceil_div(s.N, bn); };
@@ -197,15 +225,20 @@ inline GradTile grad_tile(const GradShape& s)
     if (tiles(64, 64) <= 256) return GradTile::T64x64;
     if (tiles(64, 128) <= 256) return GradTile::T64x128;
     if (tiles(128, 128) <= 256) return GradTile::T128x128Deep;
+    if (!s.wide) {
+        if (s.M <= 64) return GradTile::T64x128;
+        if (!s.vec) return s.a_kmajor ? GradTile::T64x128Two : GradTile::T128x128;
+        if (s.N <= 64) return GradTile::T64x64;
+        if (s.N <= 128) return GradTile::T128x128;
+        if (s.M > 128 && tiles(128, 256) > 256) return GradTile::T256x256;
+        return s.K <= 128 && !s.a_kmajor ? GradTile::T128x128 : GradTile::Wide128x256;
+    }
     if (s.split_a) {
         if (!s.vec) return GradTile::T64x128Two;
         return tiles(128, 256) >= 160 ? GradTile::Wide128x256 : GradTile::T64x128;
     }
     if (!s.vec) return GradTile::T128x128;
-    const int64_t narrow = s.M < s.N ? s.M : s.N;
-    if (!s.wide && narrow <= 128) return narrow <= 64 ? GradTile::T64x64 : GradTile::T128x128;
-    if (s.wide) return tiles(256, 128) >= 160 ? GradTile::Tall256x128 : GradTile::T128x128;
-    return tiles(256, 256) >= 160 ? GradTile::T256x256 : GradTile::T128x128;
+    return tiles(256, 128) >= 160 ? GradTile::Tall256x128 : GradTile::T128x128;
 }
 
 inline int64_t grad_grid(const GradShape& s, const Tile& t) { return ceil_div(s.M, t.bm) * ceil_div(s.N, t.bn); }

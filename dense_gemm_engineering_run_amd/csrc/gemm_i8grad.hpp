@@ -5,16 +5,17 @@
 //
 // Q is stored k by k (element (n, k) at n + k * ldq), A m- or k-contiguous.
 // The scale cannot leave the sum, so it joins a factor before the matrix units
-// take it:
-//   16-bit C: the restored value scales[k] * Q[n][k], rounded to A's type, as
-//     gemm_dequantize_rows gives it (off by half a step: 2^-8 of itself in bf16,
-//     2^-11 in fp16, 2^-25 where that is more).
-//   fp32 C: a product with the scale rounded to fp32, held whole by three bf16
-//     terms of 8 bits each: scales[k] * Q[n][k] for bf16 A, scales[k] * A[m][k] for
-//     fp16 and fp32 A (Q is exact in bf16).  Two terms (17 bits) made the result
-//     2.5e-6 off (relative, 8192 k of normal values), where fp32 sums alone are off
-//     by 5e-7.  For fp32 A three bf16 MFMAs take less than half the time of the
-//     fp32 ones.
+// take it: A, as Q is exact in bf16 (bf16 A into fp32 C: Q, which is converted
+// anyway).  The product scales[k] * A[m][k] (scales[k] * Q[n][k]), rounded to fp32,
+// enters in bf16 terms:
+//   fp32 C: three of 8 bits each, which hold it whole.  Two made the result 2.5e-6
+//     off (relative, 8192 k of normal values), where fp32 sums alone are off by
+//     5e-7.  For fp32 A three bf16 MFMAs take less than half the time of the fp32
+//     ones.
+//   16-bit C: two, off by 2^-16 of it at most, where C's own rounding is off by up
+//     to 2^-9 (bf16) or 2^-12 (fp16).  With one (the restored value rounded to A's
+//     type) results were 2.35e-3 off in bf16 and 2.9e-4 in fp16, where that rounding
+//     alone is off by 1.66e-3 and 2.1e-4.
 #pragma once
 
 #include "gemm_i8_tiles.hpp"
@@ -31,36 +32,53 @@ struct GradParams {
 // Terms that the kernels split each factor into, and the type they multiply in.
 template <In TI, Out TO>
 struct GradTypes {
-    static constexpr bool SPLIT_A = TO == Out::F32 && TI != In::BF16;   // the scale joins A (else Q)
-    static constexpr int TA = SPLIT_A ? 3 : 1;
-    static constexpr int TQ = TO == Out::F32 && !SPLIT_A ? 3 : 1;
-    static constexpr In MT = SPLIT_A ? In::BF16 : TI;
+    static constexpr bool SPLIT_A = TO != Out::F32 || TI != In::BF16;   // the scale joins A (else Q)
+    static constexpr int TERMS = TO == Out::F32 ? 3 : 2;
+    static constexpr int TA = SPLIT_A ? TERMS : 1, TQ = SPLIT_A ? 1 : TERMS;
 };
 
-// Eight fp32 values as 16-bit ones.
-template <In T>
-__device__ __forceinline__ void split8(float (&v)[8], i32x4 (&t)[1])
+// Two fp32 values rounded to bf16, side by side.
+__device__ __forceinline__ int pack_bf16(float lo, float hi)
 {
     typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(int, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+// ... cut off to bf16.
+__device__ __forceinline__ int cut_bf16(float lo, float hi)
+{
+    return (int)__builtin_amdgcn_perm((uint32_t)__float_as_int(hi), (uint32_t)__float_as_int(lo), 0x07060302u);
+}
+// What that leaves, exactly (of an infinity, NaN).
+__device__ __forceinline__ float rest_bf16(float v) { return v - __int_as_float(__float_as_int(v) & (int)0xffff0000); }
+
+// Eight integers of a byte each: bf16 holds them.
+__device__ __forceinline__ void split8(float (&v)[8], i32x4 (&t)[1])
+{
+#pragma unroll
+    for (int d = 0; d < 4; ++d) t[0][d] = pack_bf16(v[2 * d], v[2 * d + 1]);
+}
+
+// Eight fp32 values in two bf16 terms: the first 8 bits, and the rest rounded.  An
+// infinity is all in the first, so that it stays one times Q.
+__device__ __forceinline__ void split8(float (&v)[8], i32x4 (&t)[2])
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = settled(v[e]);
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-        const f32x2 x = {v[2 * d], v[2 * d + 1]};
-        if constexpr (T == In::F16) {
-            typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-            t[0][d] = __builtin_bit_cast(int, __builtin_convertvector(x, f16x2));
-        } else {
-            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-            t[0][d] = __builtin_bit_cast(int, __builtin_convertvector(x, bf16x2));
-        }
+        t[0][d] = cut_bf16(v[2 * d], v[2 * d + 1]);
+        float r[2] = {rest_bf16(v[2 * d]), rest_bf16(v[2 * d + 1])};
+        r[0] = r[0] == r[0] ? r[0] : 0.f;
+        r[1] = r[1] == r[1] ? r[1] : 0.f;
+        t[1][d] = pack_bf16(r[0], r[1]);
     }
 }
 
-// The same in three bf16 terms by cutting off: 8 of the 24 bits each, nothing
-// is left (of an infinity, NaN).
-template <In T>
+// ... in three by cutting off: 8 of the 24 bits each, nothing is left (of an
+// infinity, NaN).
 __device__ __forceinline__ void split8(float (&v)[8], i32x4 (&t)[3])
 {
-    static_assert(T == In::BF16, "terms of 8 bits");
 #pragma unroll
     for (int s = 0; s < 3; ++s)
 #pragma unroll
@@ -69,11 +87,10 @@ __device__ __forceinline__ void split8(float (&v)[8], i32x4 (&t)[3])
                 v[2 * d] = settled(v[2 * d]);
                 v[2 * d + 1] = settled(v[2 * d + 1]);
             }
-            t[s][d] = (int)__builtin_amdgcn_perm((uint32_t)__float_as_int(v[2 * d + 1]), (uint32_t)__float_as_int(v[2 * d]),
-                                                 0x07060302u);
+            t[s][d] = cut_bf16(v[2 * d], v[2 * d + 1]);
             if (s < 2) {
-                v[2 * d] -= __int_as_float(__float_as_int(v[2 * d]) & (int)0xffff0000);
-                v[2 * d + 1] -= __int_as_float(__float_as_int(v[2 * d + 1]) & (int)0xffff0000);
+                v[2 * d] = rest_bf16(v[2 * d]);
+                v[2 * d + 1] = rest_bf16(v[2 * d + 1]);
             }
         }
 }
@@ -151,13 +168,13 @@ struct HalfChunk<true> {
 // The operands: k-tiles from memory to registers, D tiles ahead, and from there
 // to LDS as DmaOperand lays them out, a tile a term.
 
-// Q: k rows of ROWS bytes to [BK][ROWS] values, exact or times scales[k].  A lane
+// Q: k rows of ROWS bytes to [BK][ROWS] bf16 values, exact or times scales[k].  A lane
 // loads what makes one 16-byte chunk of values, or two, side by side (their XOR
 // keys are even).
-template <In MT, int ROWS, int BK, int NW, int TERMS, bool SCALED, bool VEC, int D>
+template <int ROWS, int BK, int NW, int TERMS, bool VEC, int D>
 struct QOperand {
     using LDS = DmaOperand<ROWS, BK, NW, false, 16>;
-    static constexpr bool PAIR = VEC && LDS::IPW % 2 == 0;
+    static constexpr bool SCALED = TERMS > 1, PAIR = VEC && LDS::IPW % 2 == 0;
     static constexpr int W = PAIR ? 2 : 1, UNITS = LDS::IPW / W, PER_ROW = LDS::RCH / W;
     int voff[UNITS];
     ByteChunk8<VEC> q[D][LDS::IPW];
@@ -222,7 +239,7 @@ struct QOperand {
                 if constexpr (SCALED) v[e] *= s[d][u];
             }
             i32x4 t[TERMS];
-            split8<MT>(v, t);
+            split8(v, t);
 #pragma unroll
             for (int x = 0; x < TERMS; ++x) *(i32x4*)(tile + x * LDS::BYTES + chunk * 16) = t[x];
         }
@@ -251,12 +268,11 @@ __device__ __forceinline__ i32x4 a_frag(const char* t, int rbase, int kb, int la
     }
 }
 
-// A: 16-bit values as they are, or (SPLIT) fp16 and fp32 ones times scales[k] in
-// three bf16 terms.
-template <In TI, int ROWS, int BK, int NW, bool KMAJ, bool SPLIT, bool VEC, int D>
+// A: bf16 values as they are, or (SPLIT) times scales[k] in TERMS bf16 terms.
+template <In TI, int ROWS, int BK, int NW, bool KMAJ, int TERMS, bool VEC, int D>
 struct AOperand {
     using LDS = DmaOperand<ROWS, BK, NW, KMAJ, 16>;
-    static constexpr bool WIDE = TI == In::F32;
+    static constexpr bool WIDE = TI == In::F32, SPLIT = TERMS > 1;
     static constexpr int ES = WIDE ? 4 : 2, NS = !SPLIT ? 0 : KMAJ ? 8 : 1;
     int voff[LDS::IPW];
     i32x4 wide[WIDE ? D : 1][WIDE ? LDS::IPW : 1][2];
@@ -333,7 +349,7 @@ struct AOperand {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] = __int_as_float(wide[d][j][e / 4][e % 4]);
                 } else {
-                    QuantType<In::F16>::unpack(half[d][j].get(lead, voff[j]), v);
+                    QuantType<TI>::unpack(half[d][j].get(lead, voff[j]), v);
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] *= s[d][j][KMAJ ? e : 0];
@@ -343,10 +359,10 @@ struct AOperand {
                     for (int e = 0; e < 8; ++e)
                         if ((KMAJ ? e : 0) >= left) v[e] = 0.f;
                 }
-                i32x4 t[3];
-                split8<In::BF16>(v, t);
+                i32x4 t[TERMS];
+                split8(v, t);
 #pragma unroll
-                for (int x = 0; x < 3; ++x) *(i32x4*)(tile + x * LDS::BYTES + slot * 16) = t[x];
+                for (int x = 0; x < TERMS; ++x) *(i32x4*)(tile + x * LDS::BYTES + slot * 16) = t[x];
             }
         }
     }
@@ -360,11 +376,10 @@ __global__ void __launch_bounds__(WM * WN * 64, OCC)
 gemm_i8grad_kernel(GradParams g)
 {
     using GT = GradTypes<TI, TO>;
-    constexpr In MT = GT::MT;
     constexpr int TA = GT::TA, TQ = GT::TQ, NW = WM * WN;
-    using KT = Dma16<MT, TO, BM, BN, BK, WM, WN, 16, 2, AK, false>;
-    using OA = AOperand<TI, BM, BK, NW, AK, GT::SPLIT_A, VEC, D>;
-    using OQ = QOperand<MT, BN, BK, NW, TQ, !GT::SPLIT_A, VEC, D>;
+    using KT = Dma16<In::BF16, TO, BM, BN, BK, WM, WN, 16, 2, AK, false>;
+    using OA = AOperand<TI, BM, BK, NW, AK, TA, VEC, D>;
+    using OQ = QOperand<BN, BK, NW, TQ, VEC, D>;
     constexpr int STAGE = TA * KT::OA::BYTES + TQ * KT::OB::BYTES, SMEM = 2 * STAGE;
     static_assert(SMEM <= 160 * 1024 && SMEM >= KT::SMEM, "LDS budget");
     __shared__ __attribute__((aligned(1024))) char smem[SMEM];
@@ -406,21 +421,32 @@ gemm_i8grad_kernel(GradParams g)
                 const int stage = D == 1 ? t & 1 : d % 2;
                 const char* const sa = smem + stage * STAGE;
                 const char* const sq = sa + TA * KT::OA::BYTES;
-                // The next k-group's fragments ahead, where registers hold both.
+                // The next k-group's fragments ahead, where registers hold both; where not
+                // (the 256x256 tile), a term's are read behind the products of the other.
                 constexpr bool AHEAD = KT::TM * KT::TN * 4 + 8 * (TA * KT::TM + TQ * KT::TN) <= 200;
                 constexpr int F = AHEAD ? 2 : 1;
+                static_assert(AHEAD || TQ == 1, "terms read one by one are A's");
                 i32x4 fa[F][TA][KT::TM], fq[F][TQ][KT::TN];
+                auto read_a = [&](int x, int s) {
+#pragma unroll
+                    for (int i = 0; i < KT::TM; ++i)
+                        fa[x % F][s][i] = a_frag<typename KT::OA, AK>(sa + s * KT::OA::BYTES, wm * KT::WTM + i * 16, x * 32, lane);
+                };
+                auto read_q = [&](int x, int s) {
+#pragma unroll
+                    for (int j = 0; j < KT::TN; ++j)
+                        fq[x % F][s][j] = KT::OB::template frag<16>(sq + s * KT::OB::BYTES, wn * KT::WTN + j * 16, x * 32, lane);
+                };
                 auto read = [&](int x) {
+                    if constexpr (AHEAD) {
 #pragma unroll
-                    for (int s = 0; s < TA; ++s)
+                        for (int s = 0; s < TA; ++s) read_a(x, s);
 #pragma unroll
-                        for (int i = 0; i < KT::TM; ++i)
-                            fa[x % F][s][i] = a_frag<typename KT::OA, AK>(sa + s * KT::OA::BYTES, wm * KT::WTM + i * 16, x * 32, lane);
-#pragma unroll
-                    for (int s = 0; s < TQ; ++s)
-#pragma unroll
-                        for (int j = 0; j < KT::TN; ++j)
-                            fq[x % F][s][j] = KT::OB::template frag<16>(sq + s * KT::OB::BYTES, wn * KT::WTN + j * 16, x * 32, lane);
+                        for (int s = 0; s < TQ; ++s) read_q(x, s);
+                    } else {
+                        read_a(x, TA - 1);
+                        read_q(x, 0);
+                    }
                 };
                 // The other stage: every wave has read it before the last barrier.
                 auto next = [&]() {
@@ -437,11 +463,16 @@ gemm_i8grad_kernel(GradParams g)
                     if (AHEAD && x + 1 < KT::NG) read(x + 1);
                     // Small terms first.
 #pragma unroll
-                    for (int s = TA * TQ - 1; s >= 0; --s)
+                    for (int s = TA * TQ - 1; s >= 0; --s) {
 #pragma unroll
                         for (int i = 0; i < KT::TM; ++i)
 #pragma unroll
-                            for (int j = 0; j < KT::TN; ++j) mfma_step<MT, 16>(fa[x % F][s / TQ][i], fq[x % F][s % TQ][j], acc[i][j]);
+                            for (int j = 0; j < KT::TN; ++j)
+                                mfma_step<In::BF16, 16>(fa[x % F][s / TQ][i], fq[x % F][s % TQ][j], acc[i][j]);
+                        if constexpr (!AHEAD) {
+                            if (s > 0) read_a(x, s - 1);
+                        }
+                    }
                     if (!AHEAD && x + 1 < KT::NG) read(x + 1);
                 }
                 if constexpr (!early) {
@@ -466,11 +497,10 @@ __global__ void __launch_bounds__(NW * 64)
 gemm_i8grad_stream_kernel(GradParams g)
 {
     using GT = GradTypes<TI, TO>;
-    constexpr In MT = GT::MT;
     constexpr int TA = GT::TA, TQ = GT::TQ;
-    using KT = Dma16<MT, TO, BM, BN, BK, 1, 1, 16, 2, AK, false>;
-    using OA = AOperand<TI, BM, BK, 1, AK, GT::SPLIT_A, VEC, D>;
-    using OQ = QOperand<MT, BN, BK, 1, TQ, !GT::SPLIT_A, VEC, D>;
+    using KT = Dma16<In::BF16, TO, BM, BN, BK, 1, 1, 16, 2, AK, false>;
+    using OA = AOperand<TI, BM, BK, 1, AK, TA, VEC, D>;
+    using OQ = QOperand<BN, BK, 1, TQ, VEC, D>;
     constexpr int STAGE = TA * KT::OA::BYTES + TQ * KT::OB::BYTES, PART = BM * BN;
     constexpr int SMEM = NW * (STAGE > PART * 4 ? STAGE : PART * 4);
     static_assert(SMEM <= 160 * 1024, "LDS budget");
@@ -523,7 +553,7 @@ gemm_i8grad_stream_kernel(GradParams g)
 #pragma unroll
                     for (int i = 0; i < KT::TM; ++i)
 #pragma unroll
-                        for (int j = 0; j < KT::TN; ++j) mfma_step<MT, 16>(fa[s / TQ][i], fq[s % TQ][j], acc[i][j]);
+                        for (int j = 0; j < KT::TN; ++j) mfma_step<In::BF16, 16>(fa[s / TQ][i], fq[s % TQ][j], acc[i][j]);
             }
             __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): read, the next tile may be written
             asm volatile("" ::: "memory");
@@ -558,7 +588,7 @@ struct GradCall {
     bool vec;             // A and Q allow 16-byte loads
 };
 
-inline GradShape shape_of(const GradCall& c, bool wide, bool split_a) { return {c.vec, wide, split_a, c.g.p.M, c.g.p.N, c.g.p.K}; }
+inline GradShape shape_of(const GradCall& c, bool wide, bool split_a) { return {c.vec, wide, split_a, c.g.p.M, c.g.p.N, c.g.p.K, c.a_kmajor}; }
 
 template <In TI, Out TO>
 struct GradInst {
@@ -591,21 +621,28 @@ struct GradInst {
     template <bool AK, bool VEC>
     static hipError_t go(const GradCall& c, hipStream_t s)
     {
-        const GradTile t = grad_tile(shape_of(c, WIDE, GT::SPLIT_A));
-        switch (t) {
+        switch (grad_tile(shape_of(c, WIDE, GT::SPLIT_A))) {
         case GradTile::Stream32x32: return stream<GradTile::Stream32x32, AK, VEC>(c, s);
         case GradTile::Stream32x64: return stream<GradTile::Stream32x64, AK, VEC>(c, s);
         case GradTile::T64x64: return tile<GradTile::T64x64, AK, VEC>(c, s);
         case GradTile::T64x128: return tile<GradTile::T64x128, AK, VEC>(c, s);
         case GradTile::T128x128Deep: return tile<GradTile::T128x128Deep, AK, VEC>(c, s);
+        case GradTile::T64x128Two:
+            if constexpr (GT::SPLIT_A && !VEC && (WIDE || AK)) return tile<GradTile::T64x128Two, AK, VEC>(c, s);
+            break;
+        case GradTile::T128x128:
+            if constexpr (WIDE ? !GT::SPLIT_A : VEC || !AK) return tile<GradTile::T128x128, AK, VEC>(c, s);
+            break;
+        case GradTile::T256x256:
+            if constexpr (!WIDE && VEC) return tile<GradTile::T256x256, AK, VEC>(c, s);
+            break;
+        case GradTile::Tall256x128:
+            if constexpr (WIDE && !GT::SPLIT_A && VEC) return tile<GradTile::Tall256x128, AK, VEC>(c, s);
+            break;
+        case GradTile::Wide128x256:
+            if constexpr (GT::SPLIT_A && VEC) return tile<GradTile::Wide128x256, AK, VEC>(c, s);
+            break;
         default: break;
-        }
-        if constexpr (GT::SPLIT_A) {
-            if constexpr (!VEC) return tile<GradTile::T64x128Two, AK, false>(c, s);
-            else return tile<GradTile::Wide128x256, AK, true>(c, s);
-        } else {
-            if (t == GradTile::T128x128) return tile<GradTile::T128x128, AK, VEC>(c, s);
-            if constexpr (VEC) return tile<WIDE ? GradTile::Tall256x128 : GradTile::T256x256, AK, true>(c, s);
         }
         return hipErrorInvalidValue;
     }

@@ -447,9 +447,9 @@ int gemm_run_i8(int64_t M, int64_t N, int64_t K, char a_major, char b_major, cha
  * (tokens x in) sums over output channels: A the same gradient, a_major 'k', Q
  * the 8-bit weights (out x in) with their scales.
  *
- * Sums are fp32.  Into 16-bit C, scales[k] * Q[n][k] enters rounded to A's
- * type, as gemm_dequantize_rows gives it.  Into fp32 C, scales[k] * Q[n][k] (bf16
- * A) or scales[k] * A[m][k] (fp16 and fp32 A), rounded to fp32, enters whole.
+ * Sums are fp32.  Into fp32 C, scales[k] * Q[n][k] (bf16 A) or scales[k] * A[m][k]
+ * (fp16 and fp32 A), rounded to fp32, enters whole; into 16-bit C, scales[k] *
+ * A[m][k], rounded to fp32, enters to 2^-16 of itself.
  * An infinity or NaN in A or scales makes infinities or NaN of what it reaches
  * (into fp32 C an infinity may come out as NaN).
  * accumulate adds to C in fp32 before the rounding to C's type.  K == 0 writes

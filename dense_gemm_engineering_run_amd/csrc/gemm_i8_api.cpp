@@ -125,9 +125,7 @@ int run(int64_t M, int64_t N, int64_t K, char a, char b, char c, int type, const
     }
     q.s = mg::I8Scales{scale_a, scale_b};
     q.vec = vec;
-    const mg::I8Shape shape = mg::shape_of(q);
-    const mg::Tile& tile = mg::kI8Tiles[(int)mg::i8_tile(shape)];
-    if (mg::i8_grid(shape, tile) > mg::kMaxGridThreads / tile.threads) return GEMM_ERR_BAD_SHAPE;
+    if (!mg::i8_fits(mg::shape_of(q))) return GEMM_ERR_BAD_SHAPE;
     hipError_t e = launch_parts(q, type, eo, (hipStream_t)stream);
     const int st = e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
     if (mg::log_enabled())

@@ -108,6 +108,12 @@ inline int64_t i8_cost(const I8Shape& s)
     const int64_t a_cu = !s.vec && t.bm == 128 && t.bn == 128 ? 2 : 1;
     return ceil_div(i8_grid(s, t), 256 * a_cu) * a_cu * t.bm * t.bn * s.K;
 }
+// A launch can have its grid.
+inline bool i8_fits(const I8Shape& s)
+{
+    const Tile& t = kI8Tiles[(int)i8_tile(s)];
+    return i8_grid(s, t) <= kMaxGridThreads / t.threads;
+}
 struct I8Edges {
     int64_t rows, cols;
 };
@@ -118,7 +124,10 @@ inline I8Edges i8_edges(const I8Shape& s)
     I8Edges best = {0, 0};
     int64_t least = i8_cost(s);
     for (const I8Edges e : {I8Edges{0, n}, I8Edges{m, 0}, I8Edges{m, n}}) {
-        const int64_t cost = i8_cost({s.vec, s.M - e.rows, s.N - e.cols, s.K}) + call * ((e.rows != 0) + (e.cols != 0));
+        const I8Shape rest = {s.vec, s.M - e.rows, s.N - e.cols, s.K}, rows = {s.vec, e.rows, s.N, s.K},
+                      cols = {s.vec, s.M - e.rows, e.cols, s.K};
+        if (!i8_fits(rest) || !i8_fits(rows) || !i8_fits(cols)) continue;
+        const int64_t cost = i8_cost(rest) + call * ((e.rows != 0) + (e.cols != 0));
         if (cost < least) {
             least = cost;
             best = e;

@@ -1,0 +1,58 @@
+"""What the 8-bit calls launch (CPU only): the host's rules, compiled as they
+stand."""
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+SOURCE = r"""
+#include <cstdio>
+#include "gemm_i8_tiles.hpp"
+int main()
+{
+    int vec;
+    long long M, N, K;
+    while (std::scanf("%d %lld %lld %lld", &vec, &M, &N, &K) == 4) {
+        const mg::I8Edges e = mg::i8_edges({!!vec, M, N, K});
+        std::printf("%d %d", (int)e.rows, (int)e.cols);
+        // Threads of the parts: what is left, the rows at the end, the columns at the end.
+        const long long parts[3][2] = {{M - e.rows, N - e.cols}, {e.rows, N}, {M - e.rows, e.cols}};
+        for (const auto& p : parts) {
+            const mg::I8Shape s = {!!vec, p[0], p[1], K};
+            const mg::Tile& t = mg::kI8Tiles[(int)mg::i8_tile(s)];
+            std::printf(" %lld", p[0] && p[1] ? (long long)mg::i8_grid(s, t) * t.threads : 0);
+        }
+        std::printf("\n");
+    }
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def edges(tmp_path_factory):
+    d = tmp_path_factory.mktemp("launches8")
+    (d / "rules.cpp").write_text(SOURCE)
+    exe = str(d / "rules")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I", os.path.join(ROOT, "dense_gemm_engineering_run_amd", "csrc"),
+                    str(d / "rules.cpp"), "-o", exe], check=True)
+
+    def run(shapes):
+        """Per (aligned, M, N, K): rows, columns cut off and the parts' threads."""
+        text = "\n".join(f"{int(a)} {M} {N} {K}" for a, M, N, K in shapes)
+        out = subprocess.run([exe], input=text, check=True, capture_output=True, text=True).stdout
+        got = [tuple(map(int, line.split())) for line in out.splitlines()]
+        assert len(got) == len(shapes)
+        return got
+
+    return run
+
+
+def test_the_parts_of_a_launch_that_fits_fit(edges):
+    """What has no cut is refused by the entry point where it is too large."""
+    long = [1 << 30, (1 << 30) - 126, (1 << 29) + 130, (1 << 23) + 5]
+    shapes = [(vec, *s, K) for vec in (True, False) for n in (130, 144, 258, 1026) for m in long for s in ((m, n), (n, m))
+              for K in (1, 16, 4096, 131071)]
+    for s, got in zip(shapes, edges(shapes)):
+        if got[0] or got[1]:
+            assert max(got[2:]) < 1 << 32, (s, got)

@@ -96,17 +96,27 @@ inline I8Tile i8_tile(const I8Shape& s)
 inline int64_t i8_grid(const I8Shape& s, const Tile& t) { return ceil_div(s.M, t.bm) * ceil_div(s.N, t.bn); }
 
 // C's last columns and rows, up to 16 past a multiple of 128, can go to calls of
-// their own behind the rest: where that saves the CUs a round of tiles, or lets a
-// smaller tile do, and what it saves is more than such a call's 5 to 12 us (20 *
-// 2^20 of a tile's products; the unaligned 128x128 tile runs twice a CU).
-// us, in brackets without: 8193 x 4096 x 4096 133 (159); 2049 rows of it 45.5
-// (51.2); 4100 x 4104 x 2048 54 (66); 4095 x 2049 x 1028 into fp32 28.1 (34.9);
-// unaligned, on 128x128 tiles, 35.0 (41.1), 2048 x 4100 x 4096 83 (97).
+// their own behind the rest, where that saves the CUs a round of tiles or lets a
+// smaller tile do.  Costs in products of one CU, about 4 * 2^20 a us: rounds of
+// tiles (an unaligned 128x128 tile shares its CU where there are more than 256),
+// and for an edge's call 16 * 2^20 for being one, with its own rounds or, where
+// that is more, the bytes that it reads (an edge of a long C reads the long
+// operand once more; 1 us is as many).  us, in brackets without the cut: 8193 x
+// 4096 x 4096 135 (167); 2049 rows of it 45.4 (49.9); 4100 x 4104 x 2048 55 (68);
+// unaligned 2049 x 4096 x 4096 61 (87), 4095 x 2049 x 1028 into fp32 31 (39).  Left
+// whole: 65536 x 144 x 2048 87 (51), 130 x 65536 x 2048 67 (50), unaligned 16384 x
+// 130 x 4096 60 (43).  Of 328 such sizes the worst is 9 % off its better way.
 inline int64_t i8_cost(const I8Shape& s)
 {
     const Tile& t = kI8Tiles[(int)i8_tile(s)];
-    const int64_t a_cu = !s.vec && t.bm == 128 && t.bn == 128 ? 2 : 1;
-    return ceil_div(i8_grid(s, t), 256 * a_cu) * a_cu * t.bm * t.bn * s.K;
+    const int64_t grid = i8_grid(s, t), a_cu = !s.vec && t.bm == 128 && t.bn == 128 && grid > 256 ? 2 : 1;
+    return ceil_div(grid, 256 * a_cu) * a_cu * t.bm * t.bn * s.K;
+}
+inline int64_t i8_edge_cost(const I8Shape& s)
+{
+    if (s.M == 0 || s.N == 0) return 0;
+    const int64_t cost = i8_cost(s), bytes = (s.M + s.N) * s.K;
+    return (16 << 20) + (cost > bytes ? cost : bytes);
 }
 // A launch can have its grid.
 inline bool i8_fits(const I8Shape& s)
@@ -119,7 +129,6 @@ struct I8Edges {
 };
 inline I8Edges i8_edges(const I8Shape& s)
 {
-    const int64_t call = 20 << 20;
     const int64_t m = s.M > 128 && s.M % 128 <= 16 ? s.M % 128 : 0, n = s.N > 128 && s.N % 128 <= 16 ? s.N % 128 : 0;
     I8Edges best = {0, 0};
     int64_t least = i8_cost(s);
@@ -127,7 +136,7 @@ inline I8Edges i8_edges(const I8Shape& s)
         const I8Shape rest = {s.vec, s.M - e.rows, s.N - e.cols, s.K}, rows = {s.vec, e.rows, s.N, s.K},
                       cols = {s.vec, s.M - e.rows, e.cols, s.K};
         if (!i8_fits(rest) || !i8_fits(rows) || !i8_fits(cols)) continue;
-        const int64_t cost = i8_cost(rest) + call * ((e.rows != 0) + (e.cols != 0));
+        const int64_t cost = i8_cost(rest) + i8_edge_cost(rows) + i8_edge_cost(cols);
         if (cost < least) {
             least = cost;
             best = e;

@@ -56,3 +56,17 @@ def test_the_parts_of_a_launch_that_fits_fit(edges):
     for s, got in zip(shapes, edges(shapes)):
         if got[0] or got[1]:
             assert max(got[2:]) < 1 << 32, (s, got)
+
+
+def test_edges_of_long_products_are_priced_by_their_length(edges):
+    """Sizes measured with and without the cut, the faster one by 10 % and more
+    (K in a multiple of 16 bytes, or at any byte)."""
+    whole = [(True, 65536, 130, 2048), (True, 65536, 144, 2048), (True, 130, 65536, 2048), (True, 144, 32768, 4096),
+             (True, 32768, 260, 2048), (True, 260, 8192, 4096), (True, 65536, 272, 512), (True, 16384, 130, 4096),
+             (False, 130, 65536, 2048), (False, 65536, 260, 2048), (False, 16384, 130, 4096), (False, 130, 16384, 2048),
+             (False, 8192, 272, 2048), (False, 260, 8192, 4096)]
+    assert [got[:2] for got in edges(whole)] == [(0, 0)] * len(whole)
+    cut = [(True, 8193, 4096, 4096, 1, 0), (True, 2049, 4096, 4096, 1, 0), (True, 4100, 4104, 2048, 4, 8),
+           (True, 16384, 1030, 1024, 0, 6), (True, 2053, 4096, 2048, 5, 0), (False, 2049, 4096, 4096, 1, 0),
+           (False, 4095, 2049, 1028, 0, 1), (False, 2048, 4112, 2048, 0, 16), (False, 8193, 4096, 4096, 1, 0)]
+    assert [got[:2] for got in edges([s[:4] for s in cut])] == [s[4:] for s in cut]

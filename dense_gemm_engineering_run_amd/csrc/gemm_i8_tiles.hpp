@@ -218,8 +218,8 @@ struct GradShape {
 //   8192 x 4096, 4096     713 (846)   752 (719)      656 (665)       627 (840)
 //     64 x 65536, 2048     58  (62)    60  (55)       90  (83)        88 (110)
 //
-// fp32 C: the largest that fills most of the CUs.  us, bf16 into fp32 / fp32, A
-// m-major (k-major is within a few percent):
+// fp32 C: the largest that fills most of the CUs, but for a narrow C.  us, bf16 into
+// fp32 / fp32, A m-major (k-major in brackets, else within a few percent):
 //   M x N, K              32x32 str.   32x64 str.    64x64        64x128       128x128, deep
 //    512 x  256, 1000      7.2/7.7       10/9.6      13/16         21/19
 //     32 x 4096, 4096       16/18        26/22       42/50
@@ -227,14 +227,26 @@ struct GradShape {
 //   1024 x 1024, 4096       64/77        52/44       44/50         71/65         88/ -
 //   2048 x 1024, 4096                                83/97         71/66         - /92
 //   2048 x 2048, 4096                               165/192       142/113        95/104
-//                          64x128      128x128      256x128 | 128x256 (Q's terms, A's terms)
-//   4096 x 2048, 1024       80/61        50/74       49/54
-//   3008 x 2000, 3008      158/126      123/197     113/118
-//   4096 x 4096, 2048       - /225      181/ -      176/179
-//   8192 x 2048, 1024       - /115       94/ -       98/94
-// Unaligned: 2049 x 1028, 4095 k takes 141/136 on 64x128, 95/96 on 128x128, deep (153
-// tiles); 3000 x 2000, 3001 k - /127 on 64x128, - /197 on 128x128, - /134 on 64x128
-// with two a CU (k-major - /129, 159 on 64x128).
+//                          64x128        128x128     256x128 | 128x256 (Q's terms, A's terms)
+//   4096 x 2048, 1024       80/61         50/74       49/54
+//   2304 x 1952,   64       13/9.8 (12/12) 8.1/12     8.5/8.4 (8.7/8.5)
+//   2304 x 1952, 2048      110/83 (105/97) 81/131     77/80 (74/76)
+//   2600 x 1952, 2048      113/87 (107/99) 83/132     78/82 (74/78)
+//   3008 x 2000, 3008      158/126       123/197     113/118
+//   4096 x 4096, 2048       - /225       181/ -      176/179
+//   8192 x 2048, 1024       - /115        94/ -       98/94
+//     64 x 65536, 2048      81/67 (78/72) 101/ -     182/101 (145/88)
+//    128 x 65536, 1024      81/64 (78/73)  50/ -      92/52 (79/50)
+//  65536 x   64, 2048      155/144       107/150     101/206; 64x64: 101/128
+//  65536 x  128, 1024       85/78 (87/88)  56/81      56/111; 128x128, deep: 60/70 (62/76)
+// Unaligned                64x128     two a CU    128x128, deep  128x128
+//   2049 x 1028, 4095      141/135     146/111        95/96      113/137
+//   2304 x 1950, 2048      111/107     115/92         98/100      84/139
+//   3000 x 2000, 3001      161/155     169/138       141/144     127/201
+//     64 x 65536, 2048      82/76       84/67        110/113     101/141
+//    128 x 65536, 1024      81/78       83/68         57/59       51/75
+//  65536 x   64, 2048      162/161     162/149       115/134     109/155; 64x64: 106/135
+//  65536 x  128, 1024       87/88       89/79         62/72       60/84
 inline GradTile grad_tile(const GradShape& s)
 {
     auto tiles = [&](int bm, int bn) { return ceil_div(s.M, bm) * ceil_div(s.N, bn); };
@@ -243,8 +255,8 @@ inline GradTile grad_tile(const GradShape& s)
     if (tiles(64, 64) <= 256) return GradTile::T64x64;
     if (tiles(64, 128) <= 256) return GradTile::T64x128;
     if (tiles(128, 128) <= 256) return GradTile::T128x128Deep;
+    if (s.M <= 64) return s.wide && s.split_a && !s.vec ? GradTile::T64x128Two : GradTile::T64x128;
     if (!s.wide) {
-        if (s.M <= 64) return GradTile::T64x128;
         if (!s.vec) return s.a_kmajor ? GradTile::T64x128Two : GradTile::T128x128;
         if (s.N <= 64) return GradTile::T64x64;
         if (s.N <= 128) return GradTile::T128x128;
@@ -252,10 +264,12 @@ inline GradTile grad_tile(const GradShape& s)
         return s.K <= 128 && !s.a_kmajor ? GradTile::T128x128 : GradTile::Wide128x256;
     }
     if (s.split_a) {
+        if (s.N <= 64) return GradTile::T64x64;
+        if (s.N <= 128 || (!s.vec && s.M <= 128)) return GradTile::T128x128Deep;
         if (!s.vec) return GradTile::T64x128Two;
-        return tiles(128, 256) >= 160 ? GradTile::Wide128x256 : GradTile::T64x128;
+        return s.a_kmajor || tiles(128, 256) >= 160 ? GradTile::Wide128x256 : GradTile::T64x128;
     }
-    if (!s.vec) return GradTile::T128x128;
+    if (!s.vec || s.M <= 128) return GradTile::T128x128;
     return tiles(256, 128) >= 160 ? GradTile::Tall256x128 : GradTile::T128x128;
 }
 

@@ -96,3 +96,14 @@ def test_an_infinity_of_a_keeps_its_sign(dtype, a_major, aligned, M, N):
     rest = torch.ones(M, dtype=torch.bool)
     rest[[3, 7]] = False
     assert torch.isfinite(x.c[rest.cuda()]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16_f32", "bf16_f32"])
+@pytest.mark.parametrize("a_major", "mk")
+@pytest.mark.parametrize("aligned", [True, False])
+def test_thin_fp32_outputs(dtype, a_major, aligned):
+    for i, (M, N, K) in enumerate(((64, 40000, 70), (20, 33000, 33), (100, 50000, 130), (40000, 60, 64), (40000, 100, 131), (2304, 1950, 40))):
+        say(dtype, a_major, aligned, M, N, K)
+        at = (None, 0) if aligned else (1, 3)
+        Gradient(M, N, K, dtype, a_major, *at, seed=i).run(accumulate=i % 2 == 1)
+        Gradient(M, N, K, dtype, a_major, *at, "int", seed=i).run(accumulate=i % 2 == 0)

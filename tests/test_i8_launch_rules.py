@@ -9,8 +9,19 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SOURCE = r"""
 #include <cstdio>
 #include "gemm_i8_tiles.hpp"
-int main()
+int grad()
 {
+    int vec, wide, split, kmajor;
+    long long M, N, K;
+    while (std::scanf("%d %d %d %d %lld %lld %lld", &vec, &wide, &split, &kmajor, &M, &N, &K) == 7) {
+        const mg::GradTile t = mg::grad_tile({!!vec, !!wide, !!split, M, N, K, !!kmajor});
+        std::printf("%s\n", mg::kGradTiles[(int)t].name);
+    }
+    return 0;
+}
+int main(int argc, char**)
+{
+    if (argc > 1) return grad();
     int vec;
     long long M, N, K;
     while (std::scanf("%d %lld %lld %lld", &vec, &M, &N, &K) == 4) {
@@ -30,19 +41,35 @@ int main()
 
 
 @pytest.fixture(scope="module")
-def edges(tmp_path_factory):
+def exe(tmp_path_factory):
     d = tmp_path_factory.mktemp("launches8")
     (d / "rules.cpp").write_text(SOURCE)
     exe = str(d / "rules")
     subprocess.run(["g++", "-std=c++17", "-O1", "-I", os.path.join(ROOT, "dense_gemm_engineering_run_amd", "csrc"),
                     str(d / "rules.cpp"), "-o", exe], check=True)
+    return exe
 
+
+@pytest.fixture(scope="module")
+def edges(exe):
     def run(shapes):
         """Per (aligned, M, N, K): rows, columns cut off and the parts' threads."""
         text = "\n".join(f"{int(a)} {M} {N} {K}" for a, M, N, K in shapes)
         out = subprocess.run([exe], input=text, check=True, capture_output=True, text=True).stdout
         got = [tuple(map(int, line.split())) for line in out.splitlines()]
         assert len(got) == len(shapes)
+        return got
+
+    return run
+
+
+@pytest.fixture(scope="module")
+def grad(exe):
+    def run(calls):
+        """Per (aligned, fp32 C, terms of A, A k-major, M, N, K): the tile's name."""
+        text = "\n".join(" ".join(str(int(x)) for x in c) for c in calls)
+        got = subprocess.run([exe, "grad"], input=text, check=True, capture_output=True, text=True).stdout.splitlines()
+        assert len(got) == len(calls)
         return got
 
     return run
@@ -70,3 +97,25 @@ def test_edges_of_long_products_are_priced_by_their_length(edges):
            (True, 16384, 1030, 1024, 0, 6), (True, 2053, 4096, 2048, 5, 0), (False, 2049, 4096, 4096, 1, 0),
            (False, 4095, 2049, 1028, 0, 1), (False, 2048, 4112, 2048, 0, 16), (False, 8193, 4096, 4096, 1, 0)]
     assert [got[:2] for got in edges([s[:4] for s in cut])] == [s[4:] for s in cut]
+
+
+# Gradients into a thin fp32 C: M, N, K, and where the tile that many tiles of it
+# would take is 10 % and more behind, the fastest: bf16 A (Q's terms), others (A's)
+THIN = [(64, 65536, 2048, "64x128", "64x128"), (16, 65536, 2048, "64x128", "64x128"), (100, 65536, 1024, "128x128", None),
+        (65536, 64, 2048, None, "64x64"), (65536, 16, 2048, None, "64x64"), (65536, 128, 1024, None, "128x128, deep")]
+
+
+def test_thin_fp32_gradients_run_tiles_that_fit_them(grad):
+    calls, want = [], []
+    for M, N, K, q, a in THIN:
+        for split, name in ((False, q), (True, a)):
+            for kmajor in (False, True) if name else ():
+                calls.append((True, True, split, kmajor, M, N, K))
+                want.append(name)
+    assert grad(calls) == want
+
+
+def test_inputs_gradients_of_a_tile_for_most_cus(grad):
+    """A k-major, 129 to 160 tiles of 128 x 256: 64x128 tiles take 5 to 27 % longer."""
+    assert grad([(True, True, True, True, *s) for s in ((2304, 1952, 2048), (20000, 256, 1000), (8192, 528, 2048), (1104, 4000, 1024))]) \
+        == ["128x256"] * 4

@@ -170,7 +170,7 @@ int run_grad(int64_t M, int64_t N, int64_t K, char a, char b, char c, int dtype,
     q.a_kmajor = a == 'k';
     q.vec = vec;
     const mg::GradShape shape = mg::shape_of(q, eo == 4, dtype != GEMM_DTYPE_BF16_F32);
-    const mg::Tile& tile = mg::kGradTiles[(int)mg::grad_tile(shape)];
+    const mg::Tile tile = mg::tile_of(mg::grad_tile(shape), shape.wide, shape.split_a, shape.a_kmajor);
     if (mg::grad_grid(shape, tile) > mg::kMaxGridThreads / tile.threads) return GEMM_ERR_BAD_SHAPE;
     const int st = kGradLaunch[dtype](q, (hipStream_t)stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
     if (mg::log_enabled())

@@ -178,6 +178,23 @@ constexpr Tile deep_tile(bool wide, bool split_a, bool a_kmajor)
     if (!split_a) return {"", 128, 128, 64, 2, 4, 16, 1, 2, 512};
     return !wide || a_kmajor ? kGradTiles[(int)GradTile::T128x128Deep] : Tile{"", 128, 128, 64, 4, 2, 16, 1, 2, 512};
 }
+// What runs as tile t in a kind of call.
+constexpr Tile tile_of(GradTile t, bool wide, bool split_a, bool a_kmajor)
+{
+    return t == GradTile::T128x128Deep ? deep_tile(wide, split_a, a_kmajor) : tile_of(t);
+}
+// The kinds of calls that each tile has a kernel for.
+constexpr bool has_kernel(GradTile t, bool vec, bool wide, bool split_a, bool a_kmajor)
+{
+    switch (t) {
+    case GradTile::T64x128Two: return split_a && !vec && (wide || a_kmajor);
+    case GradTile::T128x128: return wide ? !split_a : vec || !a_kmajor;
+    case GradTile::T256x256: return !wide && vec;
+    case GradTile::Tall256x128: return wide && !split_a && vec;
+    case GradTile::Wide128x256: return split_a && vec;
+    default: return true;
+    }
+}
 
 struct GradShape {
     bool vec;             // A and Q allow 16-byte loads

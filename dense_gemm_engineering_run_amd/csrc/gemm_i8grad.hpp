@@ -605,46 +605,34 @@ struct GradInst {
         return hipLaunchKernel(kernel, dim3((unsigned)grad_grid(shape_of(c, WIDE, GT::SPLIT_A), t)), dim3(t.threads), args, 0, s);
     }
     template <GradTile T, bool AK, bool VEC>
-    static hipError_t stream(const GradCall& c, hipStream_t s)
-    {
-        constexpr Tile t = tile_of(T);
-        return run((const void*)&gemm_i8grad_stream_kernel<TI, TO, t.bm, t.bn, t.bk, t.extra, t.stages, AK, VEC>, c, t, s);
-    }
-    template <GradTile T, bool AK, bool VEC>
     static hipError_t tile(const GradCall& c, hipStream_t s)
     {
-        constexpr Tile t = T == GradTile::T128x128Deep ? deep_tile(WIDE, GT::SPLIT_A, AK) : tile_of(T);
-        return run(c.g.p.epi ? (const void*)&gemm_i8grad_kernel<TI, TO, t.bm, t.bn, t.bk, t.wm, t.wn, t.stages, t.extra, AK, VEC, true>
-                             : (const void*)&gemm_i8grad_kernel<TI, TO, t.bm, t.bn, t.bk, t.wm, t.wn, t.stages, t.extra, AK, VEC, false>,
-                   c, t, s);
+        constexpr Tile t = tile_of(T, WIDE, GT::SPLIT_A, AK);
+        if constexpr (!has_kernel(T, VEC, WIDE, GT::SPLIT_A, AK))
+            return hipErrorInvalidValue;
+        else if constexpr (T == GradTile::Stream32x32 || T == GradTile::Stream32x64)
+            return run((const void*)&gemm_i8grad_stream_kernel<TI, TO, t.bm, t.bn, t.bk, t.extra, t.stages, AK, VEC>, c, t, s);
+        else
+            return run(c.g.p.epi ? (const void*)&gemm_i8grad_kernel<TI, TO, t.bm, t.bn, t.bk, t.wm, t.wn, t.stages, t.extra, AK, VEC, true>
+                                 : (const void*)&gemm_i8grad_kernel<TI, TO, t.bm, t.bn, t.bk, t.wm, t.wn, t.stages, t.extra, AK, VEC, false>,
+                       c, t, s);
     }
     template <bool AK, bool VEC>
     static hipError_t go(const GradCall& c, hipStream_t s)
     {
         switch (grad_tile(shape_of(c, WIDE, GT::SPLIT_A))) {
-        case GradTile::Stream32x32: return stream<GradTile::Stream32x32, AK, VEC>(c, s);
-        case GradTile::Stream32x64: return stream<GradTile::Stream32x64, AK, VEC>(c, s);
+        case GradTile::Stream32x32: return tile<GradTile::Stream32x32, AK, VEC>(c, s);
+        case GradTile::Stream32x64: return tile<GradTile::Stream32x64, AK, VEC>(c, s);
         case GradTile::T64x64: return tile<GradTile::T64x64, AK, VEC>(c, s);
         case GradTile::T64x128: return tile<GradTile::T64x128, AK, VEC>(c, s);
+        case GradTile::T64x128Two: return tile<GradTile::T64x128Two, AK, VEC>(c, s);
         case GradTile::T128x128Deep: return tile<GradTile::T128x128Deep, AK, VEC>(c, s);
-        case GradTile::T64x128Two:
-            if constexpr (GT::SPLIT_A && !VEC && (WIDE || AK)) return tile<GradTile::T64x128Two, AK, VEC>(c, s);
-            break;
-        case GradTile::T128x128:
-            if constexpr (WIDE ? !GT::SPLIT_A : VEC || !AK) return tile<GradTile::T128x128, AK, VEC>(c, s);
-            break;
-        case GradTile::T256x256:
-            if constexpr (!WIDE && VEC) return tile<GradTile::T256x256, AK, VEC>(c, s);
-            break;
-        case GradTile::Tall256x128:
-            if constexpr (WIDE && !GT::SPLIT_A && VEC) return tile<GradTile::Tall256x128, AK, VEC>(c, s);
-            break;
-        case GradTile::Wide128x256:
-            if constexpr (GT::SPLIT_A && VEC) return tile<GradTile::Wide128x256, AK, VEC>(c, s);
-            break;
-        default: break;
+        case GradTile::T128x128: return tile<GradTile::T128x128, AK, VEC>(c, s);
+        case GradTile::T256x256: return tile<GradTile::T256x256, AK, VEC>(c, s);
+        case GradTile::Tall256x128: return tile<GradTile::Tall256x128, AK, VEC>(c, s);
+        case GradTile::Wide128x256: return tile<GradTile::Wide128x256, AK, VEC>(c, s);
+        default: return hipErrorInvalidValue;
         }
-        return hipErrorInvalidValue;
     }
     static hipError_t launch(const GradCall& c, hipStream_t s)
     {

@@ -8,6 +8,7 @@ import pytest
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SOURCE = r"""
 #include <cstdio>
+#include <cstring>
 #include "gemm_i8_tiles.hpp"
 int grad()
 {
@@ -15,7 +16,7 @@ int grad()
     long long M, N, K;
     while (std::scanf("%d %d %d %d %lld %lld %lld", &vec, &wide, &split, &kmajor, &M, &N, &K) == 7) {
         const mg::GradTile t = mg::grad_tile({!!vec, !!wide, !!split, M, N, K, !!kmajor});
-        std::printf("%s\n", mg::kGradTiles[(int)t].name);
+        std::printf("%s%s\n", mg::kGradTiles[(int)t].name, mg::has_kernel(t, vec, wide, split, kmajor) ? "" : " (none)");
     }
     return 0;
 }
@@ -34,6 +35,7 @@ int main(int argc, char**)
             const mg::Tile& t = mg::kI8Tiles[(int)mg::i8_tile(s)];
             std::printf(" %lld", p[0] && p[1] ? (long long)mg::i8_grid(s, t) * t.threads : 0);
         }
+        std::printf(" %d", std::strncmp(mg::kI8Tiles[(int)mg::i8_tile({!!vec, M, N, K})].name, "unaligned", 9) != 0);
         std::printf("\n");
     }
 }
@@ -53,7 +55,8 @@ def exe(tmp_path_factory):
 @pytest.fixture(scope="module")
 def edges(exe):
     def run(shapes):
-        """Per (aligned, M, N, K): rows, columns cut off and the parts' threads."""
+        """Per (aligned, M, N, K): rows, columns cut off, the parts' threads, and
+        whether the whole would run a kernel for aligned operands."""
         text = "\n".join(f"{int(a)} {M} {N} {K}" for a, M, N, K in shapes)
         out = subprocess.run([exe], input=text, check=True, capture_output=True, text=True).stdout
         got = [tuple(map(int, line.split())) for line in out.splitlines()]
@@ -82,7 +85,25 @@ def test_the_parts_of_a_launch_that_fits_fit(edges):
               for K in (1, 16, 4096, 131071)]
     for s, got in zip(shapes, edges(shapes)):
         if got[0] or got[1]:
-            assert max(got[2:]) < 1 << 32, (s, got)
+            assert max(got[2:5]) < 1 << 32, (s, got)
+
+
+SIZES = [1, 15, 16, 31, 33, 64, 65, 100, 128, 130, 257, 400, 1000, 1950, 2304, 4096, 10000, 30000, 65536, 1 << 20]
+
+
+def test_every_product_has_a_kernel_for_its_operands(edges):
+    shapes = [(vec, M, N, K) for vec in (True, False) for M in SIZES for N in SIZES for K in (1, 100, 4096)]
+    assert all(bool(got[5]) == s[0] for s, got in zip(shapes, edges(shapes)))
+
+
+def test_every_gradient_has_a_kernel(grad):
+    """16-bit C: A's terms; fp32 C: A's or Q's."""
+    calls = [(vec, wide, split, kmajor, M, N, K) for vec in (True, False) for wide, split in ((False, True), (True, True), (True, False))
+             for kmajor in (True, False) for M in SIZES for N in SIZES for K in (1, 100, 129, 4096)]
+    names = grad(calls)
+    assert not [c for c, name in zip(calls, names) if "none" in name]
+    # ... and every tile runs for some call.
+    assert len(set(names)) == 10
 
 
 def test_edges_of_long_products_are_priced_by_their_length(edges):

@@ -449,7 +449,8 @@ int gemm_run_i8(int64_t M, int64_t N, int64_t K, char a_major, char b_major, cha
  *
  * Sums are fp32.  Into fp32 C, scales[k] * Q[n][k] (bf16 A) or scales[k] * A[m][k]
  * (fp16 and fp32 A), rounded to fp32, enters whole; into 16-bit C, scales[k] *
- * A[m][k], rounded to fp32, enters to 2^-16 of itself.
+ * A[m][k], rounded to fp32, enters to 2^-16 of itself.  Bits of it below 2^-133 are
+ * lost (it enters whole from 2^-110 on, to 2^-16 of itself from 2^-118 on).
  * An infinity or NaN in A or scales makes infinities or NaN of what it reaches
  * (into fp32 C an infinity may come out as NaN).
  * accumulate adds to C in fp32 before the rounding to C's type.  K == 0 writes

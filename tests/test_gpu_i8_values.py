@@ -5,7 +5,10 @@ of itself), its first 8 bits cut off (the rest is less than 2^-7 of it), the res
 rounded to 8 bits (2^-9 of that): 2^-24 + 2^-16 of itself.  The sum has 2 K fp32
 terms.  With S = sum_k |A| |scales Q|,
     E = (2 K + 1) 2^-24 S + 2^-16 S,    then the rounding to C: eps(C) / 2 (|ref| + E)
-(2^-25 more for fp16's subnormals).
+(2^-25 more for fp16's subnormals).  Into fp32 C three terms hold the product whole:
+(3 K + 2) 2^-24 S.  Of a term, bits below bf16's smallest subnormal are lost: 2^-133
+times the other factor more for every k (and fp32's own, a few 2^-149 for every
+addition).
 """
 import pytest
 import torch
@@ -107,3 +110,24 @@ def test_thin_fp32_outputs(dtype, a_major, aligned):
         at = (None, 0) if aligned else (1, 3)
         Gradient(M, N, K, dtype, a_major, *at, seed=i).run(accumulate=i % 2 == 1)
         Gradient(M, N, K, dtype, a_major, *at, "int", seed=i).run(accumulate=i % 2 == 0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16_f32", "bf16_bf16"])
+@pytest.mark.parametrize("a_major", "mk")
+@pytest.mark.parametrize("exponent", [-105, -110, -114, -118, -122, -127, -131])
+def test_factors_near_the_end_of_the_range(dtype, a_major, exponent):
+    """scales near 2^exponent, A near 1: what is lost is no more than the bits below 2^-133."""
+    for M, N, K in ((40, 48, 64), (300, 600, 40), (2048, 2048, 64)):
+        x = Gradient(M, N, K, dtype, a_major, None)
+        a = torch.randn((M, K), generator=torch.Generator().manual_seed(1)).clamp(-4, 4)
+        x.a.copy_(a)
+        x.s.copy_(((1 + ints((K,), 2, 0, 1023).double() / 1024) * 2.0 ** exponent).float())
+        A, Q, s = x.a.double(), x.q.double(), x.s.double()
+        ref, S = A @ (s[:, None] * Q.t()), A.abs() @ (s[:, None] * Q.t().abs())
+        other = A.abs().sum(1, keepdim=True) if dtype == "bf16_f32" else Q.abs().sum(1)
+        E = (3 * K + 2) * 2.0 ** -24 * S + 2.0 ** -133 * other + 3 * K * 2.0 ** -149
+        if dtype == "bf16_bf16":
+            E = E + 2.0 ** -16 * S + torch.finfo(x.tout).eps / 2 * (ref.abs() + E) + 2.0 ** -134
+        g.gemm_i8_grad(x.a, x.q, x.s, x.c)
+        diff = (x.c.double() - ref).abs()
+        assert bool((diff <= E).all()), float((diff / E).max())

@@ -69,8 +69,15 @@ struct I8Shape {
 //   3000 of 4095 x 2047                              156      87.0    53.8     60.2
 //   8192 of 4096 x 1024                                               71.4     73.1
 //   8192 of 4096 x 4096                                              241.4    215.1
-// (Two 128x128 tiles share a CU, and a last round of few of them is short; a
-// 128x256 tile has one for itself.)
+// Two 128x128 tiles share a CU, a 128x256 tile has one for itself: the wide ones
+// lose where their last round would be half a round or less of the others, and
+// for short K.  Times of 128x256 to 128x128, by how many tiles the last round has
+// (2048 columns, 4224 to 16384 rows; bf16 / fp32 outputs):
+//   K          up to 128 of 256    160 to 224        256
+//    512         1.13-1.15/1.22   .97-.99/1.03-1.06  1.04/1.01
+//   1000, 1500   1.12-1.18/1.19   .95-.97/.98-1.03   1.02/1.00
+//   2000, 2500   1.09-1.17/1.19   .93-.97/.95-1.00   .94-.98/.97
+//   4096         1.04-1.16/1.16   .90-.92/.92-.94    .85-.92/.92
 inline I8Tile i8_tile(const I8Shape& s)
 {
     auto tiles = [&](int bm, int bn) { return ceil_div(s.M, bm) * ceil_div(s.N, bn); };
@@ -81,7 +88,7 @@ inline I8Tile i8_tile(const I8Shape& s)
         if (tiles(64, 64) <= 512) return I8Tile::Odd64x64;
         if (tiles(128, 128) <= 256) return I8Tile::Odd128x128;
         const int64_t wide = tiles(128, 256);
-        return wide <= 256 || (s.K >= 2048 && (wide - 1) % 256 >= 160) ? I8Tile::Odd128x256 : I8Tile::Odd128x128;
+        return wide <= 256 || (s.K >= 2048 && (wide - 1) % 256 >= 128) ? I8Tile::Odd128x256 : I8Tile::Odd128x128;
     }
     if (tiles(16, 16) <= 256) return I8Tile::Stream16x16;
     if (tiles(16, 32) <= 256) return I8Tile::Stream16x32;
@@ -264,6 +271,8 @@ struct GradShape {
 //    128 x 65536, 1024      81/78       83/68         57/59       51/75
 //  65536 x   64, 2048      162/161     162/149       115/134     109/155; 64x64: 106/135
 //  65536 x  128, 1024       87/88       89/79         62/72       60/84
+// (For 129 to 159 tiles of 256x128, or of 128x256 with m-major A, the smaller ones
+// take 4 % longer from K = 512 on; at K = 64 128x128 5 % less, 64x128 14 % more.)
 inline GradTile grad_tile(const GradShape& s)
 {
     auto tiles = [&](int bm, int bn) { return ceil_div(s.M, bm) * ceil_div(s.N, bn); };

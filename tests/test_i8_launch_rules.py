@@ -20,11 +20,13 @@ int grad()
     }
     return 0;
 }
-int main(int argc, char**)
+int main(int argc, char** argv)
 {
-    if (argc > 1) return grad();
+    if (argc > 1 && !std::strcmp(argv[1], "grad")) return grad();
     int vec;
     long long M, N, K;
+    while (argc > 1 && std::scanf("%d %lld %lld %lld", &vec, &M, &N, &K) == 4)
+        std::printf("%s\n", mg::kI8Tiles[(int)mg::i8_tile({!!vec, M, N, K})].name);
     while (std::scanf("%d %lld %lld %lld", &vec, &M, &N, &K) == 4) {
         const mg::I8Edges e = mg::i8_edges({!!vec, M, N, K});
         std::printf("%d %d", (int)e.rows, (int)e.cols);
@@ -140,3 +142,14 @@ def test_inputs_gradients_of_a_tile_for_most_cus(grad):
     """A k-major, 129 to 160 tiles of 128 x 256: 64x128 tiles take 5 to 27 % longer."""
     assert grad([(True, True, True, True, *s) for s in ((2304, 1952, 2048), (20000, 256, 1000), (8192, 528, 2048), (1104, 4000, 1024))]) \
         == ["128x256"] * 4
+
+
+def test_unaligned_wide_tiles_by_their_last_round(exe):
+    """128x256 tiles beside 128x128 ones, two of which share a CU: measured 10 to 16 %
+    slower with a last round of 1 to 128 tiles, 5 to 10 % faster with 160 and more."""
+    shapes = [(128 * (n // 8), 2048, K) for K in (2500, 4096) for n in (264, 320, 384, 416, 448, 512, 640, 672, 928)]
+    text = "\n".join(f"0 {M} {N} {K}" for M, N, K in shapes)
+    got = subprocess.run([exe, "product"], input=text, check=True, capture_output=True, text=True).stdout.splitlines()
+    n = "unaligned 128x128"
+    w = "unaligned 128x256"
+    assert got == [n, n, n, w, w, w, n, w, w] * 2

@@ -556,8 +556,9 @@ def _rows8(wide, q, scales, names):
 
 def quantize_rows(x, q, scales, stream=None):
     """Rows of x (M, K) to 8-bit integers q (M, K) and a float32 scale each
-    (gemm_quantize_rows): scales = max |x| / 127 of a row, q = x / scales to the
-    nearest, ties to even.  x and q are row-major.  Returns q and scales."""
+    (gemm_quantize_rows): scales = max |x| / 127 of a row, q = 127 x / max |x| to
+    the nearest integer, ties to even, as if the quotient were exact (not x over the
+    rounded scale).  x and q are row-major.  Returns q and scales."""
     index, M, K, ldx, ldq, code, at = _rows8(x, q, scales, ("x", "q"))
     _launch(_lib.gemm_quantize_rows, index, stream, M, K, code, x.data_ptr(), q.data_ptr(), at, ldx, ldq)
     return q, scales

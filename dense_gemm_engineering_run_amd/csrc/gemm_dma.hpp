@@ -33,7 +33,8 @@
 // read as zeros.  For a k-contiguous operand the elements k >= K of the last,
 // partial k-tile hold whatever follows in memory (padding, possibly NaN), so
 // after that tile lands they are overwritten with zeros in LDS, for both
-// operands, before any wave reads it.
+// operands (of 8-bit integers, which have no NaN, for A only), before any wave
+// reads it.
 #pragma once
 
 #include "gemm_kernel.hpp"

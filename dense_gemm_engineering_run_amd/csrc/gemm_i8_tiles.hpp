@@ -156,6 +156,7 @@ inline I8Edges i8_edges(const I8Shape& s)
 
 // bk: k of a tile; stages: tiles of loads in flight (streaming: a wave's);
 // extra: waves that stream, else waves a SIMD that the registers leave room for.
+// (The deep 128x128 tile here is one of three: deep_tile.)
 enum class GradTile : int {
     Stream32x32, Stream32x64, T64x64, T64x128, T64x128Two, T128x128Deep, T128x128, T256x256, Tall256x128, Wide128x256, Count
 };

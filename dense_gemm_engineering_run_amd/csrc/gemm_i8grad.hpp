@@ -127,7 +127,8 @@ struct Walk {
     }
 };
 
-// Eight bytes of a row: from any byte (three words, shifted), or 8-byte aligned.
+// Eight bytes of a row: from any byte (three words, shifted), or of a 16-byte
+// aligned one.
 template <bool VEC>
 struct ByteChunk8 {
     int w0, w1, w2;
@@ -371,8 +372,8 @@ struct AOperand {
 };
 
 // LDS in two stages, D tiles of loads in flight; while a tile is multiplied the
-// next one is scaled, converted and written.  VEC: 16-byte aligned A, 8-byte
-// aligned Q; else any element and byte.  EPI: added to C.
+// next one is scaled, converted and written.  VEC: 16-byte aligned A and Q; else
+// any element and byte.  EPI: added to C.
 template <In TI, Out TO, int BM, int BN, int BK, int WM, int WN, int D, int OCC, bool AK, bool VEC, bool EPI>
 __global__ void __launch_bounds__(WM * WN * 64, OCC)
 gemm_i8grad_kernel(GradParams g)

@@ -131,3 +131,15 @@ def test_factors_near_the_end_of_the_range(dtype, a_major, exponent):
         g.gemm_i8_grad(x.a, x.q, x.s, x.c)
         diff = (x.c.double() - ref).abs()
         assert bool((diff <= E).all()), float((diff / E).max())
+
+
+@pytest.mark.parametrize("dtype", NARROW)
+@pytest.mark.parametrize("a_major", "mk")
+@pytest.mark.parametrize("aligned", [True, False])
+def test_thin_16_bit_outputs_and_short_sums(dtype, a_major, aligned):
+    for i, (M, N, K) in enumerate(((64, 40000, 70), (20, 33000, 33), (100, 40000, 128), (40000, 60, 64), (40000, 100, 131), (2304, 1950, 128),
+                                   (2304, 1950, 129), (3000, 2816, 40))):
+        say(dtype, a_major, aligned, M, N, K)
+        at = (None, 0) if aligned else (1, 3)
+        check(Gradient(M, N, K, dtype, a_major, *at, seed=i))
+        Gradient(M, N, K, dtype, a_major, *at, "int", seed=i).run(accumulate=True)
